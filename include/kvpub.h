@@ -239,6 +239,207 @@ KVPUB_API kvpub_status kvpub_gather(kvpub_ctx *ctx, uint32_t replica, uint32_t l
                                     void *rope_out, int64_t rope_row_stride, void *indexer_out,
                                     int64_t indexer_row_stride, kvpub_stream_t stream);
 
+/* ---- Attention over the published cache ------------------------------------
+ *
+ * The rows of one replica's layer are the keys and the values of latent
+ * attention in its absorbed form: for the row at position p of a sequence,
+ *   c_p[k] = value(code_k) * scale_(k/128), k < 512, and r_p = its 64 RoPE values,
+ * and for query token t and head h
+ *   s(t,h,p) = scale * (q_latent[t,h] . c_p + q_rope[t,h] . r_p),
+ *   lse[t,h] = ln sum_p exp(s(t,h,p)),  out[t,h] = sum_p exp(s(t,h,p) - lse[t,h]) c_p
+ * over the positions that t sees; every head shares the position's one vector.
+ * A query that sees nothing gives out = 0 and lse = -inf.  What a query does
+ * not see has no effect on it, whatever its bytes hold (NaN codes, infinite
+ * scales); a NaN or an infinity in a row that it does see leaves its output
+ * row unspecified, NaN as a rule.  Scores, maxima, sums and outputs are held in binary32; the
+ * weights are rounded to bf16 (times the row's tile scale) for the product
+ * with the codes, and out once at the end.  Results do not depend on timing:
+ * the same call on the same GPU gives the same bits.
+ *
+ * All pointers below are device pointers; descriptors are host structures that
+ * are read during the call only.  No call here allocates or synchronizes: all
+ * are safe under stream capture.  A context poisoned by a fence timeout still
+ * attends (reading publishes nothing) but does not evict. */
+
+/* Query tokens, bf16.  Element (t, h, k) is at t*token_stride + h*head_stride + k.
+ * Pointers 16-byte aligned, strides multiples of 8 elements, at most 2^31 - 1;
+ * head strides at least the row width (any value if num_heads is 1). */
+typedef struct {
+    const void *q_latent;             /* [T, H, 512] */
+    const void *q_rope;               /* [T, H, 64] */
+    int64_t q_latent_token_stride;
+    int64_t q_latent_head_stride;
+    int64_t q_rope_token_stride;
+    int64_t q_rope_head_stride;
+    int64_t num_tokens;               /* T, 0..2^24 */
+    uint32_t num_heads;               /* H, 1..128 */
+    float scale;                      /* finite; the softmax scale (not implied by any dimension) */
+} kvpub_queries;
+
+/* The cached positions of num_seqs sequences.  Position p of sequence b is row
+ * p % 64 of page page_table[b*page_table_stride + p/64].  Sequence b's query
+ * tokens are q_start[b] .. q_start[b+1]-1 (n of them); they are the newest
+ * positions of the sequence, stored before the call: token i of n is position
+ * kv_len[b] - n + i.
+ *   tree_mask == NULL: token i sees positions 0 .. kv_len[b] - n + i.
+ *   otherwise the n tokens are nodes of a drafted tree: token i sees every
+ *   position below kv_len[b] - n, and of the drafted ones those node j with bit
+ *   j % 64 of tree_mask[t*tree_words + j/64] set, t = q_start[b] + i (nodes
+ *   beyond 64*tree_words are not seen).  A node sees itself only if its bit says so.
+ * If kv_len[b] < n the first positions are negative and not there.
+ * kv_len values are taken as at least 0 and at most max_kv_len; tokens
+ * beyond the first max_q_len of a sequence, and tokens that belong to no
+ * sequence, keep their output as it was.  A page number outside the context's
+ * pages hides its 64 positions and is counted once a call
+ * (kvpub_error_read's invalid count). */
+typedef struct {
+    const int32_t *kv_len;            /* [num_seqs] */
+    const int32_t *q_start;           /* [num_seqs + 1], ascending; NULL: one token a sequence */
+    const int32_t *page_table;        /* [num_seqs, >= ceil(max_kv_len / 64)] */
+    int64_t page_table_stride;        /* elements, >= ceil(max_kv_len / 64) */
+    const uint64_t *tree_mask;        /* [T, tree_words] or NULL */
+    uint32_t tree_words;              /* 0 without a tree_mask, else 1..64 */
+    uint32_t num_seqs;                /* 0..65536 */
+    uint32_t max_q_len;               /* >= 1; most query tokens of one sequence */
+    uint32_t max_kv_len;              /* most cached positions of one sequence, at most 2^30 */
+} kvpub_pages;
+
+/* Bytes of workspace that kvpub_attend / kvpub_attend_slots takes for such a
+ * call (0 if the descriptor is not valid).  It depends on num_heads,
+ * num_tokens, num_seqs, max_q_len, max_kv_len (num_slots) alone and grows with
+ * each, so a program sizes it once for its largest call.  The workspace holds
+ * the partial results of one call while that call runs, needs no
+ * initialization and keeps nothing between calls; calls that may run at the
+ * same time (other streams, captured graphs replayed side by side) each need
+ * one of their own. */
+KVPUB_API uint64_t kvpub_attend_workspace(const kvpub_queries *q, const kvpub_pages *pages);
+KVPUB_API uint64_t kvpub_attend_slots_workspace(const kvpub_queries *q, uint32_t num_slots);
+
+/* Latent attention of q over the sequences' cached positions in replica
+ * `replica`, layer `layer`, asynchronously on `stream`.
+ *   out: bf16, element (t,h,k) at t*out_token_stride + h*out_head_stride + k,
+ *        512 values a row; alignment and stride rules as for the queries
+ *   lse: binary32 (t,h) at t*lse_token_stride + h, or NULL; 4-byte aligned
+ *   workspace: 16-byte aligned, workspace_bytes >= kvpub_attend_workspace(q, pages)
+ * T == 0 or num_seqs == 0 launches nothing. */
+KVPUB_API kvpub_status kvpub_attend(kvpub_ctx *ctx, uint32_t replica, uint32_t layer, const kvpub_queries *q,
+                                    const kvpub_pages *pages, void *out, int64_t out_token_stride,
+                                    int64_t out_head_stride, float *lse, int64_t lse_token_stride,
+                                    void *workspace, uint64_t workspace_bytes, kvpub_stream_t stream);
+
+/* kvpub_attend over a list of slots for each token, as a selection gives it:
+ * token t sees the slots slots[t*slots_stride + i], i < num_slots.  -1 is
+ * padding; any other slot outside [0, num_pages*64) is skipped and counted.  A
+ * slot listed twice counts twice.  slots: int64, 8-byte aligned, num_slots
+ * at most 2^24 (0: every out is 0), slots_stride >= num_slots. */
+KVPUB_API kvpub_status kvpub_attend_slots(kvpub_ctx *ctx, uint32_t replica, uint32_t layer, const kvpub_queries *q,
+                                          const int64_t *slots, int64_t slots_stride, uint32_t num_slots, void *out,
+                                          int64_t out_token_stride, int64_t out_head_stride, float *lse,
+                                          int64_t lse_token_stride, void *workspace, uint64_t workspace_bytes,
+                                          kvpub_stream_t stream);
+
+/* The softmax weight that each cached position received from q, summed over
+ * the sequence's tokens and heads, on top of what it had:
+ *   weights_out[b][p] = weights_in[b][p] + sum_{t,h} exp(s(t,h,p) - lse[t,h])
+ * for p < max_kv_len, the sum over the tokens that see p (0 for positions at
+ * or beyond kv_len[b] and on bad pages).  weights_in NULL: zeros; weights_in ==
+ * weights_out adds in place; otherwise the two do not overlap.  lse is what
+ * kvpub_attend gave for the same queries and pages; a row of -inf adds nothing.
+ *   weights: binary32 [num_seqs], row stride weights_stride >= max_kv_len elements
+ * The sums run in one fixed order (no atomics). */
+KVPUB_API kvpub_status kvpub_attend_weights(kvpub_ctx *ctx, uint32_t replica, uint32_t layer, const kvpub_queries *q,
+                                            const kvpub_pages *pages, const float *lse, int64_t lse_token_stride,
+                                            const float *weights_in, float *weights_out, int64_t weights_stride,
+                                            kvpub_stream_t stream);
+
+/* One eviction: sequence b, of len = kv_len[b] positions (taken as 0 ..
+ * max_kv_len), keeps min(len, budget) of them.  If len > budget those are the
+ * first `first`, the last `last`, and of the rest the budget - first - last of
+ * the largest accumulated weight; equal weights keep the lower position, a NaN
+ * counts below every number.  In ascending order they become positions 0, 1, ..
+ * of the destination table: the Main-KV row (656 bytes) and the Indexer-K row
+ * (128 codes and their scale) of layer `layer` are read once, from replica 0,
+ * and written to every replica.  The destination is the source table itself (in
+ * place: dst_table == page_table with equal strides, and no page twice in it)
+ * or pages that no source sequence of the call uses (a shared prefix stays
+ * whole).
+ *   kept[b][i]        = position that moved to i, -1 for new_len <= i < budget
+ *   new_len[b]        = min(len, budget)
+ *   weights_out[b][i] = weights_in[b][kept[b][i]] for i < new_len, 0 up to max_kv_len
+ * weights_out may be weights_in itself, otherwise the two do not overlap.
+ * A kept position whose source or destination page is outside the context's
+ * pages is not copied, and counted.  The rows behind new_len keep their bytes. */
+typedef struct {
+    const float *weights_in;          /* [num_seqs], row stride weights_stride >= max_kv_len */
+    float *weights_out;               /* the same shape and stride */
+    int64_t weights_stride;
+    const int32_t *kv_len;            /* [num_seqs] */
+    const int32_t *page_table;        /* as in kvpub_pages */
+    int64_t page_table_stride;
+    const int32_t *dst_table;         /* [num_seqs, >= ceil(min(budget, max_kv_len) / 64)] */
+    int64_t dst_table_stride;
+    int32_t *kept;                    /* [num_seqs, budget], row stride kept_stride >= budget */
+    int64_t kept_stride;
+    int32_t *new_len;                 /* [num_seqs] */
+    uint32_t num_seqs;                /* 0..65536 */
+    uint32_t max_kv_len;              /* 1..2^30 */
+    uint32_t budget;                  /* 1..2^30 */
+    uint32_t first;                   /* first + last <= budget */
+    uint32_t last;
+    uint32_t reserved;                /* must be 0 */
+} kvpub_evict_io;
+
+/* Bytes of workspace of an eviction; rules as for kvpub_attend_workspace. */
+KVPUB_API uint64_t kvpub_evict_workspace(const kvpub_evict_io *io);
+
+/* Evict asynchronously on `stream`.  weights, tables, kept and lengths are
+ * 4-byte aligned, the workspace 16-byte.  A poisoned context changes nothing. */
+KVPUB_API kvpub_status kvpub_evict(kvpub_ctx *ctx, uint32_t layer, const kvpub_evict_io *io, void *workspace,
+                                   uint64_t workspace_bytes, kvpub_stream_t stream);
+
+/* Latent attention in its expanded form, for prefill: the latent vectors of the
+ * keys (kvpub_gather) have been projected up to a key part and a value for each
+ * head, and the 64 RoPE values stay shared:
+ *   s(t,h,u) = scale * (q_nope[t,h] . k_nope[u,h] + q_rope[t,h] . k_rope[u]),
+ *   out[t,h] = sum_u softmax_u(s(t,h,u)) v[u,h]
+ * Sequence b's tokens are q_start[b] .. q_start[b+1]-1 (n) and its keys
+ * k_start[b] .. k_start[b+1]-1 (m).  causal: token i sees keys 0 .. m - n + i,
+ * else all m.  No key seen: out 0, lse -inf.  All bf16, accumulated in
+ * binary32; the weights are rounded to bf16 for the product with v.  Keys and
+ * values that a token does not see have no effect on it; one that is not finite
+ * leaves the rows that see it unspecified.  16-byte
+ * aligned, strides multiples of 8 elements and at most 2^31 - 1, as for
+ * kvpub_queries.  Values and key parts may be interleaved (strides of 256 a head).
+ * The context gives the device only. */
+typedef struct {
+    const void *q_nope;               /* [T, H, 128] */
+    const void *q_rope;               /* [T, H, 64] */
+    const void *k_nope;               /* [U, H, 128] */
+    const void *k_rope;               /* [U, 64] */
+    const void *v;                    /* [U, H, 128] */
+    void *out;                        /* [T, H, 128] */
+    float *lse;                       /* [T, H] at t*lse_token_stride + h, or NULL */
+    int64_t q_nope_token_stride, q_nope_head_stride;
+    int64_t q_rope_token_stride, q_rope_head_stride;
+    int64_t k_nope_token_stride, k_nope_head_stride;
+    int64_t k_rope_token_stride;
+    int64_t v_token_stride, v_head_stride;
+    int64_t out_token_stride, out_head_stride;
+    int64_t lse_token_stride;
+    const int32_t *q_start;           /* [num_seqs + 1], ascending */
+    const int32_t *k_start;           /* [num_seqs + 1], ascending */
+    int64_t num_tokens;               /* T, 0..2^24 */
+    int64_t num_keys;                 /* U, 0..2^24 */
+    uint32_t num_seqs;                /* 0..65535 */
+    uint32_t num_heads;               /* 1..128 */
+    uint32_t max_q_len;               /* >= 1; tokens beyond the first max_q_len of a sequence keep their output */
+    uint32_t causal;                  /* 0 or 1 */
+    float scale;
+    uint32_t reserved;                /* must be 0 */
+} kvpub_expanded_io;
+
+KVPUB_API kvpub_status kvpub_attend_expanded(kvpub_ctx *ctx, const kvpub_expanded_io *io, kvpub_stream_t stream);
+
 /* Replica storage at stable virtual addresses, on cfg->device (vLLM PR
  * #52863, Relationship to existing work: the replicated cache builds on a
  * cache kept at a stable virtual address so that it can grow in place).

@@ -10,7 +10,9 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libkvpub.so")
-SOURCES = ["kvpub_api.hip", "store_kernel.hip", "fence_kernel.hip", "gather_kernel.hip", "vmm.hip"]
+SOURCES = ["kvpub_api.hip", "store_kernel.hip", "fence_kernel.hip", "gather_kernel.hip", "attend_kernel.hip",
+           "evict_kernel.hip", "expanded_kernel.hip",
+           "vmm.hip"]
 FLOOR_LIB = os.path.join(PKG, "libkvpub_floor.so")
 FLOOR_SOURCES = ["floor_kernel.hip"]
 ARCH = "gfx950"

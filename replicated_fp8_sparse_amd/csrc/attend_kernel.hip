@@ -1,0 +1,860 @@
+// Latent attention over the published cache for gfx950: the reader that the
+// store writes for.  vLLM PR #52863 "[Kernel][PCP] Publish replicated KV updates
+// through PyTorch symmetric memory", Summary and Design: attention reads the
+// local replica in the layout the store writes; a row is key and value of all heads.
+//
+// Mathematics.  With codes k_j (tile j of 128) and tile scales a_j of a row,
+//   score = scale * (sum_j a_j (q_j . k_j) + q_r . r),   out_j = sum_p (w_p a_pj) k_pj / sum_p w_p,
+// so the codes enter the matrix instructions as they are and each tile's scale
+// multiplies an accumulator (scores) or the weight (values): no row is rounded
+// to bf16.  A code is exact in bf16, and so is its product with a bf16 query in
+// the accumulator.  (The scaled e4m3 instruction would take the codes as they
+// are and each query as the sum of two e4m3 numbers at the same rate; its sums
+// were found off by 2^-16 of the largest product, too much for lse.)  The
+// weights are rounded to bf16 for the second product.
+//
+// Mapping.  A block of 8 waves takes a unit (sequence, M rows = (token, head)
+// pairs) over a run of 64-row tiles (a page), a tile being one copy of 41984
+// contiguous bytes into LDS.  A row's stride of 656 bytes (164 banks, 36 modulo
+// 64) puts 16 rows on distinct banks, so the page's own layout is read free of
+// conflicts.  Scores come out transposed (keys down, query rows across): a lane
+// holds 4 keys of one query row, row maxima and sums need two shuffles, and the
+// weights are already laid out as an operand of the second product if its key
+// order follows; ds_read_b64_tr_b8 picks the values' columns in that order.
+// One pass: running maximum and sum, the accumulator rescaled only when the
+// maximum grew by more than 2^8.
+//
+// Work split.  All units' tiles form one line that the blocks cut into equal
+// runs, whatever the lengths of the sequences; a unit cut between blocks leaves
+// partial results that combine_kernel joins in block order.
+#include "kvpub_internal.h"
+
+namespace kvpub {
+namespace {
+
+typedef int i32x2 __attribute__((ext_vector_type(2)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+template <class T> using lptr = __attribute__((address_space(3))) T*;
+
+constexpr int kRow = 656;
+constexpr int kTileBytes = 64 * kRow;            // 41984 = 41 copies of 1024 bytes
+constexpr int kRing = 3;
+constexpr int kWaves = 8;                        // two a SIMD: 256 registers each
+constexpr int kThreads = kWaves * 64;
+constexpr float kLn2 = 0.693147180559945309f;
+constexpr float kLazy = 8.0f;                    // rescale when a maximum grows past 2^8
+
+// LDS: the tile ring (after the last tile the waves' exchange area), each
+// wave's copies of slot lists (4 tiles deep).
+constexpr int kSlotRing = 4;
+struct Shared {
+    alignas(16) uint8_t ring[131072];
+    alignas(16) int64_t slots[kWaves][kSlotRing][64];
+    float stat[2][kWaves / 2][64];
+    uint64_t scan[kWaves];
+    uint64_t found[2];
+};
+static_assert(sizeof(Shared) <= 163840, "160 KB of LDS");
+
+__device__ __forceinline__ uint32_t lds_offset(const void* p) {
+    return (uint32_t)(uintptr_t)(lptr<const uint8_t>)(const uint8_t*)p;
+}
+
+// 64 lanes x 16 bytes from each lane's address to 1024 consecutive LDS bytes.
+// Written as asm because the compiler otherwise waits for every outstanding copy
+// before any LDS read; wait_tile() below counts them instead.
+__device__ __forceinline__ void copy16_to_lds(const uint8_t* src, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(src) : "memory");
+}
+__device__ __forceinline__ void copy4_to_lds(const uint8_t* src, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(lds), "v"(src) : "memory");
+}
+
+// Every wave's own copies of all but the newest tile have landed, then all waves'.
+__device__ __forceinline__ void wait_tile(uint32_t wave, bool newer) {
+    if (!newer) asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    else if (wave == 0) asm volatile("s_waitcnt vmcnt(6) lgkmcnt(0)" ::: "memory");
+    else asm volatile("s_waitcnt vmcnt(5) lgkmcnt(0)" ::: "memory");
+    asm volatile("s_barrier" ::: "memory");
+}
+__device__ __forceinline__ void barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// One 16-row group of queries as operands: lane (l%16, l/16) = (row, 16 values of
+// each 64: the first 8 go with one matrix instruction, the others with the next).
+struct QFrag {
+    bf16x8 lat[16];
+    bf16x8 rope[2];
+};
+
+__device__ __forceinline__ void load_query(QFrag& f, const uint16_t* lat, const uint16_t* rope, uint32_t g) {
+#pragma unroll
+    for (int c = 0; c < 16; ++c) f.lat[c] = *(const bf16x8*)(lat + (c >> 1) * 64 + g * 16 + (c & 1) * 8);
+#pragma unroll
+    for (int c = 0; c < 2; ++c) f.rope[c] = *(const bf16x8*)(rope + c * 32 + g * 8);
+}
+
+// 8 codes as bf16 (exact).
+__device__ __forceinline__ bf16x8 widen(int c0, int c1) {
+    const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c0, 1.0f, false);
+    const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c0, 1.0f, true);
+    const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c1, 1.0f, false);
+    const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c1, 1.0f, true);
+    return bf16x8{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
+}
+
+__device__ __forceinline__ float tile_scale(const uint8_t* rows, uint32_t key, int j) {
+    return *(const float*)(rows + key * kRow + 512 + j * 4);
+}
+
+// Raw scores of 16 keys x 16 query rows (lane: query row l%16, keys 4*(l/16) + i).
+// rows: the 16 keys' LDS rows.
+template <int R16>
+__device__ __forceinline__ void scores16(f32x4* s, const uint8_t* rows, const QFrag* q, uint32_t l16, uint32_t g) {
+    const uint8_t* mine = rows + l16 * kRow;
+    const bf16x8 r0 = *(const bf16x8*)(mine + 528 + g * 16);
+    const bf16x8 r1 = *(const bf16x8*)(mine + 592 + g * 16);
+#pragma unroll
+    for (int r = 0; r < R16; ++r) {
+        const f32x4 z = {0.f, 0.f, 0.f, 0.f};
+        s[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(r0, q[r].rope[0], z, 0, 0, 0);
+        s[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(r1, q[r].rope[1], s[r], 0, 0, 0);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        __builtin_amdgcn_sched_barrier(0);
+        float a[4];                              // this lane's keys' scales
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a[i] = tile_scale(rows, 4 * g + i, j);
+        bf16x8 k[4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const i32x4 v = *(const i32x4*)(mine + j * 128 + h * 64 + g * 16);
+            k[h * 2] = widen(v[0], v[1]);
+            k[h * 2 + 1] = widen(v[2], v[3]);
+        }
+#pragma unroll
+        for (int r = 0; r < R16; ++r) {
+            f32x4 c = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int h = 0; h < 4; ++h) c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k[h], q[r].lat[j * 4 + h], c, 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[r][i] = fmaf(c[i], a[i], s[r][i]);
+        }
+    }
+}
+
+// ---- the line of work ---------------------------------------------------------
+
+// What one sequence (or one token's slot list) asks for.
+struct Seq {
+    uint32_t q0;         // first token
+    uint32_t n;          // tokens
+    uint32_t kv;         // positions
+    uint32_t units;      // row groups of M
+    uint32_t tiles;      // 64-row tiles of each, at least 1
+};
+
+template <bool Slots>
+__device__ __forceinline__ Seq sequence(const AttendParams& p, uint32_t b, uint32_t M, bool empty) {
+    Seq s;
+    if (Slots) {
+        s.q0 = b;
+        s.n = 1;
+        s.kv = empty ? 0u : p.num_slots;
+    } else {
+        const int32_t kv = p.kv_len[b];
+        int64_t q0 = b, q1 = (int64_t)b + 1;
+        if (p.q_start) { q0 = p.q_start[b]; q1 = p.q_start[b + 1]; }
+        q0 = q0 < 0 ? 0 : q0;
+        q1 = q1 > (int64_t)p.num_tokens ? (int64_t)p.num_tokens : q1;
+        const int64_t n = q1 > q0 ? q1 - q0 : 0;
+        s.q0 = (uint32_t)q0;
+        s.n = (uint32_t)n;
+        s.kv = kv < 0 || empty ? 0u : ((uint32_t)kv > p.max_kv ? p.max_kv : (uint32_t)kv);
+    }
+    const uint32_t m = s.n > p.max_q ? p.max_q : s.n;     // tokens beyond max_q_len are not computed
+    s.units = (m * p.heads + M - 1) / M;
+    s.tiles = s.kv ? (s.kv + 63) / 64 : 1u;
+    return s;
+}
+
+// Prefix sums of the sequences' work by the block's threads: returns the
+// total; if `at` lies within, found[0..1] = (sequence, offset in it).  `line`
+// (may be null) receives the prefix of every sequence and the total.
+template <bool Slots>
+__device__ uint64_t walk(const AttendParams& p, uint32_t M, bool empty, uint64_t at, uint64_t* line, Shared& sh) {
+    const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = tid >> 6;
+    uint64_t carry = 0;
+    for (uint32_t b0 = 0; b0 < p.num_seqs; b0 += kThreads) {
+        const uint32_t b = b0 + tid;
+        uint64_t w = 0;
+        if (b < p.num_seqs) {
+            const Seq s = sequence<Slots>(p, b, M, empty);
+            w = (uint64_t)s.units * s.tiles;
+        }
+        uint64_t x = w;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const uint64_t y = __shfl_up(x, d);
+            if (lane >= (uint32_t)d) x += y;
+        }
+        __syncthreads();
+        if (lane == 63) sh.scan[wave] = x;
+        __syncthreads();
+        uint64_t before = carry, total = carry;
+        for (uint32_t v = 0; v < kWaves; ++v) {
+            if (v < wave) before += sh.scan[v];
+            total += sh.scan[v];
+        }
+        const uint64_t first = before + x - w;
+        if (b < p.num_seqs && line) line[b] = first;
+        if (w && at >= first && at < first + w) { sh.found[0] = b; sh.found[1] = at - first; }
+        carry = total;
+    }
+    __syncthreads();
+    return carry;
+}
+
+// Tiles a block takes: an equal share, at least 2 (a shorter run costs more in
+// partial results than it gains).
+__device__ __forceinline__ uint64_t share(uint64_t total, uint32_t blocks) {
+    const uint64_t c = (total + blocks - 1) / blocks;
+    return c < 2 ? 2 : c;
+}
+
+// ---- tiles -----------------------------------------------------------------------
+
+// Where a unit's tiles come from, and which keys of a tile exist.
+template <bool Slots>
+struct Source {
+    const AttendParams& p;
+    const int32_t* table;      // this sequence's pages
+    const int64_t* list;       // this token's slots
+    uint32_t kv;
+    int64_t capacity;
+    Shared& sh;
+    uint32_t wave, lane;
+
+    __device__ __forceinline__ int64_t page(uint32_t t) const {   // -1: no such page
+        const int64_t g = table[t];
+        return g >= 0 && g < capacity / 64 ? g : -1;
+    }
+    // Slots of tile t into this wave's copy (clamped to the list: always in bounds).
+    __device__ __forceinline__ void fetch_slots(uint32_t t) const {
+        const uint32_t last = 2u * kv - 1u;
+        uint32_t i = t * 128u + lane;
+        const uint32_t at = lds_offset(&sh.slots[wave][t % kSlotRing][0]);
+        copy4_to_lds((const uint8_t*)list + 4ull * (i < last ? i : last), at);
+        i += 64;
+        copy4_to_lds((const uint8_t*)list + 4ull * (i < last ? i : last), at + 256);
+    }
+    __device__ __forceinline__ bool good(int64_t s) const { return (uint64_t)s < (uint64_t)capacity; }
+    __device__ __forceinline__ uint64_t row_of(int64_t s) const {
+        const uint64_t v = good(s) ? (uint64_t)s : 0u;
+        return (v >> 6) * p.main_page_stride + (v & 63u) * (uint64_t)kRow;
+    }
+    // This wave's share of tile t into ring buffer `buf`: chunks wave, wave + 8, ...
+    __device__ __forceinline__ void fetch(uint32_t t, int64_t pg, uint32_t buf) const {
+        if (Slots) {
+            const int64_t* my = &sh.slots[wave][t % kSlotRing][0];
+#pragma unroll
+            for (int i = 0; i < 6; ++i) {
+                const uint32_t c = wave + kWaves * i;
+                if (i == 5 && wave != 0) break;
+                const uint32_t x = c * 64u + lane, r = x / 41u, o = (x - r * 41u) * 16u;
+                copy16_to_lds(p.main_base + row_of(my[r]) + o, buf + c * 1024u);
+            }
+        } else {
+            const uint8_t* base = p.main_base + (uint64_t)(pg < 0 ? 0 : pg) * p.main_page_stride + lane * 16u;
+#pragma unroll
+            for (int i = 0; i < 6; ++i) {
+                const uint32_t c = wave + kWaves * i;
+                if (i == 5 && wave != 0) break;
+                copy16_to_lds(base + c * 1024u, buf + c * 1024u);
+            }
+        }
+    }
+};
+
+// A tile that some query row does not see whole: rows that exist for none
+// (bit clear in `live`) become zeros, and so do the codes of rows that hold a NaN
+// code or an infinite or NaN scale, with a NaN among their RoPE values for whoever
+// sees them; the others are not touched by it.  All threads; ends in a barrier.
+__device__ __forceinline__ void clean_tile(uint8_t* tile, uint64_t live) {
+    const uint32_t key = threadIdx.x >> 3, j = threadIdx.x & 7u;     // 64 codes a thread
+    uint8_t* row = tile + key * kRow;
+    const bool gone = !((live >> key) & 1u);
+    bool nan = false;
+    if (!gone) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const i32x4 v = *(const i32x4*)(row + j * 64 + c * 16);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) nan |= ((((uint32_t)v[i] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0;
+        }
+        if (j < 4) nan |= (*(const uint32_t*)(row + 512 + j * 4) & 0x7F800000u) == 0x7F800000u;
+    }
+    const uint64_t who = __ballot(nan);
+    const bool bad = ((who >> ((threadIdx.x & 63u) & ~7u)) & 255u) != 0;
+    if (gone || bad) {
+        const i32x4 z = {0, 0, 0, 0};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) *(i32x4*)(row + j * 64 + c * 16) = z;
+        if (j < 4) *(float*)(row + 512 + j * 4) = 0.f;
+    }
+    if (bad && j == 0) *(uint16_t*)(row + 528) = 0x7FC0;
+    barrier();
+}
+
+// Sees of one query row: positions below `lim`, or drafted nodes by their bits.
+struct Sees {
+    uint32_t lim;              // positions below lim are seen
+    const uint64_t* tree;      // bits of the drafted positions from `base` on, or null
+    int64_t base;
+    uint32_t kv, words;
+    __device__ __forceinline__ bool operator()(uint32_t pos) const {
+        if (pos < lim) return true;
+        if (!tree || pos >= kv) return false;
+        const uint64_t j = (uint64_t)((int64_t)pos - base);
+        return j < 64ull * words && ((tree[j >> 6] >> (j & 63u)) & 1u);
+    }
+};
+
+// Sees of token i (of n) of a sequence of kv positions.
+template <bool Slots>
+__device__ __forceinline__ Sees sees(const AttendParams& p, const Seq& s, uint32_t i) {
+    Sees v;
+    v.tree = nullptr;
+    v.base = (int64_t)s.kv - s.n;
+    v.kv = s.kv;
+    v.words = p.tree_words;
+    int64_t lim = Slots ? (int64_t)s.kv : v.base + i + 1;
+    if (!Slots && p.tree) {
+        lim = v.base;
+        v.tree = p.tree + (uint64_t)(s.q0 + i) * p.tree_words;
+    }
+    v.lim = lim < 0 ? 0u : (uint32_t)lim;
+    return v;
+}
+
+// ---- attention ---------------------------------------------------------------------
+
+// R16: 16-row groups of a wave; RW waves split the rows, KW the keys of a tile,
+// DW the value columns (those waves form the same scores).
+template <int R16, int RW, int KW, int DW, bool Slots>
+__global__ __launch_bounds__(kThreads) void attend_kernel(const AttendParams p) {
+    static_assert(RW * KW * DW == kWaves, "every wave has its part");
+    constexpr int M = 16 * R16 * RW;
+    constexpr int NB = 32 / DW;                     // 16-column blocks of a wave
+    __shared__ Shared sh;
+    const uint32_t lane = threadIdx.x & 63u, l16 = lane & 15u, g = lane >> 4;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t rw = wave % RW, kw = (wave / RW) % KW, dw = wave / (RW * KW);
+    const int64_t capacity = p.head->capacity;
+    const bool empty = capacity <= 0;
+
+    uint64_t total;
+    if (Slots) {
+        const Seq s = sequence<true>(p, 0, M, empty);
+        total = (uint64_t)p.num_seqs * s.units * s.tiles;
+    } else {
+        total = walk<false>(p, M, empty, ~0ull, blockIdx.x == 0 ? p.line : nullptr, sh);
+    }
+    const uint64_t each = share(total, gridDim.x);
+    if (blockIdx.x == 0 && threadIdx.x == 0) p.line[p.num_seqs] = each;
+    uint64_t pos = each * blockIdx.x;
+    const uint64_t end = pos + each < total ? pos + each : total;
+    if (pos >= end) return;
+    const uint64_t begin = pos;
+    uint32_t b;
+    uint64_t off;
+    if (Slots) {
+        const Seq s = sequence<true>(p, 0, M, empty);
+        const uint64_t w = (uint64_t)s.units * s.tiles;
+        b = (uint32_t)(pos / w);
+        off = pos - b * w;
+    } else {
+        walk<false>(p, M, empty, pos, nullptr, sh);
+        b = __builtin_amdgcn_readfirstlane((uint32_t)sh.found[0]);
+        off = __builtin_amdgcn_readfirstlane((uint32_t)sh.found[1]) |
+              ((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(sh.found[1] >> 32)) << 32);
+    }
+
+    while (pos < end) {
+        const Seq s = sequence<Slots>(p, b, M, empty);
+        const uint64_t work = (uint64_t)s.units * s.tiles;
+        if (off >= work) { ++b; off = 0; continue; }     // pos < end <= total: a later sequence has work
+        const uint32_t unit = (uint32_t)(off / s.tiles);
+        uint32_t t0 = (uint32_t)(off - (uint64_t)unit * s.tiles);
+        const uint32_t t1 = (uint64_t)(s.tiles - t0) < end - pos ? s.tiles : t0 + (uint32_t)(end - pos);
+        const bool whole = t0 == 0 && t1 == s.tiles;
+        const uint32_t slot = 2u * blockIdx.x + (pos == begin ? 0u : 1u);
+        pos += t1 - t0;
+        off += t1 - t0;
+
+        // this wave's query rows
+        const uint32_t m = s.n > p.max_q ? p.max_q : s.n;
+        const uint32_t rows = m * p.heads, row0 = unit * M;
+        QFrag q[R16];
+        uint32_t token[R16];
+#pragma unroll
+        for (int r = 0; r < R16; ++r) {
+            // rows behind the last one repeat it and are not written
+            const uint32_t at = row0 + (rw * R16 + r) * 16u + l16, row = at < rows ? at : rows - 1;
+            const uint32_t i = row / p.heads, h = row - i * p.heads;
+            const uint64_t t = (uint64_t)s.q0 + i;
+            load_query(q[r], p.q_latent + t * p.q_latent_token + h * p.q_latent_head,
+                       p.q_rope + t * p.q_rope_token + h * p.q_rope_head, g);
+            token[r] = i;
+        }
+        // positions below `clear` are seen by every row of the unit
+        const Sees lowest = sees<Slots>(p, s, row0 / p.heads);
+        const uint32_t clear = lowest.lim;
+        // and none of its rows sees a tile from `t_end` on
+        uint32_t t_end = s.kv ? t1 : t0;
+        if (!Slots && !p.tree) {
+            const uint32_t last_row = (row0 + M < rows ? row0 + M : rows) - 1;
+            const Sees highest = sees<Slots>(p, s, last_row / p.heads);
+            const uint32_t tl = (highest.lim + 63) / 64;
+            t_end = t_end < tl ? t_end : tl;
+        }
+
+        __builtin_amdgcn_sched_barrier(0);
+        f32x4 o[R16][NB];
+        float mx[R16], sum[R16];
+#pragma unroll
+        for (int r = 0; r < R16; ++r) {
+            mx[r] = -INFINITY;
+            sum[r] = 0.f;
+#pragma unroll
+            for (int d = 0; d < NB; ++d) o[r][d] = f32x4{0.f, 0.f, 0.f, 0.f};
+        }
+
+        const Source<Slots> src{p, Slots ? nullptr : p.pages + (uint64_t)b * p.pages_stride,
+                                Slots ? p.slots + (uint64_t)b * p.slots_stride : nullptr, s.kv, capacity, sh, wave, lane};
+        const uint32_t ring = lds_offset(sh.ring);
+        int64_t pg[3] = {-1, -1, -1};                    // pages of tiles t, t + 1, t + 2
+        if (t0 < t_end) {
+            if (Slots) {
+                for (uint32_t t = t0; t < t0 + 3; ++t)
+                    if (t < t_end) src.fetch_slots(t);
+                asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            } else {
+                pg[0] = src.page(t0);
+                if (t0 + 1 < t_end) pg[1] = src.page(t0 + 1);
+                if (t0 + 2 < t_end) pg[2] = src.page(t0 + 2);
+            }
+            src.fetch(t0, pg[0], ring + (t0 % kRing) * kTileBytes);
+            if (t0 + 1 < t_end) src.fetch(t0 + 1, pg[1], ring + ((t0 + 1) % kRing) * kTileBytes);
+        }
+        for (uint32_t t = t0; t < t_end; ++t) {
+            wait_tile(wave, t + 1 < t_end);
+            if (Slots && t + 3 < t_end) src.fetch_slots(t + 3);
+            if (t + 2 < t_end) src.fetch(t + 2, pg[2], ring + ((t + 2) % kRing) * kTileBytes);
+            const int64_t page = pg[0];
+            pg[0] = pg[1];
+            pg[1] = pg[2];
+            if (!Slots) pg[2] = t + 3 < t_end ? src.page(t + 3) : -1;
+            uint8_t* tile = sh.ring + (t % kRing) * kTileBytes;
+
+            uint64_t live = ~0ull;
+            bool masked;
+            if (Slots) {
+                const uint32_t left = s.kv - t * 64u;
+                const int64_t v = sh.slots[wave][t % kSlotRing][lane];
+                const bool in = lane < left;
+                live = __ballot(in && src.good(v));
+                const uint64_t wrong = __ballot(in && v != -1 && !src.good(v));
+                if (wrong && unit == 0 && threadIdx.x == 0) atomicAdd(p.invalid_count, (unsigned long long)__popcll(wrong));
+                masked = live != ~0ull;
+            } else {
+                if (page < 0) {
+                    if (unit == 0 && threadIdx.x == 0) atomicAdd(p.invalid_count, 1ull);
+                    continue;
+                }
+                const uint32_t left = s.kv - t * 64u;
+                if (left < 64) live = (1ull << left) - 1;
+                masked = t * 64u + 64u > clear;
+            }
+            if (masked) clean_tile(tile, live);
+
+#pragma unroll 1
+            for (int half = 0; half < 2 / KW; ++half) {
+                const uint32_t k0 = (KW == 2 ? kw : (uint32_t)half) * 32u;
+                const uint8_t* rows32 = tile + k0 * kRow;
+                f32x4 x[2][R16];
+#pragma unroll
+                for (int u = 0; u < 2; ++u) scores16<R16>(x[u], rows32 + u * 16 * kRow, q, l16, g);
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int r = 0; r < R16; ++r) x[u][r] *= p.scale_log2;
+                if (masked) {
+#pragma unroll
+                    for (int r = 0; r < R16; ++r) {
+                        uint32_t on = 0;                 // bit 4 u + i
+                        const Sees see = sees<Slots>(p, s, token[r]);
+#pragma unroll 1
+                        for (uint32_t c = 0; c < 8; ++c) {
+                            const uint32_t key = k0 + (c >> 2) * 16 + 4 * g + (c & 3u);
+                            const bool here = ((live >> key) & 1u) && (Slots || see(t * 64u + key));
+                            on |= here ? 1u << c : 0u;
+                        }
+#pragma unroll
+                        for (int u = 0; u < 2; ++u)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                x[u][r][i] = (on >> (u * 4 + i)) & 1u ? x[u][r][i] : -INFINITY;
+                    }
+                }
+#pragma unroll
+                for (int r = 0; r < R16; ++r) {
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            top = fmaxf(top, x[u][r][i]);
+                        }
+                    top = fmaxf(top, __shfl_xor(top, 16));
+                    top = fmaxf(top, __shfl_xor(top, 32));
+                    if (__any(top > mx[r] + kLazy || (mx[r] == -INFINITY && top > mx[r]))) {
+                        const float next = fmaxf(mx[r], top);
+                        const float keep = mx[r] == -INFINITY ? 0.f : exp2f(mx[r] - next);
+                        mx[r] = next;
+                        sum[r] *= keep;
+#pragma unroll
+                        for (int d = 0; d < NB; ++d) o[r][d] *= keep;
+                    }
+                    const float ref = mx[r] == -INFINITY ? 0.f : mx[r];
+                    float e[2][4];
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            e[u][i] = __builtin_amdgcn_exp2f(x[u][r][i] - ref);
+                            sum[r] += e[u][i];
+                        }
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) x[u][r][i] = e[u][i];
+                }
+                // values: 8 keys of this lane group (4 of each 16) x 16 columns
+                const uint32_t vk = (l16 >> 1) < 4 ? 4 * g + (l16 >> 1) : 12 + 4 * g + (l16 >> 1);
+                const uint8_t* vrow = rows32 + vk * kRow + (l16 & 1u) * 8u;
+#pragma unroll
+                for (int j = 0; j < NB / 8 || j == 0; ++j) {
+                    __builtin_amdgcn_sched_barrier(0);
+                    const int tj = NB >= 8 ? (int)dw * (NB / 8) + j : (int)(dw * NB / 8);    // the scale's tile
+                    bf16x8 w[R16];
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float a = tile_scale(rows32, u * 16 + 4 * g + i, tj);
+#pragma unroll
+                            for (int r = 0; r < R16; ++r) w[r][u * 4 + i] = (__bf16)(x[u][r][i] * a);
+                        }
+#pragma unroll
+                    for (int d = 0; d < (NB < 8 ? NB : 8); ++d) {
+                        if (d % 4 == 0) __builtin_amdgcn_sched_barrier(0);
+                        const uint32_t col = (dw * NB + j * 8 + d) * 16u;
+                        const i32x2 c = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lptr<i32x2>)(vrow + col));
+                        const bf16x8 v = widen(c.x, c.y);
+#pragma unroll
+                        for (int r = 0; r < R16; ++r)
+                            o[r][j * 8 + d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, w[r], o[r][j * 8 + d], 0, 0, 0);
+                    }
+                }
+            }
+        }
+        barrier();    // the ring is free
+
+        // join the key halves, then write
+#pragma unroll
+        for (int r = 0; r < R16; ++r) {
+            sum[r] += __shfl_xor(sum[r], 16);
+            sum[r] += __shfl_xor(sum[r], 32);
+            if (KW == 2) {
+                f32x4* ex = (f32x4*)sh.ring + (uint32_t)((dw * RW + rw) * R16 + r) * (NB * 64) + lane;
+                if (kw == 1) {
+#pragma unroll
+                    for (int d = 0; d < NB; ++d) ex[d * 64] = o[r][d];
+                    sh.stat[0][(dw * RW + rw) * R16 + r][lane] = mx[r];
+                    sh.stat[1][(dw * RW + rw) * R16 + r][lane] = sum[r];
+                }
+                barrier();
+                if (kw == 0) {
+                    const float m2 = sh.stat[0][(dw * RW + rw) * R16 + r][lane], s2 = sh.stat[1][(dw * RW + rw) * R16 + r][lane];
+                    const float next = fmaxf(mx[r], m2);
+                    const float k1 = mx[r] == -INFINITY ? 0.f : exp2f(mx[r] - next), k2 = m2 == -INFINITY ? 0.f : exp2f(m2 - next);
+                    // a NaN sum with no maximum (every weight of a half a NaN) has to stay one
+                    sum[r] = (mx[r] == -INFINITY ? sum[r] : sum[r] * k1) + (m2 == -INFINITY ? s2 : s2 * k2);
+                    mx[r] = next;
+#pragma unroll
+                    for (int d = 0; d < NB; ++d) {
+                        if (d % 4 == 0) __builtin_amdgcn_sched_barrier(0);
+                        const f32x4 other = ex[d * 64];
+                        o[r][d] = o[r][d] * (mx[r] == -INFINITY ? 1.f : k1) + other * (mx[r] == -INFINITY ? 1.f : k2);
+                    }
+                }
+            }
+            const uint32_t row = row0 + (rw * R16 + r) * 16u + l16;
+            if (kw == 0 && row < rows) {
+                const float inv = sum[r] == 0.f ? 0.f : 1.f / sum[r];
+                const float lse2 = sum[r] == 0.f ? -INFINITY : (mx[r] == -INFINITY ? 0.f : mx[r]) + log2f(sum[r]);
+                if (whole) {
+                    const uint32_t i = row / p.heads, h = row - i * p.heads;
+                    const uint64_t t = (uint64_t)s.q0 + i;
+                    uint16_t* out = p.out + t * p.out_token + h * p.out_head + dw * NB * 16;
+#pragma unroll
+                    for (int d = 0; d < NB; ++d) {
+                        const f32x4 v = o[r][d] * inv;
+                        *(bf16x4*)(out + d * 16 + g * 4) = __builtin_convertvector(v, bf16x4);
+                    }
+                    if (p.lse && g == 0 && dw == 0) p.lse[t * p.lse_token + h] = lse2 * kLn2;
+                } else {
+                    const uint64_t at = (uint64_t)slot * M + (rw * R16 + r) * 16u + l16;
+                    float* out = p.part + at * 512 + dw * NB * 16;
+#pragma unroll
+                    for (int d = 0; d < NB; ++d) *(f32x4*)(out + d * 16 + g * 4) = o[r][d] * inv;
+                    if (g == 0 && dw == 0) p.part_lse[at] = lse2;
+                }
+            }
+        }
+        barrier();    // before the ring takes the next unit's tiles
+    }
+}
+
+// Joins the partial results of units that were cut between blocks: a group of
+// 128 threads takes one (token, head) row, 4 columns a thread, and adds the
+// blocks' parts in order.
+template <bool Slots>
+__global__ __launch_bounds__(256) void combine_kernel(const AttendParams p, uint32_t M) {
+    const uint64_t each = p.line[p.num_seqs];
+    const bool empty = p.head->capacity <= 0;
+    const uint32_t col = (threadIdx.x & 127u) * 4u;
+    const uint64_t per = (uint64_t)p.max_q * p.heads, all = per * p.num_seqs;
+    for (uint64_t x = (uint64_t)blockIdx.x * 2 + (threadIdx.x >> 7); x < all; x += (uint64_t)gridDim.x * 2) {
+        const uint32_t b = (uint32_t)(x / per), row = (uint32_t)(x - b * per);
+        const Seq s = sequence<Slots>(p, b, M, empty);
+        const uint32_t m = s.n > p.max_q ? p.max_q : s.n;
+        if (row >= m * p.heads) continue;
+        const uint32_t unit = row / M;
+        const uint64_t first = (Slots ? (uint64_t)b * s.units * s.tiles : p.line[b]) + (uint64_t)unit * s.tiles;
+        const uint64_t w0 = first / each, w1 = (first + s.tiles - 1) / each;
+        if (w0 == w1) continue;
+        const uint32_t in = row - unit * M;
+        float top = -INFINITY;
+        for (uint64_t w = w0; w <= w1; ++w) {
+            const uint64_t at = (2 * w + (w == w0 && first != w0 * each ? 1 : 0)) * M + in;
+            top = fmaxf(top, p.part_lse[at]);
+        }
+        const float ref = top == -INFINITY ? 0.f : top;
+        float total = 0.f;
+        f32x4 o = {0.f, 0.f, 0.f, 0.f};
+        for (uint64_t w = w0; w <= w1; ++w) {
+            const uint64_t at = (2 * w + (w == w0 && first != w0 * each ? 1 : 0)) * M + in;
+            const float k = exp2f(p.part_lse[at] - ref);
+            const f32x4 v = *(const f32x4*)(p.part + at * 512 + col);
+            total += k;
+            o += v * k;
+        }
+        const uint32_t i = row / p.heads, h = row - i * p.heads;
+        const uint64_t t = (uint64_t)s.q0 + i;
+        o = o * (total == 0.f ? 0.f : 1.f / total);
+        *(bf16x4*)(p.out + t * p.out_token + h * p.out_head + col) = __builtin_convertvector(o, bf16x4);
+        if (p.lse && col == 0) p.lse[t * p.lse_token + h] = total == 0.f ? -INFINITY : (ref + log2f(total)) * kLn2;
+    }
+}
+
+// ---- accumulated weights ------------------------------------------------------------
+
+// A block takes up to kWeightTiles tiles of one sequence and passes over its
+// query rows, 128 at a time (16 a wave, the operands in registers).  A position
+// belongs to one block: its sum over rows runs lane by lane (DPP over the 16
+// rows of a lane group), pass by pass and wave by wave, always in that order.
+// Bound by reading the rows, once per 128 query rows.
+constexpr uint32_t kWeightTiles = 16;
+
+struct WeightShared {
+    alignas(16) uint8_t ring[kRing * kTileBytes];
+    float sums[kWaves][kWeightTiles * 64];
+};
+
+// Sum over the 16 lanes of a row: every lane gets it.
+__device__ __forceinline__ float sum16(float v) {
+    v += __shfl_xor(v, 1);
+    v += __shfl_xor(v, 2);
+    v += __shfl_xor(v, 4);
+    return v + __shfl_xor(v, 8);
+}
+
+__global__ __launch_bounds__(kThreads) void weights_kernel(const AttendParams p, uint32_t run) {
+    __shared__ WeightShared sh;
+    const uint32_t lane = threadIdx.x & 63u, l16 = lane & 15u, g = lane >> 4;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t b = p.first_seq + blockIdx.y, t0 = blockIdx.x * run;
+    const int64_t capacity = p.head->capacity;
+    const Seq s = sequence<false>(p, b, 128, capacity <= 0);
+    const uint32_t tiles = s.kv ? s.tiles : 0u;
+    const uint32_t t1 = t0 + run < tiles ? t0 + run : tiles;
+    const uint32_t m = s.n > p.max_q ? p.max_q : s.n, rows = m * p.heads;
+    for (uint32_t i = threadIdx.x; i < kWaves * kWeightTiles * 64; i += kThreads) (&sh.sums[0][0])[i] = 0.f;
+    const int32_t* table = p.pages + (uint64_t)b * p.pages_stride;
+    const int64_t base = (int64_t)s.kv - s.n;
+    const uint32_t clear = base < 0 ? 0u : (uint32_t)(p.tree ? base : base + 1);   // every token sees those
+    const uint32_t ring = lds_offset(sh.ring);
+    auto page = [&](uint32_t t) -> int64_t {
+        const int64_t v = t < t1 ? table[t] : -1;
+        return v >= 0 && v < capacity / 64 ? v : -1;
+    };
+    auto fetch = [&](uint32_t t, int64_t pg) {
+        const uint8_t* from = p.main_base + (uint64_t)(pg < 0 ? 0 : pg) * p.main_page_stride + lane * 16u;
+        const uint32_t to = ring + (t % kRing) * kTileBytes;
+#pragma unroll
+        for (int i = 0; i < 6; ++i) {
+            const uint32_t c = wave + kWaves * i;
+            if (i == 5 && wave != 0) break;
+            copy16_to_lds(from + c * 1024u, to + c * 1024u);
+        }
+    };
+
+    for (uint32_t row0 = 0; row0 < rows && t0 < t1; row0 += 128) {
+        const uint32_t at = row0 + wave * 16u + l16, row = at < rows ? at : rows - 1;
+        const uint32_t i = row / p.heads, h = row - i * p.heads;
+        const uint64_t t = (uint64_t)s.q0 + i;
+        QFrag q[1];
+        load_query(q[0], p.q_latent + t * p.q_latent_token + h * p.q_latent_head,
+                   p.q_rope + t * p.q_rope_token + h * p.q_rope_head, g);
+        const float lse = p.lse[t * p.lse_token + h];
+        // a row of -inf saw nothing; rows behind the last one add nothing
+        const bool adds = at < rows && lse != -INFINITY;
+        const float lse2 = adds ? lse * 1.44269504088896341f : INFINITY;
+        barrier();                        // the ring is free
+        int64_t pg[3] = {page(t0), page(t0 + 1), page(t0 + 2)};
+        fetch(t0, pg[0]);
+        if (t0 + 1 < t1) fetch(t0 + 1, pg[1]);
+        for (uint32_t x = t0; x < t1; ++x) {
+            wait_tile(wave, x + 1 < t1);
+            if (x + 2 < t1) fetch(x + 2, pg[2]);
+            const int64_t now = pg[0];
+            pg[0] = pg[1];
+            pg[1] = pg[2];
+            pg[2] = page(x + 3);
+            if (now < 0) {
+                if (row0 == 0 && threadIdx.x == 0) atomicAdd(p.invalid_count, 1ull);
+                continue;
+            }
+            uint8_t* tile = sh.ring + (x % kRing) * kTileBytes;
+            const uint32_t left = s.kv - x * 64u;
+            const uint64_t live = left < 64 ? (1ull << left) - 1 : ~0ull;
+            const bool masked = x * 64u + 64u > clear;
+            if (masked) clean_tile(tile, live);
+#pragma unroll 1
+            for (uint32_t u = 0; u < 4; ++u) {
+                f32x4 v[1];
+                scores16<1>(v, tile + u * 16 * kRow, q, l16, g);
+                v[0] *= p.scale_log2;
+                if (masked) {
+                    const Sees see = sees<false>(p, s, i);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t key = u * 16 + 4 * g + k;
+                        const bool on = ((live >> key) & 1u) && see(x * 64u + key);
+                        v[0][k] = on ? v[0][k] : -INFINITY;
+                    }
+                }
+                float keep = 0.f;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float w = adds ? __builtin_amdgcn_exp2f(v[0][k] - lse2) : 0.f;
+                    const float total = sum16(w);
+                    keep = (int)l16 == k ? total : keep;
+                }
+                if (l16 < 4) sh.sums[wave][(x - t0) * 64 + u * 16 + 4 * g + l16] += keep;
+            }
+        }
+    }
+    barrier();
+    __syncthreads();
+    const uint32_t end = t0 + run;
+    for (uint32_t k = threadIdx.x; k < (end - t0) * 64u; k += kThreads) {
+        const uint32_t pos = t0 * 64u + k;
+        if (pos >= p.max_kv) break;
+        const uint64_t at = (uint64_t)b * p.weights_stride + pos;
+        float v = 0.f;
+        for (uint32_t w = 0; w < kWaves; ++w) v += sh.sums[w][k];
+        p.weights_out[at] = (p.weights_in ? p.weights_in[at] : 0.f) + v;
+    }
+}
+
+template <int R16, int RW, int KW, int DW>
+hipError_t launch_shape(const AttendParams& p, uint32_t blocks, hipStream_t stream) {
+    constexpr uint32_t M = 16 * R16 * RW;
+    const uint64_t rows = (uint64_t)p.max_q * p.heads * p.num_seqs;
+    const uint32_t joins = (uint32_t)(rows / 2 + 1 < 4096 ? rows / 2 + 1 : 4096);
+    (void)hipGetLastError();
+    if (p.by_slots) {
+        attend_kernel<R16, RW, KW, DW, true><<<dim3(blocks), dim3(kThreads), 0, stream>>>(p);
+        combine_kernel<true><<<dim3(joins), dim3(256), 0, stream>>>(p, M);
+    } else {
+        attend_kernel<R16, RW, KW, DW, false><<<dim3(blocks), dim3(kThreads), 0, stream>>>(p);
+        combine_kernel<false><<<dim3(joins), dim3(256), 0, stream>>>(p, M);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace
+
+AttendPlan plan_attend(uint64_t rows, uint64_t num_seqs, uint64_t max_kv) {
+    AttendPlan a;
+    a.rows = rows <= 16 ? 16u : rows <= 32 ? 32u : rows <= 64 ? 64u : 128u;
+    const uint64_t units = num_seqs * ((rows + a.rows - 1) / a.rows);
+    const uint64_t tiles = max_kv ? (max_kv + 63) / 64 : 1;
+    // one block a CU; never more than the line has runs of two tiles
+    const uint64_t runs = units * ((tiles + 1) / 2) + 1;
+    a.blocks = (uint32_t)(units >= 256 || runs >= 256 ? 256 : runs);
+    a.line_bytes = ((num_seqs + 1) * 8 + 255) / 256 * 256;
+    a.lse_bytes = (uint64_t)a.blocks * 2 * a.rows * 4;
+    a.bytes = a.line_bytes + a.lse_bytes + (uint64_t)a.blocks * 2 * a.rows * 512 * 4;
+    return a;
+}
+
+hipError_t launch_attend(const AttendParams& given, void* workspace, hipStream_t stream) {
+    AttendParams p = given;
+    const AttendPlan a = plan_attend((uint64_t)p.max_q * p.heads, p.num_seqs, p.by_slots ? p.num_slots : p.max_kv);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    p.line = reinterpret_cast<uint64_t*>(ws);
+    p.part_lse = reinterpret_cast<float*>(ws + a.line_bytes);
+    p.part = reinterpret_cast<float*>(ws + a.line_bytes + a.lse_bytes);
+    switch (a.rows) {
+        case 16: return launch_shape<1, 1, 2, 4>(p, a.blocks, stream);
+        case 32: return launch_shape<1, 2, 2, 2>(p, a.blocks, stream);
+        case 64: return launch_shape<1, 4, 2, 1>(p, a.blocks, stream);
+        default: return launch_shape<1, 8, 1, 1>(p, a.blocks, stream);
+    }
+}
+
+hipError_t launch_attend_weights(const AttendParams& p, hipStream_t stream) {
+    const uint32_t tiles = (p.max_kv + 63) / 64;
+    // runs long enough to fill the card about twice, up to what a block's sums hold
+    uint64_t run = ((uint64_t)tiles * p.num_seqs + 511) / 512;
+    run = run < 1 ? 1 : run > kWeightTiles ? kWeightTiles : run;
+    const uint32_t blocks = (uint32_t)((tiles + run - 1) / run);
+    (void)hipGetLastError();
+    for (uint32_t b = 0; b < p.num_seqs; b += 32768) {          // the grid's second dimension
+        AttendParams q = p;
+        q.num_seqs = p.num_seqs - b < 32768 ? p.num_seqs - b : 32768;
+        q.first_seq = b;
+        weights_kernel<<<dim3(blocks, q.num_seqs), dim3(kThreads), 0, stream>>>(q, (uint32_t)run);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace kvpub

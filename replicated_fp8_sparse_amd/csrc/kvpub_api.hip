@@ -4,6 +4,7 @@
 // direct-KV publication fence", commit list: opt-in allocation either fully
 // succeeds at startup or leaves nothing behind; teardown drops every view).
 #include <algorithm>
+#include <cmath>
 #include <cstddef>
 #include <cstdio>
 #include <cstdlib>
@@ -251,6 +252,102 @@ std::mutex g_static_mu;
 void release_static(kvpub_ctx* c) {
     std::lock_guard<std::mutex> lock(g_static_mu);
     g_static[c->cfg.device].in_use = false;
+}
+
+// ---- attention: argument checks and parameter blocks ------------------------
+
+constexpr int64_t kMaxQueryTokens = int64_t(1) << 24;
+constexpr uint32_t kMaxPositions = 1u << 30;
+constexpr uint32_t kMaxSeqs = 65536;
+
+bool good_stride(int64_t s, int64_t least) { return s >= least && s % 8 == 0 && s <= INT32_MAX; }
+
+// A [T, H, width] bf16 array: token stride any multiple of 8 from 0 on (0 repeats a row).
+bool good_rows(const void* base, int64_t token, int64_t head, int64_t width, uint32_t heads) {
+    return base && aligned(base, 16) && good_stride(token, 0) && good_stride(head, heads > 1 ? width : 0);
+}
+
+bool good_queries(const kvpub_queries* q) {
+    return q && q->num_tokens >= 0 && q->num_tokens <= kMaxQueryTokens && q->num_heads >= 1 && q->num_heads <= 128 &&
+           std::isfinite(q->scale) && std::isfinite(q->scale * 1.44269504f);
+}
+
+bool good_pages(const kvpub_pages* g) {
+    if (!g || g->num_seqs > kMaxSeqs || g->max_q_len < 1 || g->max_kv_len > kMaxPositions) return false;
+    return g->tree_mask ? g->tree_words >= 1 && g->tree_words <= 64 : g->tree_words == 0;
+}
+
+// Rows that a written array must keep apart: heads by head, tokens by token.
+bool good_output(const void* out, int64_t token, int64_t head, int64_t width, uint32_t heads, int64_t tokens) {
+    if (!good_rows(out, token, head, width, heads)) return false;
+    return tokens <= 1 || token >= width;
+}
+
+bool good_lse(const float* lse, int64_t stride, uint32_t heads, int64_t tokens) {
+    return !lse || (aligned(lse, 4) && stride >= 0 && stride <= INT32_MAX && (tokens <= 1 || stride >= (int64_t)heads));
+}
+
+kvpub_status check_reader(const kvpub_ctx* ctx, uint32_t replica, uint32_t layer) {
+    if (!ctx || replica >= ctx->cfg.num_replicas || layer >= ctx->cfg.num_layers) return KVPUB_ERR_INVALID_ARG;
+    // a page that cannot be read is replaced by page 0 in the address, so one has to be backed
+    if (ctx->cfg.num_pages == 0) return KVPUB_ERR_INVALID_ARG;
+    return KVPUB_OK;
+}
+
+kvpub_status check_queries(const kvpub_queries* q) {
+    if (!good_queries(q)) return KVPUB_ERR_INVALID_ARG;
+    if (q->num_tokens == 0) return KVPUB_OK;
+    if (!good_rows(q->q_latent, q->q_latent_token_stride, q->q_latent_head_stride, KVPUB_LATENT_DIM, q->num_heads) ||
+        !good_rows(q->q_rope, q->q_rope_token_stride, q->q_rope_head_stride, KVPUB_ROPE_DIM, q->num_heads))
+        return KVPUB_ERR_INVALID_ARG;
+    return KVPUB_OK;
+}
+
+kvpub_status check_pages(const kvpub_queries* q, const kvpub_pages* g) {
+    if (!good_pages(g)) return KVPUB_ERR_INVALID_ARG;
+    if (g->num_seqs == 0 || q->num_tokens == 0) return KVPUB_OK;
+    const int64_t tiles = ((int64_t)g->max_kv_len + 63) / 64;
+    if (!g->kv_len || !aligned(g->kv_len, 4) || !g->page_table || !aligned(g->page_table, 4)) return KVPUB_ERR_INVALID_ARG;
+    if (!aligned(g->q_start, 4) || !aligned(g->tree_mask, 8)) return KVPUB_ERR_INVALID_ARG;
+    if (g->page_table_stride < tiles || g->page_table_stride > INT32_MAX) return KVPUB_ERR_INVALID_ARG;
+    // one token a sequence: every sequence needs its token
+    if (!g->q_start && (int64_t)g->num_seqs > q->num_tokens) return KVPUB_ERR_INVALID_ARG;
+    return KVPUB_OK;
+}
+
+kvpub::AttendParams attend_params(kvpub_ctx* ctx, uint32_t replica, uint32_t layer, const kvpub_queries* q) {
+    kvpub::AttendParams a;
+    std::memset(&a, 0, sizeof a);
+    a.main_base = ctx->main_base[replica] + (uint64_t)layer * ctx->cfg.main_layer_stride;
+    a.main_page_stride = ctx->cfg.main_page_stride;
+    a.head = reinterpret_cast<const kvpub::CtxHead*>(ctx->words + kvpub::kStatusOffset);
+    a.invalid_count = reinterpret_cast<unsigned long long*>(ctx->words + kvpub::kInvalidOffset);
+    a.q_latent = static_cast<const uint16_t*>(q->q_latent);
+    a.q_rope = static_cast<const uint16_t*>(q->q_rope);
+    a.q_latent_token = q->q_latent_token_stride;
+    a.q_latent_head = q->q_latent_head_stride;
+    a.q_rope_token = q->q_rope_token_stride;
+    a.q_rope_head = q->q_rope_head_stride;
+    a.num_tokens = (uint32_t)q->num_tokens;
+    a.heads = q->num_heads;
+    a.scale_log2 = (float)((double)q->scale * 1.4426950408889634074);
+    return a;
+}
+
+void set_pages(kvpub::AttendParams& a, const kvpub_pages* g) {
+    a.num_seqs = g->num_seqs;
+    a.max_q = (uint32_t)std::min<int64_t>(g->q_start ? g->max_q_len : 1, a.num_tokens);
+    a.max_kv = g->max_kv_len;
+    a.kv_len = g->kv_len;
+    a.q_start = g->q_start;
+    a.pages = g->page_table;
+    a.pages_stride = g->page_table_stride;
+    a.tree = g->tree_mask;
+    a.tree_words = g->tree_words;
+}
+
+uint64_t query_rows(const kvpub_queries* q, const kvpub_pages* g) {
+    return (uint64_t)std::min<int64_t>(g->q_start ? g->max_q_len : 1, q->num_tokens) * q->num_heads;
 }
 
 }  // namespace
@@ -522,6 +619,215 @@ KVPUB_API kvpub_status kvpub_gather(kvpub_ctx* ctx, uint32_t replica, uint32_t l
     const uint64_t idx_span = std::max(ctx->cfg.num_pages * ctx->cfg.idx_page_stride, ctx->cfg.idx_layer_stride);
     g.offsets32 = main_span <= UINT32_MAX && idx_span <= UINT32_MAX ? 1u : 0u;
     return map_hip(kvpub::launch_gather(g, static_cast<hipStream_t>(stream)));
+}
+
+KVPUB_API uint64_t kvpub_attend_workspace(const kvpub_queries* q, const kvpub_pages* pages) {
+    if (!good_queries(q) || !good_pages(pages) || q->num_tokens == 0 || pages->num_seqs == 0) return 0;
+    return kvpub::plan_attend(query_rows(q, pages), pages->num_seqs, pages->max_kv_len).bytes;
+}
+
+KVPUB_API uint64_t kvpub_attend_slots_workspace(const kvpub_queries* q, uint32_t num_slots) {
+    if (!good_queries(q) || num_slots > (1u << 24) || q->num_tokens == 0) return 0;
+    return kvpub::plan_attend(q->num_heads, q->num_tokens, num_slots).bytes;
+}
+
+KVPUB_API kvpub_status kvpub_attend(kvpub_ctx* ctx, uint32_t replica, uint32_t layer, const kvpub_queries* q,
+                                    const kvpub_pages* pages, void* out, int64_t out_token_stride,
+                                    int64_t out_head_stride, float* lse, int64_t lse_token_stride,
+                                    void* workspace, uint64_t workspace_bytes, kvpub_stream_t stream) {
+    kvpub_status st = check_reader(ctx, replica, layer);
+    if (st == KVPUB_OK) st = check_queries(q);
+    if (st == KVPUB_OK) st = check_pages(q, pages);
+    if (st != KVPUB_OK || q->num_tokens == 0 || pages->num_seqs == 0) return st;
+    if (!good_output(out, out_token_stride, out_head_stride, KVPUB_LATENT_DIM, q->num_heads, q->num_tokens) ||
+        !good_lse(lse, lse_token_stride, q->num_heads, q->num_tokens))
+        return KVPUB_ERR_INVALID_ARG;
+    if (!workspace || !aligned(workspace, 16) || workspace_bytes < kvpub_attend_workspace(q, pages))
+        return KVPUB_ERR_INVALID_ARG;
+    DeviceGuard guard(ctx->cfg.device);
+    if (!guard.ok) return KVPUB_ERR_HIP;
+    kvpub::AttendParams a = attend_params(ctx, replica, layer, q);
+    set_pages(a, pages);
+    a.out = static_cast<uint16_t*>(out);
+    a.out_token = out_token_stride;
+    a.out_head = out_head_stride;
+    a.lse = lse;
+    a.lse_token = lse_token_stride;
+    return map_hip(kvpub::launch_attend(a, workspace, static_cast<hipStream_t>(stream)));
+}
+
+KVPUB_API kvpub_status kvpub_attend_slots(kvpub_ctx* ctx, uint32_t replica, uint32_t layer, const kvpub_queries* q,
+                                          const int64_t* slots, int64_t slots_stride, uint32_t num_slots, void* out,
+                                          int64_t out_token_stride, int64_t out_head_stride, float* lse,
+                                          int64_t lse_token_stride, void* workspace, uint64_t workspace_bytes,
+                                          kvpub_stream_t stream) {
+    kvpub_status st = check_reader(ctx, replica, layer);
+    if (st == KVPUB_OK) st = check_queries(q);
+    if (st != KVPUB_OK) return st;
+    if (num_slots > (1u << 24)) return KVPUB_ERR_INVALID_ARG;
+    if (q->num_tokens == 0) return KVPUB_OK;
+    if (num_slots > 0 && !slots) return KVPUB_ERR_INVALID_ARG;
+    if (!aligned(slots, 8) || slots_stride < (int64_t)num_slots || slots_stride > INT32_MAX) return KVPUB_ERR_INVALID_ARG;
+    if (!good_output(out, out_token_stride, out_head_stride, KVPUB_LATENT_DIM, q->num_heads, q->num_tokens) ||
+        !good_lse(lse, lse_token_stride, q->num_heads, q->num_tokens))
+        return KVPUB_ERR_INVALID_ARG;
+    if (!workspace || !aligned(workspace, 16) || workspace_bytes < kvpub_attend_slots_workspace(q, num_slots))
+        return KVPUB_ERR_INVALID_ARG;
+    DeviceGuard guard(ctx->cfg.device);
+    if (!guard.ok) return KVPUB_ERR_HIP;
+    kvpub::AttendParams a = attend_params(ctx, replica, layer, q);
+    a.num_seqs = a.num_tokens;
+    a.max_q = 1;
+    a.by_slots = 1;
+    a.num_slots = num_slots;
+    a.slots = slots;
+    a.slots_stride = slots_stride;
+    a.out = static_cast<uint16_t*>(out);
+    a.out_token = out_token_stride;
+    a.out_head = out_head_stride;
+    a.lse = lse;
+    a.lse_token = lse_token_stride;
+    return map_hip(kvpub::launch_attend(a, workspace, static_cast<hipStream_t>(stream)));
+}
+
+KVPUB_API kvpub_status kvpub_attend_weights(kvpub_ctx* ctx, uint32_t replica, uint32_t layer, const kvpub_queries* q,
+                                            const kvpub_pages* pages, const float* lse, int64_t lse_token_stride,
+                                            const float* weights_in, float* weights_out, int64_t weights_stride,
+                                            kvpub_stream_t stream) {
+    kvpub_status st = check_reader(ctx, replica, layer);
+    if (st == KVPUB_OK) st = check_queries(q);
+    if (st == KVPUB_OK) st = check_pages(q, pages);
+    if (st != KVPUB_OK || q->num_tokens == 0 || pages->num_seqs == 0 || pages->max_kv_len == 0) return st;
+    if (!lse || !good_lse(lse, lse_token_stride, q->num_heads, q->num_tokens)) return KVPUB_ERR_INVALID_ARG;
+    if (!weights_out || !aligned(weights_out, 4) || !aligned(weights_in, 4)) return KVPUB_ERR_INVALID_ARG;
+    if (weights_stride < (int64_t)pages->max_kv_len || weights_stride > INT32_MAX) return KVPUB_ERR_INVALID_ARG;
+    DeviceGuard guard(ctx->cfg.device);
+    if (!guard.ok) return KVPUB_ERR_HIP;
+    kvpub::AttendParams a = attend_params(ctx, replica, layer, q);
+    set_pages(a, pages);
+    a.lse = const_cast<float*>(lse);
+    a.lse_token = lse_token_stride;
+    a.weights_in = weights_in;
+    a.weights_out = weights_out;
+    a.weights_stride = weights_stride;
+    return map_hip(kvpub::launch_attend_weights(a, static_cast<hipStream_t>(stream)));
+}
+
+static bool good_evict(const kvpub_evict_io* io) {
+    return io && io->reserved == 0 && io->num_seqs <= kMaxSeqs && io->max_kv_len >= 1 && io->max_kv_len <= kMaxPositions &&
+           io->budget >= 1 && io->budget <= kMaxPositions && (uint64_t)io->first + io->last <= io->budget;
+}
+
+KVPUB_API uint64_t kvpub_evict_workspace(const kvpub_evict_io* io) {
+    if (!good_evict(io)) return 0;
+    const uint64_t chunks = (io->max_kv_len + 63) / 64;
+    return (uint64_t)io->num_seqs * (2 * chunks + 2) * 4;
+}
+
+KVPUB_API kvpub_status kvpub_evict(kvpub_ctx* ctx, uint32_t layer, const kvpub_evict_io* io, void* workspace,
+                                   uint64_t workspace_bytes, kvpub_stream_t stream) {
+    kvpub_status st = check_reader(ctx, 0, layer);
+    if (st != KVPUB_OK) return st;
+    if (!good_evict(io)) return KVPUB_ERR_INVALID_ARG;
+    if (io->num_seqs == 0) return KVPUB_OK;
+    const void* arrays[] = {io->weights_in, io->weights_out, io->kv_len, io->page_table, io->dst_table, io->kept, io->new_len};
+    for (const void* p : arrays)
+        if (!p || !aligned(p, 4)) return KVPUB_ERR_INVALID_ARG;
+    const uint32_t most = std::min(io->budget, io->max_kv_len);
+    if (io->weights_stride < (int64_t)io->max_kv_len || io->weights_stride > INT32_MAX) return KVPUB_ERR_INVALID_ARG;
+    if (io->kept_stride < (int64_t)io->budget || io->kept_stride > INT32_MAX) return KVPUB_ERR_INVALID_ARG;
+    if (io->page_table_stride < ((int64_t)io->max_kv_len + 63) / 64 || io->page_table_stride > INT32_MAX) return KVPUB_ERR_INVALID_ARG;
+    if (io->dst_table_stride < ((int64_t)most + 63) / 64 || io->dst_table_stride > INT32_MAX) return KVPUB_ERR_INVALID_ARG;
+    const bool in_place = io->dst_table == io->page_table;
+    if (in_place && io->dst_table_stride != io->page_table_stride) return KVPUB_ERR_INVALID_ARG;
+    if (io->new_len == io->kv_len) return KVPUB_ERR_INVALID_ARG;      // kv_len is read again by later launches of the call
+    if (!workspace || !aligned(workspace, 16) || workspace_bytes < kvpub_evict_workspace(io)) return KVPUB_ERR_INVALID_ARG;
+    DeviceGuard guard(ctx->cfg.device);
+    if (!guard.ok) return KVPUB_ERR_HIP;
+    kvpub::EvictParams e;
+    std::memset(&e, 0, sizeof e);
+    for (uint32_t r = 0; r < ctx->cfg.num_replicas; ++r) {
+        e.main_base[r] = ctx->main_base[r] + (uint64_t)layer * ctx->cfg.main_layer_stride;
+        e.idx_base[r] = ctx->idx_base[r] + (uint64_t)layer * ctx->cfg.idx_layer_stride;
+    }
+    e.main_page_stride = ctx->cfg.main_page_stride;
+    e.idx_page_stride = ctx->cfg.idx_page_stride;
+    e.replicas = ctx->cfg.num_replicas;
+    e.head = reinterpret_cast<const kvpub::CtxHead*>(ctx->words + kvpub::kStatusOffset);
+    e.invalid_count = reinterpret_cast<unsigned long long*>(ctx->words + kvpub::kInvalidOffset);
+    e.weights_in = io->weights_in;
+    e.weights_out = io->weights_out;
+    e.weights_stride = io->weights_stride;
+    e.kv_len = io->kv_len;
+    e.pages = io->page_table;
+    e.pages_stride = io->page_table_stride;
+    e.dst = io->dst_table;
+    e.dst_stride = io->dst_table_stride;
+    e.kept = io->kept;
+    e.kept_stride = io->kept_stride;
+    e.new_len = io->new_len;
+    e.num_seqs = io->num_seqs;
+    e.max_kv = io->max_kv_len;
+    e.budget = io->budget;
+    e.first = io->first;
+    e.last = io->last;
+    e.in_place = in_place ? 1u : 0u;
+    e.state = static_cast<uint32_t*>(workspace);
+    return map_hip(kvpub::launch_evict(e, static_cast<hipStream_t>(stream)));
+}
+
+KVPUB_API kvpub_status kvpub_attend_expanded(kvpub_ctx* ctx, const kvpub_expanded_io* io, kvpub_stream_t stream) {
+    if (!ctx || !io) return KVPUB_ERR_INVALID_ARG;
+    if (io->reserved != 0 || io->causal > 1 || io->num_heads < 1 || io->num_heads > 128 || io->num_seqs > 65535 ||
+        io->max_q_len < 1 || io->num_tokens < 0 || io->num_tokens > kMaxQueryTokens || io->num_keys < 0 ||
+        io->num_keys > kMaxQueryTokens || !std::isfinite(io->scale) || !std::isfinite(io->scale * 1.44269504f))
+        return KVPUB_ERR_INVALID_ARG;
+    if (io->num_tokens == 0 || io->num_seqs == 0) return KVPUB_OK;
+    const uint32_t H = io->num_heads;
+    if (!good_rows(io->q_nope, io->q_nope_token_stride, io->q_nope_head_stride, 128, H) ||
+        !good_rows(io->q_rope, io->q_rope_token_stride, io->q_rope_head_stride, 64, H) ||
+        !good_output(io->out, io->out_token_stride, io->out_head_stride, 128, H, io->num_tokens) ||
+        !good_lse(io->lse, io->lse_token_stride, H, io->num_tokens))
+        return KVPUB_ERR_INVALID_ARG;
+    if (io->num_keys > 0 &&
+        (!good_rows(io->k_nope, io->k_nope_token_stride, io->k_nope_head_stride, 128, H) ||
+         !good_rows(io->k_rope, io->k_rope_token_stride, 64, 64, 1) ||
+         !good_rows(io->v, io->v_token_stride, io->v_head_stride, 128, H)))
+        return KVPUB_ERR_INVALID_ARG;
+    if (!io->q_start || !io->k_start || !aligned(io->q_start, 4) || !aligned(io->k_start, 4)) return KVPUB_ERR_INVALID_ARG;
+    DeviceGuard guard(ctx->cfg.device);
+    if (!guard.ok) return KVPUB_ERR_HIP;
+    kvpub::ExpandedParams e;
+    std::memset(&e, 0, sizeof e);
+    e.q_nope = static_cast<const uint16_t*>(io->q_nope);
+    e.q_rope = static_cast<const uint16_t*>(io->q_rope);
+    e.k_nope = static_cast<const uint16_t*>(io->k_nope);
+    e.k_rope = static_cast<const uint16_t*>(io->k_rope);
+    e.v = static_cast<const uint16_t*>(io->v);
+    e.out = static_cast<uint16_t*>(io->out);
+    e.lse = io->lse;
+    e.q_nope_token = io->q_nope_token_stride;
+    e.q_nope_head = io->q_nope_head_stride;
+    e.q_rope_token = io->q_rope_token_stride;
+    e.q_rope_head = io->q_rope_head_stride;
+    e.k_nope_token = io->k_nope_token_stride;
+    e.k_nope_head = io->k_nope_head_stride;
+    e.k_rope_token = io->k_rope_token_stride;
+    e.v_token = io->v_token_stride;
+    e.v_head = io->v_head_stride;
+    e.out_token = io->out_token_stride;
+    e.out_head = io->out_head_stride;
+    e.lse_token = io->lse_token_stride;
+    e.q_start = io->q_start;
+    e.k_start = io->k_start;
+    e.num_tokens = (uint32_t)io->num_tokens;
+    e.num_keys = (uint32_t)io->num_keys;
+    e.num_seqs = io->num_seqs;
+    e.heads = H;
+    e.max_q = (uint32_t)std::min<int64_t>(io->max_q_len, io->num_tokens);
+    e.causal = io->causal;
+    e.scale_log2 = (float)((double)io->scale * 1.4426950408889634074);
+    return map_hip(kvpub::launch_expanded(e, static_cast<hipStream_t>(stream)));
 }
 
 KVPUB_API kvpub_status kvpub_fence(kvpub_ctx* ctx, uint32_t lane, kvpub_stream_t stream) {

@@ -85,6 +85,114 @@ struct GatherParams {
     uint32_t offsets32;          // every offset within a layer fits in 32 bits (layer span < 2^32)
 };
 
+// Latent attention (attend_kernel.hip).  Strides in elements.
+struct AttendParams {
+    const uint8_t* main_base;    // the replica, already offset to the layer
+    uint64_t main_page_stride;   // bytes
+    const CtxHead* head;         // capacity (num_pages * 64)
+    unsigned long long* invalid_count;
+    const uint16_t* q_latent;    // bf16
+    const uint16_t* q_rope;
+    int64_t q_latent_token, q_latent_head, q_rope_token, q_rope_head;
+    uint32_t num_tokens;
+    uint32_t heads;
+    uint32_t num_seqs;           // slot lists: one for each token
+    uint32_t max_q;              // slot lists: 1
+    uint32_t max_kv;
+    uint32_t num_slots;
+    const int32_t* kv_len;
+    const int32_t* q_start;      // null: one token a sequence
+    const int32_t* pages;
+    int64_t pages_stride;
+    const uint64_t* tree;        // null: causal
+    uint32_t tree_words;
+    float scale_log2;            // scale * log2(e)
+    uint32_t by_slots;           // 1: slot lists, else pages
+    const int64_t* slots;
+    int64_t slots_stride;
+    uint16_t* out;               // bf16
+    int64_t out_token, out_head;
+    float* lse;                  // null: not written (attend); the given sums (weights)
+    int64_t lse_token;
+    const float* weights_in;     // weights only
+    float* weights_out;
+    int64_t weights_stride;
+    uint32_t first_seq;          // weights only: sequence of the grid's first row
+    uint64_t* line;              // workspace: prefix of each sequence's work, then the blocks' share
+    float* part_lse;             // workspace: [blocks * 2][rows]
+    float* part;                 // workspace: [blocks * 2][rows][512]
+};
+
+// How a call is cut: query rows of a unit, blocks, and the workspace's parts.
+struct AttendPlan {
+    uint32_t rows;
+    uint32_t blocks;
+    uint64_t line_bytes;
+    uint64_t lse_bytes;
+    uint64_t bytes;
+};
+// rows: the most (token, head) rows of one sequence.
+AttendPlan plan_attend(uint64_t rows, uint64_t num_seqs, uint64_t max_kv);
+// Enqueue latent attention on `stream`; returns the launch status.
+hipError_t launch_attend(const AttendParams& p, void* workspace, hipStream_t stream);
+hipError_t launch_attend_weights(const AttendParams& p, hipStream_t stream);
+
+// Eviction (evict_kernel.hip).
+struct EvictParams {
+    uint8_t* main_base[kMaxReplicas];   // replica r, already offset to the layer
+    uint8_t* idx_base[kMaxReplicas];
+    uint64_t main_page_stride;   // bytes
+    uint64_t idx_page_stride;
+    uint32_t replicas;
+    const CtxHead* head;         // status and capacity
+    unsigned long long* invalid_count;
+    const float* weights_in;
+    float* weights_out;
+    int64_t weights_stride;
+    const int32_t* kv_len;
+    const int32_t* pages;
+    int64_t pages_stride;
+    const int32_t* dst;
+    int64_t dst_stride;
+    int32_t* kept;
+    int64_t kept_stride;
+    int32_t* new_len;
+    uint32_t num_seqs;
+    uint32_t max_kv;
+    uint32_t budget;
+    uint32_t first;
+    uint32_t last;
+    uint32_t in_place;
+    uint32_t chunks;             // set by launch_evict: ceil(max_kv / 64)
+    uint32_t* state;             // workspace: each sequence's ticket, flags[chunks], ranks[chunks + 1]
+};
+hipError_t launch_evict(const EvictParams& p, hipStream_t stream);
+
+// Latent attention in its expanded form (expanded_kernel.hip).  Strides in elements.
+struct ExpandedParams {
+    const uint16_t* q_nope;
+    const uint16_t* q_rope;
+    const uint16_t* k_nope;
+    const uint16_t* k_rope;
+    const uint16_t* v;
+    uint16_t* out;
+    float* lse;                  // null: not written
+    int64_t q_nope_token, q_nope_head, q_rope_token, q_rope_head;
+    int64_t k_nope_token, k_nope_head, k_rope_token, v_token, v_head;
+    int64_t out_token, out_head, lse_token;
+    const int32_t* q_start;
+    const int32_t* k_start;
+    uint32_t num_tokens;
+    uint32_t num_keys;
+    uint32_t num_seqs;
+    uint32_t heads;
+    uint32_t max_q;
+    uint32_t causal;
+    float scale_log2;
+    uint32_t first_seq;          // set by launch_expanded
+};
+hipError_t launch_expanded(const ExpandedParams& p, hipStream_t stream);
+
 // Enqueue the dequantizing gather on `stream`; returns the launch status.
 hipError_t launch_gather(const GatherParams& p, hipStream_t stream);
 // True if ctx's replicas are exactly these bases with these layer and page strides.

@@ -46,7 +46,9 @@ EXPORTS = ("kvpub_config_init", "kvpub_create", "kvpub_create_static", "kvpub_st
            "kvpub_graph_create", "kvpub_graph_replay", "kvpub_graph_destroy",
            "kvpub_epoch_read", "kvpub_error_read", "kvpub_participant_signal",
            "kvpub_destroy", "kvpub_strerror", "kvpub_abi_version", "kvpub_vmm_create",
-           "kvpub_vmm_grow", "kvpub_vmm_pages", "kvpub_vmm_destroy")
+           "kvpub_vmm_grow", "kvpub_vmm_pages", "kvpub_vmm_destroy",
+           "kvpub_attend_workspace", "kvpub_attend", "kvpub_attend_slots_workspace", "kvpub_attend_slots",
+           "kvpub_attend_weights", "kvpub_evict_workspace", "kvpub_evict", "kvpub_attend_expanded")
 
 
 class kvpub_config(ctypes.Structure):
@@ -79,6 +81,68 @@ class kvpub_layer_io(ctypes.Structure):
                 ("reserved", ctypes.c_uint32)]
 
 
+class kvpub_queries(ctypes.Structure):
+    _fields_ = [("q_latent", ctypes.c_void_p),
+                ("q_rope", ctypes.c_void_p),
+                ("q_latent_token_stride", ctypes.c_int64),
+                ("q_latent_head_stride", ctypes.c_int64),
+                ("q_rope_token_stride", ctypes.c_int64),
+                ("q_rope_head_stride", ctypes.c_int64),
+                ("num_tokens", ctypes.c_int64),
+                ("num_heads", ctypes.c_uint32),
+                ("scale", ctypes.c_float)]
+
+
+class kvpub_pages(ctypes.Structure):
+    _fields_ = [("kv_len", ctypes.c_void_p),
+                ("q_start", ctypes.c_void_p),
+                ("page_table", ctypes.c_void_p),
+                ("page_table_stride", ctypes.c_int64),
+                ("tree_mask", ctypes.c_void_p),
+                ("tree_words", ctypes.c_uint32),
+                ("num_seqs", ctypes.c_uint32),
+                ("max_q_len", ctypes.c_uint32),
+                ("max_kv_len", ctypes.c_uint32)]
+
+
+class kvpub_evict_io(ctypes.Structure):
+    _fields_ = [("weights_in", ctypes.c_void_p),
+                ("weights_out", ctypes.c_void_p),
+                ("weights_stride", ctypes.c_int64),
+                ("kv_len", ctypes.c_void_p),
+                ("page_table", ctypes.c_void_p),
+                ("page_table_stride", ctypes.c_int64),
+                ("dst_table", ctypes.c_void_p),
+                ("dst_table_stride", ctypes.c_int64),
+                ("kept", ctypes.c_void_p),
+                ("kept_stride", ctypes.c_int64),
+                ("new_len", ctypes.c_void_p),
+                ("num_seqs", ctypes.c_uint32),
+                ("max_kv_len", ctypes.c_uint32),
+                ("budget", ctypes.c_uint32),
+                ("first", ctypes.c_uint32),
+                ("last", ctypes.c_uint32),
+                ("reserved", ctypes.c_uint32)]
+
+
+class kvpub_expanded_io(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("q_nope", "q_rope", "k_nope", "k_rope", "v", "out", "lse")] +
+                [(n, ctypes.c_int64) for n in (
+                    "q_nope_token_stride", "q_nope_head_stride", "q_rope_token_stride", "q_rope_head_stride",
+                    "k_nope_token_stride", "k_nope_head_stride", "k_rope_token_stride", "v_token_stride",
+                    "v_head_stride", "out_token_stride", "out_head_stride", "lse_token_stride")] +
+                [("q_start", ctypes.c_void_p),
+                 ("k_start", ctypes.c_void_p),
+                 ("num_tokens", ctypes.c_int64),
+                 ("num_keys", ctypes.c_int64),
+                 ("num_seqs", ctypes.c_uint32),
+                 ("num_heads", ctypes.c_uint32),
+                 ("max_q_len", ctypes.c_uint32),
+                 ("causal", ctypes.c_uint32),
+                 ("scale", ctypes.c_float),
+                 ("reserved", ctypes.c_uint32)])
+
+
 class KvpubError(RuntimeError):
     def __init__(self, status, what=""):
         self.status = status
@@ -100,6 +164,7 @@ def load(path=LIB_PATH):
     vp, u32, u64, i64, i32 = (ctypes.c_void_p, ctypes.c_uint32, ctypes.c_uint64,
                               ctypes.c_int64, ctypes.c_int)
     cfgp = ctypes.POINTER(kvpub_config)
+    qp, pp, ep = ctypes.POINTER(kvpub_queries), ctypes.POINTER(kvpub_pages), ctypes.POINTER(kvpub_evict_io)
     sig = {
         "kvpub_config_init": (None, [cfgp, u32, u32, u64]),
         "kvpub_create": (i32, [cfgp, ctypes.POINTER(vp), ctypes.POINTER(vp), ctypes.POINTER(vp)]),
@@ -121,6 +186,14 @@ def load(path=LIB_PATH):
         "kvpub_vmm_grow": (i32, [vp, u64, vp]),
         "kvpub_vmm_pages": (i32, [vp, ctypes.POINTER(u64)]),
         "kvpub_vmm_destroy": (i32, [vp]),
+        "kvpub_attend_workspace": (u64, [qp, pp]),
+        "kvpub_attend": (i32, [vp, u32, u32, qp, pp, vp, i64, i64, vp, i64, vp, u64, vp]),
+        "kvpub_attend_slots_workspace": (u64, [qp, u32]),
+        "kvpub_attend_slots": (i32, [vp, u32, u32, qp, vp, i64, u32, vp, i64, i64, vp, i64, vp, u64, vp]),
+        "kvpub_attend_weights": (i32, [vp, u32, u32, qp, pp, vp, i64, vp, vp, i64, vp]),
+        "kvpub_evict_workspace": (u64, [ep]),
+        "kvpub_evict": (i32, [vp, u32, ep, vp, u64, vp]),
+        "kvpub_attend_expanded": (i32, [vp, ctypes.POINTER(kvpub_expanded_io), vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -277,3 +350,83 @@ def layer_io(latent, rope, indexer, slot_mapping, num_tokens, layer,
     """Build a kvpub_layer_io from device addresses."""
     return kvpub_layer_io(latent, rope, indexer, latent_row_stride, rope_row_stride,
                           indexer_row_stride, slot_mapping, num_tokens, layer, 0)
+
+
+# -- attention over the published cache ---------------------------------------
+# Descriptors (None passes a null pointer) are built by queries(), pages(),
+# evict_io() and expanded_io() below.
+
+def _ref(struct):
+    return None if struct is None else ctypes.byref(struct)
+
+
+def kvpub_attend_workspace(q, pages):
+    return load().kvpub_attend_workspace(_ref(q), _ref(pages))
+
+
+def kvpub_attend(ctx, replica, layer, q, pages, out, out_token_stride, out_head_stride, lse, lse_token_stride,
+                 workspace, workspace_bytes, stream=0):
+    return load().kvpub_attend(ctx, replica, layer, _ref(q), _ref(pages), out, out_token_stride, out_head_stride,
+                               lse, lse_token_stride, workspace, workspace_bytes, stream)
+
+
+def kvpub_attend_slots_workspace(q, num_slots):
+    return load().kvpub_attend_slots_workspace(_ref(q), num_slots)
+
+
+def kvpub_attend_slots(ctx, replica, layer, q, slots, slots_stride, num_slots, out, out_token_stride,
+                       out_head_stride, lse, lse_token_stride, workspace, workspace_bytes, stream=0):
+    return load().kvpub_attend_slots(ctx, replica, layer, _ref(q), slots, slots_stride, num_slots, out,
+                                     out_token_stride, out_head_stride, lse, lse_token_stride, workspace,
+                                     workspace_bytes, stream)
+
+
+def kvpub_attend_weights(ctx, replica, layer, q, pages, lse, lse_token_stride, weights_in, weights_out,
+                         weights_stride, stream=0):
+    return load().kvpub_attend_weights(ctx, replica, layer, _ref(q), _ref(pages), lse, lse_token_stride,
+                                       weights_in, weights_out, weights_stride, stream)
+
+
+def kvpub_evict_workspace(io):
+    return load().kvpub_evict_workspace(_ref(io))
+
+
+def kvpub_evict(ctx, layer, io, workspace, workspace_bytes, stream=0):
+    return load().kvpub_evict(ctx, layer, _ref(io), workspace, workspace_bytes, stream)
+
+
+def kvpub_attend_expanded(ctx, io, stream=0):
+    return load().kvpub_attend_expanded(ctx, _ref(io), stream)
+
+
+def queries(q_latent, q_rope, num_tokens, num_heads, scale, q_latent_token_stride=None,
+            q_latent_head_stride=LATENT_DIM, q_rope_token_stride=None, q_rope_head_stride=ROPE_DIM):
+    """Build a kvpub_queries from device addresses; strides default to dense [T, H, .]."""
+    lt = num_heads * LATENT_DIM if q_latent_token_stride is None else q_latent_token_stride
+    rt = num_heads * ROPE_DIM if q_rope_token_stride is None else q_rope_token_stride
+    return kvpub_queries(q_latent, q_rope, lt, q_latent_head_stride, rt, q_rope_head_stride, num_tokens,
+                         num_heads, scale)
+
+
+def pages(kv_len, page_table, page_table_stride, num_seqs, max_kv_len, q_start=0, max_q_len=1, tree_mask=0,
+          tree_words=0):
+    """Build a kvpub_pages from device addresses."""
+    return kvpub_pages(kv_len, q_start, page_table, page_table_stride, tree_mask, tree_words, num_seqs, max_q_len,
+                       max_kv_len)
+
+
+def evict_io(weights_in, weights_out, weights_stride, kv_len, page_table, page_table_stride, dst_table,
+             dst_table_stride, kept, kept_stride, new_len, num_seqs, max_kv_len, budget, first=0, last=0):
+    """Build a kvpub_evict_io from device addresses."""
+    return kvpub_evict_io(weights_in, weights_out, weights_stride, kv_len, page_table, page_table_stride, dst_table,
+                          dst_table_stride, kept, kept_stride, new_len, num_seqs, max_kv_len, budget, first, last, 0)
+
+
+def expanded_io(q_nope, q_rope, k_nope, k_rope, v, out, lse, q_start, k_start, num_seqs, num_heads, num_tokens,
+                num_keys, max_q_len, scale, k_head_stride=128, v_head_stride=128, causal=1):
+    """Build a kvpub_expanded_io from device addresses: dense queries, outputs and
+    RoPE rows, keys and values of the given head strides."""
+    H = num_heads
+    return kvpub_expanded_io(q_nope, q_rope, k_nope, k_rope, v, out, lse, H * 128, 128, H * 64, 64,
+                             H * k_head_stride, k_head_stride, 64, H * v_head_stride, v_head_stride, H * 128, 128, H,
+                             q_start, k_start, num_tokens, num_keys, num_seqs, H, max_q_len, causal, scale, 0)
