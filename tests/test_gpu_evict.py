@@ -131,7 +131,7 @@ def run_case(pages, lens, budget, first, last, in_place, weights=None, seed=0, r
     ([130], 500, 10, 10),                       # a budget above every length
 ])
 def test_evict(lens, budget, first, last, in_place):
-    run_case(48, lens, budget, first, last, in_place, seed=len(lens) + budget)
+    run_case(64, lens, budget, first, last, in_place, seed=len(lens) + budget)
 
 
 @pytest.mark.parametrize("in_place", [False, True])
@@ -221,7 +221,7 @@ def test_store_attend_weigh_evict_attend():
     """The operators as they are used together: a sequence is attended, its weights
     accumulated over two steps, evicted to a budget in place, and attended again;
     what the kept positions held is what is attended then."""
-    c = A.Cache(24, seed=12)
+    c = A.Cache(32, seed=12)
     try:
         pg = A.Paged(c, [900, 500], [1, 1], max_kv=900)
         w = torch.zeros(2, 900, device="cuda")
