@@ -472,13 +472,14 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(const AttendParams p) 
                 if (wrong && unit == 0 && threadIdx.x == 0) atomicAdd(p.invalid_count, (unsigned long long)__popcll(wrong));
                 masked = live != ~0ull;
             } else {
-                if (page < 0) {
-                    if (unit == 0 && threadIdx.x == 0) atomicAdd(p.invalid_count, 1ull);
-                    continue;
-                }
                 const uint32_t left = s.kv - t * 64u;
                 if (left < 64) live = (1ull << left) - 1;
                 masked = t * 64u + 64u > clear;
+                if (page < 0) {                          // page 0 was copied in its place
+                    if (unit == 0 && threadIdx.x == 0) atomicAdd(p.invalid_count, 1ull);
+                    live = 0;
+                    masked = true;
+                }
             }
             if (masked) clean_tile(tile, live);
 
