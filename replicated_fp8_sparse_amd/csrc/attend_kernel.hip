@@ -48,15 +48,17 @@ constexpr int kThreads = kWaves * 64;
 constexpr float kLn2 = 0.693147180559945309f;
 constexpr float kLazy = 8.0f;                    // rescale when a maximum grows past 2^8
 
-// LDS: the tile ring (after the last tile the waves' exchange area), each
-// wave's copies of slot lists (4 tiles deep).
+// LDS: the tile ring (after the last tile the waves' exchange area), the tiles'
+// scales by tile of 128 (a lane's 4 keys are then one read), each wave's copies of
+// slot lists (4 tiles deep).
 constexpr int kSlotRing = 4;
 struct Shared {
     alignas(16) uint8_t ring[131072];
+    alignas(16) float scales[kRing][4][64];
     alignas(16) int64_t slots[kWaves][kSlotRing][64];
     float stat[2][kWaves / 2][64];
-    uint64_t scan[kWaves];
-    uint64_t found[2];
+    uint32_t scan[kWaves];
+    uint32_t found[2];
 };
 static_assert(sizeof(Shared) <= 163840, "160 KB of LDS");
 
@@ -75,9 +77,11 @@ __device__ __forceinline__ void copy4_to_lds(const uint8_t* src, uint32_t lds) {
 }
 
 // Every wave's own copies of all but the newest tile have landed, then all waves'.
+// A tile is 41 copies of rows, wave, wave + 8, ..., and one of each tile's scales
+// by waves 1..4: 6 copies for waves 0..4 and 5 for the others.
 __device__ __forceinline__ void wait_tile(uint32_t wave, bool newer) {
     if (!newer) asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-    else if (wave == 0) asm volatile("s_waitcnt vmcnt(6) lgkmcnt(0)" ::: "memory");
+    else if (wave <= 4) asm volatile("s_waitcnt vmcnt(6) lgkmcnt(0)" ::: "memory");
     else asm volatile("s_waitcnt vmcnt(5) lgkmcnt(0)" ::: "memory");
     asm volatile("s_barrier" ::: "memory");
 }
@@ -106,43 +110,66 @@ __device__ __forceinline__ bf16x8 widen(int c0, int c1) {
     return bf16x8{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
 }
 
-__device__ __forceinline__ float tile_scale(const uint8_t* rows, uint32_t key, int j) {
-    return *(const float*)(rows + key * kRow + 512 + j * 4);
-}
-
-// Raw scores of 16 keys x 16 query rows (lane: query row l%16, keys 4*(l/16) + i).
-// rows: the 16 keys' LDS rows.
+// Raw scores of 32 keys x 16 query rows: x[u][r], keys u * 16 + 4 * (l/16) + i of
+// query row l%16.  rows: the keys' LDS rows; scales: the first one's in [tile][64].
+// The next tile's codes are read while the current one is in the matrix units.
 template <int R16>
-__device__ __forceinline__ void scores16(f32x4* s, const uint8_t* rows, const QFrag* q, uint32_t l16, uint32_t g) {
-    const uint8_t* mine = rows + l16 * kRow;
-    const bf16x8 r0 = *(const bf16x8*)(mine + 528 + g * 16);
-    const bf16x8 r1 = *(const bf16x8*)(mine + 592 + g * 16);
+__device__ __forceinline__ void scores32(f32x4 (*x)[R16], const uint8_t* rows, const float* scales, const QFrag* q,
+                                         uint32_t l16, uint32_t g) {
+    const uint8_t* mine = rows + l16 * kRow + g * 16;
+    const float* scale = scales + 4 * g;
+    bf16x8 rope[2][2];
+    i32x4 raw[2][2];
 #pragma unroll
-    for (int r = 0; r < R16; ++r) {
-        const f32x4 z = {0.f, 0.f, 0.f, 0.f};
-        s[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(r0, q[r].rope[0], z, 0, 0, 0);
-        s[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(r1, q[r].rope[1], s[r], 0, 0, 0);
+    for (int u = 0; u < 2; ++u) {
+        rope[u][0] = *(const bf16x8*)(mine + u * 16 * kRow + 528);
+        rope[u][1] = *(const bf16x8*)(mine + u * 16 * kRow + 592);
     }
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) raw[u][h] = *(const i32x4*)(mine + u * 16 * kRow + h * 64);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int r = 0; r < R16; ++r) {
+            const f32x4 z = {0.f, 0.f, 0.f, 0.f};
+            x[u][r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(rope[u][0], q[r].rope[0], z, 0, 0, 0);
+            x[u][r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(rope[u][1], q[r].rope[1], x[u][r], 0, 0, 0);
+        }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         __builtin_amdgcn_sched_barrier(0);
-        float a[4];                              // this lane's keys' scales
+        i32x4 next[2][2];
+        f32x4 a[2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) a[i] = tile_scale(rows, 4 * g + i, j);
-        bf16x8 k[4];
+        for (int u = 0; u < 2; ++u) {
+            a[u] = *(const f32x4*)(scale + j * 64 + u * 16);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const i32x4 v = *(const i32x4*)(mine + j * 128 + h * 64 + g * 16);
-            k[h * 2] = widen(v[0], v[1]);
-            k[h * 2 + 1] = widen(v[2], v[3]);
+            for (int h = 0; h < 2; ++h)
+                next[u][h] = j < 3 ? *(const i32x4*)(mine + u * 16 * kRow + (j + 1) * 128 + h * 64) : raw[u][h];
         }
+        f32x4 c[2][R16];
 #pragma unroll
-        for (int r = 0; r < R16; ++r) {
-            f32x4 c = {0.f, 0.f, 0.f, 0.f};
+        for (int h = 0; h < 4; ++h)
 #pragma unroll
-            for (int h = 0; h < 4; ++h) c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k[h], q[r].lat[j * 4 + h], c, 0, 0, 0);
+            for (int u = 0; u < 2; ++u) {
+                const bf16x8 k = widen(raw[u][h >> 1][(h & 1) * 2], raw[u][h >> 1][(h & 1) * 2 + 1]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s[r][i] = fmaf(c[i], a[i], s[r][i]);
+                for (int r = 0; r < R16; ++r) {
+                    const f32x4 z = {0.f, 0.f, 0.f, 0.f};
+                    c[u][r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, q[r].lat[j * 4 + h], h ? c[u][r] : z, 0, 0, 0);
+                }
+            }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+#pragma unroll
+            for (int r = 0; r < R16; ++r)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[u][r][i] = fmaf(c[u][r][i], a[u][i], x[u][r][i]);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) raw[u][h] = next[u][h];
         }
     }
 }
@@ -158,72 +185,124 @@ struct Seq {
     uint32_t tiles;      // 64-row tiles of each, at least 1
 };
 
-template <bool Slots>
-__device__ __forceinline__ Seq sequence(const AttendParams& p, uint32_t b, uint32_t M, bool empty) {
+// Arrays that no kernel of the call writes, read through the scalar cache where
+// the index is uniform: their waits then do not drain the tiles in flight.
+template <class T> using kptr = const __attribute__((address_space(4))) T*;
+__device__ __forceinline__ int32_t uniform_load(const int32_t* p, uint32_t i) { return ((kptr<int32_t>)p)[i]; }
+
+__device__ __forceinline__ Seq shape(const AttendParams& p, int32_t kv, int64_t q0, int64_t q1, uint32_t M, bool empty) {
     Seq s;
-    if (Slots) {
-        s.q0 = b;
-        s.n = 1;
-        s.kv = empty ? 0u : p.num_slots;
-    } else {
-        const int32_t kv = p.kv_len[b];
-        int64_t q0 = b, q1 = (int64_t)b + 1;
-        if (p.q_start) { q0 = p.q_start[b]; q1 = p.q_start[b + 1]; }
-        q0 = q0 < 0 ? 0 : q0;
-        q1 = q1 > (int64_t)p.num_tokens ? (int64_t)p.num_tokens : q1;
-        const int64_t n = q1 > q0 ? q1 - q0 : 0;
-        s.q0 = (uint32_t)q0;
-        s.n = (uint32_t)n;
-        s.kv = kv < 0 || empty ? 0u : ((uint32_t)kv > p.max_kv ? p.max_kv : (uint32_t)kv);
-    }
+    q0 = q0 < 0 ? 0 : q0;
+    q1 = q1 > (int64_t)p.num_tokens ? (int64_t)p.num_tokens : q1;
+    s.q0 = (uint32_t)q0;
+    s.n = q1 > q0 ? (uint32_t)(q1 - q0) : 0u;
+    s.kv = kv < 0 || empty ? 0u : ((uint32_t)kv > p.max_kv ? p.max_kv : (uint32_t)kv);
     const uint32_t m = s.n > p.max_q ? p.max_q : s.n;     // tokens beyond max_q_len are not computed
     s.units = (m * p.heads + M - 1) / M;
     s.tiles = s.kv ? (s.kv + 63) / 64 : 1u;
     return s;
 }
 
-// Prefix sums of the sequences' work by the block's threads: returns the
-// total; if `at` lies within, found[0..1] = (sequence, offset in it).  `line`
-// (may be null) receives the prefix of every sequence and the total.
-template <bool Slots>
-__device__ uint64_t walk(const AttendParams& p, uint32_t M, bool empty, uint64_t at, uint64_t* line, Shared& sh) {
-    const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = tid >> 6;
-    uint64_t carry = 0;
-    for (uint32_t b0 = 0; b0 < p.num_seqs; b0 += kThreads) {
-        const uint32_t b = b0 + tid;
-        uint64_t w = 0;
-        if (b < p.num_seqs) {
-            const Seq s = sequence<Slots>(p, b, M, empty);
-            w = (uint64_t)s.units * s.tiles;
-        }
-        uint64_t x = w;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const uint64_t y = __shfl_up(x, d);
-            if (lane >= (uint32_t)d) x += y;
-        }
-        __syncthreads();
-        if (lane == 63) sh.scan[wave] = x;
-        __syncthreads();
-        uint64_t before = carry, total = carry;
-        for (uint32_t v = 0; v < kWaves; ++v) {
-            if (v < wave) before += sh.scan[v];
-            total += sh.scan[v];
-        }
-        const uint64_t first = before + x - w;
-        if (b < p.num_seqs && line) line[b] = first;
-        if (w && at >= first && at < first + w) { sh.found[0] = b; sh.found[1] = at - first; }
-        carry = total;
+// Sequence b; Uniform: the same for the whole wave.
+template <bool Slots, bool Uniform>
+__device__ __forceinline__ Seq sequence(const AttendParams& p, uint32_t b, uint32_t M, bool empty) {
+    if (Slots) {
+        Seq s;
+        s.q0 = b;
+        s.n = 1;
+        s.kv = empty ? 0u : p.num_slots;
+        s.units = (p.heads + M - 1) / M;
+        s.tiles = s.kv ? (s.kv + 63) / 64 : 1u;
+        return s;
     }
-    __syncthreads();
-    return carry;
+    if (Uniform) {
+        const int32_t kv = uniform_load(p.kv_len, b);
+        if (!p.q_start) return shape(p, kv, b, (int64_t)b + 1, M, empty);
+        return shape(p, kv, uniform_load(p.q_start, b), uniform_load(p.q_start, b + 1), M, empty);
+    }
+    const int32_t kv = p.kv_len[b];
+    if (!p.q_start) return shape(p, kv, b, (int64_t)b + 1, M, empty);
+    return shape(p, kv, p.q_start[b], p.q_start[b + 1], M, empty);
 }
 
-// Tiles a block takes: an equal share, at least 2 (a shorter run costs more in
-// partial results than it gains).
-__device__ __forceinline__ uint64_t share(uint64_t total, uint32_t blocks) {
-    const uint64_t c = (total + blocks - 1) / blocks;
-    return c < 2 ? 2 : c;
+__device__ __forceinline__ uint32_t scan64(uint32_t x, uint32_t lane) {
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const uint32_t y = __shfl_up(x, d);
+        if (lane >= (uint32_t)d) x += y;
+    }
+    return x;
+}
+
+// Tiles a block takes: an equal share, at least `least` (a shorter run costs more
+// in partial results than it gains).
+__device__ __forceinline__ uint32_t share(const AttendParams& p, uint32_t total, uint32_t blocks) {
+    const uint32_t c = (total + blocks - 1) / blocks;
+    return c < p.least ? p.least : c;
+}
+
+struct Place {
+    uint32_t b, off;         // the sequence, and the tile within its work
+    uint32_t each, total;
+};
+
+// Where this block's run begins, from prefix sums of the sequences' work: by each
+// wave alone up to 64 sequences, else by the whole block.  Block 0 leaves the
+// prefixes and the share for combine_kernel.
+__device__ __forceinline__ Place place(const AttendParams& p, uint32_t M, bool empty, Shared& sh) {
+    const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = tid >> 6;
+    const bool first_block = blockIdx.x == 0;
+    Place r;
+    if (p.num_seqs <= 64) {
+        uint32_t w = 0;
+        if (lane < p.num_seqs) {
+            const Seq s = sequence<false, false>(p, lane, M, empty);
+            w = s.units * s.tiles;
+        }
+        const uint32_t x = p.num_seqs == 1 ? w : scan64(w, lane), first = x - w;
+        r.total = __builtin_amdgcn_readlane(x, p.num_seqs - 1);
+        r.each = share(p, r.total, gridDim.x);
+        const uint32_t at = r.each * blockIdx.x;
+        const uint64_t here = __ballot(w && at >= first && at < x);
+        r.b = here ? (uint32_t)__builtin_ctzll(here) : 0u;
+        r.off = at - __builtin_amdgcn_readlane(first, r.b);
+        if (first_block && tid < p.num_seqs) p.line[tid] = first;
+    } else {
+        uint32_t carry = 0, at = 0;
+        for (int pass = 0; pass < 2; ++pass) {       // the total, then the place
+            carry = 0;
+            for (uint32_t b0 = 0; b0 < p.num_seqs; b0 += kThreads) {
+                const uint32_t b = b0 + tid;
+                uint32_t w = 0;
+                if (b < p.num_seqs) {
+                    const Seq s = sequence<false, false>(p, b, M, empty);
+                    w = s.units * s.tiles;
+                }
+                const uint32_t x = scan64(w, lane);
+                __syncthreads();
+                if (lane == 63) sh.scan[wave] = x;
+                __syncthreads();
+                uint32_t before = carry;
+                for (uint32_t v = 0; v < kWaves; ++v) {
+                    if (v < wave) before += sh.scan[v];
+                    carry += sh.scan[v];
+                }
+                const uint32_t first = before + x - w;
+                if (pass == 0 && first_block && b < p.num_seqs) p.line[b] = first;
+                if (pass == 1 && w && at >= first && at < first + w) {
+                    sh.found[0] = b;
+                    sh.found[1] = at - first;
+                }
+            }
+            if (pass == 0) at = share(p, carry, gridDim.x) * blockIdx.x;
+        }
+        __syncthreads();
+        r.total = __builtin_amdgcn_readfirstlane(carry);
+        r.each = share(p, r.total, gridDim.x);
+        r.b = __builtin_amdgcn_readfirstlane(sh.found[0]);
+        r.off = __builtin_amdgcn_readfirstlane(sh.found[1]);
+    }
+    return r;
 }
 
 // ---- tiles -----------------------------------------------------------------------
@@ -240,7 +319,7 @@ struct Source {
     uint32_t wave, lane;
 
     __device__ __forceinline__ int64_t page(uint32_t t) const {   // -1: no such page
-        const int64_t g = table[t];
+        const int64_t g = uniform_load(table, t);
         return g >= 0 && g < capacity / 64 ? g : -1;
     }
     // Slots of tile t into this wave's copy (clamped to the list: always in bounds).
@@ -257,8 +336,10 @@ struct Source {
         const uint64_t v = good(s) ? (uint64_t)s : 0u;
         return (v >> 6) * p.main_page_stride + (v & 63u) * (uint64_t)kRow;
     }
-    // This wave's share of tile t into ring buffer `buf`: chunks wave, wave + 8, ...
-    __device__ __forceinline__ void fetch(uint32_t t, int64_t pg, uint32_t buf) const {
+    // This wave's share of tile t: chunks wave, wave + 8, ..., and a tile's scales.
+    __device__ __forceinline__ void fetch(uint32_t t, int64_t pg) const {
+        const uint32_t buf = lds_offset(sh.ring) + (t % kRing) * kTileBytes;
+        const uint32_t at = lds_offset(&sh.scales[t % kRing][0][0]) + (wave - 1) * 256u;
         if (Slots) {
             const int64_t* my = &sh.slots[wave][t % kSlotRing][0];
 #pragma unroll
@@ -268,14 +349,16 @@ struct Source {
                 const uint32_t x = c * 64u + lane, r = x / 41u, o = (x - r * 41u) * 16u;
                 copy16_to_lds(p.main_base + row_of(my[r]) + o, buf + c * 1024u);
             }
+            if (wave >= 1 && wave <= 4) copy4_to_lds(p.main_base + row_of(my[lane]) + 508u + wave * 4u, at);
         } else {
-            const uint8_t* base = p.main_base + (uint64_t)(pg < 0 ? 0 : pg) * p.main_page_stride + lane * 16u;
+            const uint8_t* page = p.main_base + (uint64_t)(pg < 0 ? 0 : pg) * p.main_page_stride;
+            const uint8_t* base = page + wave * 1024u + lane * 16u;
 #pragma unroll
             for (int i = 0; i < 6; ++i) {
-                const uint32_t c = wave + kWaves * i;
                 if (i == 5 && wave != 0) break;
-                copy16_to_lds(base + c * 1024u, buf + c * 1024u);
+                copy16_to_lds(base + i * (kWaves * 1024), buf + wave * 1024u + i * (kWaves * 1024));
             }
+            if (wave >= 1 && wave <= 4) copy4_to_lds(page + lane * kRow + 508u + wave * 4u, at);
         }
     }
 };
@@ -284,7 +367,7 @@ struct Source {
 // (bit clear in `live`) become zeros, and so do the codes of rows that hold a NaN
 // code or an infinite or NaN scale, with a NaN among their RoPE values for whoever
 // sees them; the others are not touched by it.  All threads; ends in a barrier.
-__device__ __forceinline__ void clean_tile(uint8_t* tile, uint64_t live) {
+__device__ __forceinline__ void clean_tile(uint8_t* tile, float* scales, uint64_t live) {
     const uint32_t key = threadIdx.x >> 3, j = threadIdx.x & 7u;     // 64 codes a thread
     uint8_t* row = tile + key * kRow;
     const bool gone = !((live >> key) & 1u);
@@ -296,7 +379,7 @@ __device__ __forceinline__ void clean_tile(uint8_t* tile, uint64_t live) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) nan |= ((((uint32_t)v[i] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0;
         }
-        if (j < 4) nan |= (*(const uint32_t*)(row + 512 + j * 4) & 0x7F800000u) == 0x7F800000u;
+        if (j < 4) nan |= (__float_as_uint(scales[j * 64 + key]) & 0x7F800000u) == 0x7F800000u;
     }
     const uint64_t who = __ballot(nan);
     const bool bad = ((who >> ((threadIdx.x & 63u) & ~7u)) & 255u) != 0;
@@ -304,23 +387,34 @@ __device__ __forceinline__ void clean_tile(uint8_t* tile, uint64_t live) {
         const i32x4 z = {0, 0, 0, 0};
 #pragma unroll
         for (int c = 0; c < 4; ++c) *(i32x4*)(row + j * 64 + c * 16) = z;
-        if (j < 4) *(float*)(row + 512 + j * 4) = 0.f;
+        if (j < 4) scales[j * 64 + key] = 0.f;
     }
     if (bad && j == 0) *(uint16_t*)(row + 528) = 0x7FC0;
     barrier();
 }
 
-// Sees of one query row: positions below `lim`, or drafted nodes by their bits.
+// What one query row sees: positions below `lim`, and drafted nodes by their bits.
 struct Sees {
     uint32_t lim;              // positions below lim are seen
     const uint64_t* tree;      // bits of the drafted positions from `base` on, or null
     int64_t base;
-    uint32_t kv, words;
-    __device__ __forceinline__ bool operator()(uint32_t pos) const {
-        if (pos < lim) return true;
-        if (!tree || pos >= kv) return false;
-        const uint64_t j = (uint64_t)((int64_t)pos - base);
-        return j < 64ull * words && ((tree[j >> 6] >> (j & 63u)) & 1u);
+    uint32_t words;
+    __device__ __forceinline__ uint64_t word(int64_t i) const { return i < (int64_t)words ? tree[i] : 0ull; }
+    // Bit k: position pos + k is seen (as far as it exists).
+    __device__ __forceinline__ uint64_t bits(uint32_t pos) const {
+        const uint32_t left = lim > pos ? lim - pos : 0u;
+        uint64_t m = left >= 64 ? ~0ull : (1ull << left) - 1;
+        if (tree) {
+            const int64_t j = (int64_t)pos - base;       // node of bit 0
+            if (j >= 0) {
+                const uint32_t s = (uint32_t)j & 63u;
+                m |= word(j >> 6) >> s;
+                m |= s ? word((j >> 6) + 1) << (64u - s) : 0ull;
+            } else if (j > -64) {
+                m |= word(0) << (uint32_t)-j;
+            }
+        }
+        return m;
     }
 };
 
@@ -330,7 +424,6 @@ __device__ __forceinline__ Sees sees(const AttendParams& p, const Seq& s, uint32
     Sees v;
     v.tree = nullptr;
     v.base = (int64_t)s.kv - s.n;
-    v.kv = s.kv;
     v.words = p.tree_words;
     int64_t lim = Slots ? (int64_t)s.kv : v.base + i + 1;
     if (!Slots && p.tree) {
@@ -357,40 +450,31 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(const AttendParams p) 
     const int64_t capacity = p.head->capacity;
     const bool empty = capacity <= 0;
 
-    uint64_t total;
+    Place at;
     if (Slots) {
-        const Seq s = sequence<true>(p, 0, M, empty);
-        total = (uint64_t)p.num_seqs * s.units * s.tiles;
+        const Seq s = sequence<true, true>(p, 0, M, empty);
+        const uint32_t w = s.units * s.tiles;
+        at.total = p.num_seqs * w;
+        at.each = share(p, at.total, gridDim.x);
+        at.b = at.each * blockIdx.x / w;
+        at.off = at.each * blockIdx.x - at.b * w;
     } else {
-        total = walk<false>(p, M, empty, ~0ull, blockIdx.x == 0 ? p.line : nullptr, sh);
+        at = place(p, M, empty, sh);
     }
-    const uint64_t each = share(total, gridDim.x);
-    if (blockIdx.x == 0 && threadIdx.x == 0) p.line[p.num_seqs] = each;
-    uint64_t pos = each * blockIdx.x;
-    const uint64_t end = pos + each < total ? pos + each : total;
-    if (pos >= end) return;
-    const uint64_t begin = pos;
-    uint32_t b;
-    uint64_t off;
-    if (Slots) {
-        const Seq s = sequence<true>(p, 0, M, empty);
-        const uint64_t w = (uint64_t)s.units * s.tiles;
-        b = (uint32_t)(pos / w);
-        off = pos - b * w;
-    } else {
-        walk<false>(p, M, empty, pos, nullptr, sh);
-        b = __builtin_amdgcn_readfirstlane((uint32_t)sh.found[0]);
-        off = __builtin_amdgcn_readfirstlane((uint32_t)sh.found[1]) |
-              ((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(sh.found[1] >> 32)) << 32);
-    }
+    at.b = __builtin_amdgcn_readfirstlane(at.b);      // the same for the block: keep what follows in scalar registers
+    at.off = __builtin_amdgcn_readfirstlane(at.off);
+    at.each = __builtin_amdgcn_readfirstlane(at.each);
+    at.total = __builtin_amdgcn_readfirstlane(at.total);
+    if (blockIdx.x == 0 && threadIdx.x == 0) p.line[p.num_seqs] = at.each;
+    const uint32_t begin = at.each * blockIdx.x;
+    const uint32_t end = begin + at.each < at.total ? begin + at.each : at.total;
+    uint32_t pos = begin, b = at.b, off = at.off;
 
     while (pos < end) {
-        const Seq s = sequence<Slots>(p, b, M, empty);
-        const uint64_t work = (uint64_t)s.units * s.tiles;
-        if (off >= work) { ++b; off = 0; continue; }     // pos < end <= total: a later sequence has work
-        const uint32_t unit = (uint32_t)(off / s.tiles);
-        uint32_t t0 = (uint32_t)(off - (uint64_t)unit * s.tiles);
-        const uint32_t t1 = (uint64_t)(s.tiles - t0) < end - pos ? s.tiles : t0 + (uint32_t)(end - pos);
+        const Seq s = sequence<Slots, true>(p, b, M, empty);
+        if (off >= s.units * s.tiles) { ++b; off = 0; continue; }     // pos < end <= total: a later sequence has work
+        const uint32_t unit = off / s.tiles, t0 = off - unit * s.tiles;
+        const uint32_t t1 = s.tiles - t0 < end - pos ? s.tiles : t0 + (end - pos);
         const bool whole = t0 == 0 && t1 == s.tiles;
         const uint32_t slot = 2u * blockIdx.x + (pos == begin ? 0u : 1u);
         pos += t1 - t0;
@@ -436,7 +520,6 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(const AttendParams p) 
 
         const Source<Slots> src{p, Slots ? nullptr : p.pages + (uint64_t)b * p.pages_stride,
                                 Slots ? p.slots + (uint64_t)b * p.slots_stride : nullptr, s.kv, capacity, sh, wave, lane};
-        const uint32_t ring = lds_offset(sh.ring);
         int64_t pg[3] = {-1, -1, -1};                    // pages of tiles t, t + 1, t + 2
         if (t0 < t_end) {
             if (Slots) {
@@ -448,18 +531,19 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(const AttendParams p) 
                 if (t0 + 1 < t_end) pg[1] = src.page(t0 + 1);
                 if (t0 + 2 < t_end) pg[2] = src.page(t0 + 2);
             }
-            src.fetch(t0, pg[0], ring + (t0 % kRing) * kTileBytes);
-            if (t0 + 1 < t_end) src.fetch(t0 + 1, pg[1], ring + ((t0 + 1) % kRing) * kTileBytes);
+            src.fetch(t0, pg[0]);
+            if (t0 + 1 < t_end) src.fetch(t0 + 1, pg[1]);
         }
         for (uint32_t t = t0; t < t_end; ++t) {
             wait_tile(wave, t + 1 < t_end);
             if (Slots && t + 3 < t_end) src.fetch_slots(t + 3);
-            if (t + 2 < t_end) src.fetch(t + 2, pg[2], ring + ((t + 2) % kRing) * kTileBytes);
+            if (t + 2 < t_end) src.fetch(t + 2, pg[2]);
             const int64_t page = pg[0];
             pg[0] = pg[1];
             pg[1] = pg[2];
             if (!Slots) pg[2] = t + 3 < t_end ? src.page(t + 3) : -1;
             uint8_t* tile = sh.ring + (t % kRing) * kTileBytes;
+            float* scales = &sh.scales[t % kRing][0][0];
 
             uint64_t live = ~0ull;
             bool masked;
@@ -481,15 +565,14 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(const AttendParams p) 
                     masked = true;
                 }
             }
-            if (masked) clean_tile(tile, live);
+            if (masked) clean_tile(tile, scales, live);
 
 #pragma unroll 1
             for (int half = 0; half < 2 / KW; ++half) {
                 const uint32_t k0 = (KW == 2 ? kw : (uint32_t)half) * 32u;
                 const uint8_t* rows32 = tile + k0 * kRow;
                 f32x4 x[2][R16];
-#pragma unroll
-                for (int u = 0; u < 2; ++u) scores16<R16>(x[u], rows32 + u * 16 * kRow, q, l16, g);
+                scores32<R16>(x, rows32, scales + k0, q, l16, g);
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -497,33 +580,22 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(const AttendParams p) 
                 if (masked) {
 #pragma unroll
                     for (int r = 0; r < R16; ++r) {
-                        uint32_t on = 0;                 // bit 4 u + i
-                        const Sees see = sees<Slots>(p, s, token[r]);
-#pragma unroll 1
-                        for (uint32_t c = 0; c < 8; ++c) {
-                            const uint32_t key = k0 + (c >> 2) * 16 + 4 * g + (c & 3u);
-                            const bool here = ((live >> key) & 1u) && (Slots || see(t * 64u + key));
-                            on |= here ? 1u << c : 0u;
-                        }
+                        uint64_t on = live;
+                        if (!Slots) on &= sees<Slots>(p, s, token[r]).bits(t * 64u);
+                        on >>= k0 + 4 * g;
 #pragma unroll
                         for (int u = 0; u < 2; ++u)
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                x[u][r][i] = (on >> (u * 4 + i)) & 1u ? x[u][r][i] : -INFINITY;
+                            for (int i = 0; i < 4; ++i) x[u][r][i] = (on >> (u * 16 + i)) & 1u ? x[u][r][i] : -INFINITY;
                     }
                 }
 #pragma unroll
                 for (int r = 0; r < R16; ++r) {
-                    float top = -INFINITY;
-#pragma unroll
-                    for (int u = 0; u < 2; ++u)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            top = fmaxf(top, x[u][r][i]);
-                        }
-                    top = fmaxf(top, __shfl_xor(top, 16));
-                    top = fmaxf(top, __shfl_xor(top, 32));
+                    float top = fmaxf(fmaxf(fmaxf(x[0][r][0], x[0][r][1]), fmaxf(x[0][r][2], x[0][r][3])),
+                                      fmaxf(fmaxf(x[1][r][0], x[1][r][1]), fmaxf(x[1][r][2], x[1][r][3])));
                     if (__any(top > mx[r] + kLazy || (mx[r] == -INFINITY && top > mx[r]))) {
+                        top = fmaxf(top, __shfl_xor(top, 16));
+                        top = fmaxf(top, __shfl_xor(top, 32));
                         const float next = fmaxf(mx[r], top);
                         const float keep = mx[r] == -INFINITY ? 0.f : exp2f(mx[r] - next);
                         mx[r] = next;
@@ -547,29 +619,38 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(const AttendParams p) 
                 }
                 // values: 8 keys of this lane group (4 of each 16) x 16 columns
                 const uint32_t vk = (l16 >> 1) < 4 ? 4 * g + (l16 >> 1) : 12 + 4 * g + (l16 >> 1);
-                const uint8_t* vrow = rows32 + vk * kRow + (l16 & 1u) * 8u;
+                const uint8_t* vrow = rows32 + vk * kRow + (l16 & 1u) * 8u + dw * NB * 16;
+                const float* scale = scales + k0 + 4 * g;
+                constexpr int G = 4;                     // columns blocks read ahead
+                i32x2 c[G];
 #pragma unroll
-                for (int j = 0; j < NB / 8 || j == 0; ++j) {
+                for (int d = 0; d < G; ++d) c[d] = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lptr<i32x2>)(vrow + d * 16));
+                bf16x8 w[R16];
+#pragma unroll
+                for (int d0 = 0; d0 < NB; d0 += G) {
                     __builtin_amdgcn_sched_barrier(0);
-                    const int tj = NB >= 8 ? (int)dw * (NB / 8) + j : (int)(dw * NB / 8);    // the scale's tile
-                    bf16x8 w[R16];
+                    i32x2 next[G];
 #pragma unroll
-                    for (int u = 0; u < 2; ++u)
+                    for (int d = 0; d < G; ++d)
+                        next[d] = d0 + G < NB ? __builtin_amdgcn_ds_read_tr8_b64_v2i32((lptr<i32x2>)(vrow + (d0 + G + d) * 16)) : c[d];
+                    if (d0 % 8 == 0) {                   // a tile of 128 values: its scales
+                        const uint32_t tj = (dw * NB + d0) / 8;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float a = tile_scale(rows32, u * 16 + 4 * g + i, tj);
+                        for (int u = 0; u < 2; ++u) {
+                            const f32x4 a = *(const f32x4*)(scale + tj * 64 + u * 16);
 #pragma unroll
-                            for (int r = 0; r < R16; ++r) w[r][u * 4 + i] = (__bf16)(x[u][r][i] * a);
+                            for (int r = 0; r < R16; ++r)
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) w[r][u * 4 + i] = (__bf16)(x[u][r][i] * a[i]);
                         }
+                    }
 #pragma unroll
-                    for (int d = 0; d < (NB < 8 ? NB : 8); ++d) {
-                        if (d % 4 == 0) __builtin_amdgcn_sched_barrier(0);
-                        const uint32_t col = (dw * NB + j * 8 + d) * 16u;
-                        const i32x2 c = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lptr<i32x2>)(vrow + col));
-                        const bf16x8 v = widen(c.x, c.y);
+                    for (int d = 0; d < G; ++d) {
+                        const bf16x8 v = widen(c[d].x, c[d].y);
 #pragma unroll
                         for (int r = 0; r < R16; ++r)
-                            o[r][j * 8 + d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, w[r], o[r][j * 8 + d], 0, 0, 0);
+                            o[r][d0 + d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, w[r], o[r][d0 + d], 0, 0, 0);
+                        c[d] = next[d];
                     }
                 }
             }
@@ -637,30 +718,30 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(const AttendParams p) 
 // blocks' parts in order.
 template <bool Slots>
 __global__ __launch_bounds__(256) void combine_kernel(const AttendParams p, uint32_t M) {
-    const uint64_t each = p.line[p.num_seqs];
+    const uint32_t each = p.line[p.num_seqs];
     const bool empty = p.head->capacity <= 0;
     const uint32_t col = (threadIdx.x & 127u) * 4u;
     const uint64_t per = (uint64_t)p.max_q * p.heads, all = per * p.num_seqs;
     for (uint64_t x = (uint64_t)blockIdx.x * 2 + (threadIdx.x >> 7); x < all; x += (uint64_t)gridDim.x * 2) {
         const uint32_t b = (uint32_t)(x / per), row = (uint32_t)(x - b * per);
-        const Seq s = sequence<Slots>(p, b, M, empty);
+        const Seq s = sequence<Slots, false>(p, b, M, empty);
         const uint32_t m = s.n > p.max_q ? p.max_q : s.n;
         if (row >= m * p.heads) continue;
         const uint32_t unit = row / M;
-        const uint64_t first = (Slots ? (uint64_t)b * s.units * s.tiles : p.line[b]) + (uint64_t)unit * s.tiles;
-        const uint64_t w0 = first / each, w1 = (first + s.tiles - 1) / each;
+        const uint32_t first = (Slots ? b * s.units * s.tiles : p.line[b]) + unit * s.tiles;
+        const uint32_t w0 = first / each, w1 = (first + s.tiles - 1) / each;
         if (w0 == w1) continue;
         const uint32_t in = row - unit * M;
         float top = -INFINITY;
-        for (uint64_t w = w0; w <= w1; ++w) {
-            const uint64_t at = (2 * w + (w == w0 && first != w0 * each ? 1 : 0)) * M + in;
+        for (uint32_t w = w0; w <= w1; ++w) {
+            const uint64_t at = (uint64_t)(2 * w + (w == w0 && first != w0 * each ? 1 : 0)) * M + in;
             top = fmaxf(top, p.part_lse[at]);
         }
         const float ref = top == -INFINITY ? 0.f : top;
         float total = 0.f;
         f32x4 o = {0.f, 0.f, 0.f, 0.f};
-        for (uint64_t w = w0; w <= w1; ++w) {
-            const uint64_t at = (2 * w + (w == w0 && first != w0 * each ? 1 : 0)) * M + in;
+        for (uint32_t w = w0; w <= w1; ++w) {
+            const uint64_t at = (uint64_t)(2 * w + (w == w0 && first != w0 * each ? 1 : 0)) * M + in;
             const float k = exp2f(p.part_lse[at] - ref);
             const f32x4 v = *(const f32x4*)(p.part + at * 512 + col);
             total += k;
@@ -685,6 +766,7 @@ constexpr uint32_t kWeightTiles = 16;
 
 struct WeightShared {
     alignas(16) uint8_t ring[kRing * kTileBytes];
+    alignas(16) float scales[kRing][4][64];
     float sums[kWaves][kWeightTiles * 64];
 };
 
@@ -702,7 +784,7 @@ __global__ __launch_bounds__(kThreads) void weights_kernel(const AttendParams p,
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t b = p.first_seq + blockIdx.y, t0 = blockIdx.x * run;
     const int64_t capacity = p.head->capacity;
-    const Seq s = sequence<false>(p, b, 128, capacity <= 0);
+    const Seq s = sequence<false, true>(p, b, 128, capacity <= 0);
     const uint32_t tiles = s.kv ? s.tiles : 0u;
     const uint32_t t1 = t0 + run < tiles ? t0 + run : tiles;
     const uint32_t m = s.n > p.max_q ? p.max_q : s.n, rows = m * p.heads;
@@ -712,18 +794,19 @@ __global__ __launch_bounds__(kThreads) void weights_kernel(const AttendParams p,
     const uint32_t clear = base < 0 ? 0u : (uint32_t)(p.tree ? base : base + 1);   // every token sees those
     const uint32_t ring = lds_offset(sh.ring);
     auto page = [&](uint32_t t) -> int64_t {
-        const int64_t v = t < t1 ? table[t] : -1;
+        const int64_t v = t < t1 ? uniform_load(table, t) : -1;
         return v >= 0 && v < capacity / 64 ? v : -1;
     };
     auto fetch = [&](uint32_t t, int64_t pg) {
-        const uint8_t* from = p.main_base + (uint64_t)(pg < 0 ? 0 : pg) * p.main_page_stride + lane * 16u;
-        const uint32_t to = ring + (t % kRing) * kTileBytes;
+        const uint8_t* page = p.main_base + (uint64_t)(pg < 0 ? 0 : pg) * p.main_page_stride;
+        const uint32_t to = ring + (t % kRing) * kTileBytes + wave * 1024u;
 #pragma unroll
         for (int i = 0; i < 6; ++i) {
-            const uint32_t c = wave + kWaves * i;
             if (i == 5 && wave != 0) break;
-            copy16_to_lds(from + c * 1024u, to + c * 1024u);
+            copy16_to_lds(page + wave * 1024u + lane * 16u + i * (kWaves * 1024), to + i * (kWaves * 1024));
         }
+        if (wave >= 1 && wave <= 4)
+            copy4_to_lds(page + lane * kRow + 508u + wave * 4u, lds_offset(&sh.scales[t % kRing][0][0]) + (wave - 1) * 256u);
     };
 
     for (uint32_t row0 = 0; row0 < rows && t0 < t1; row0 += 128) {
@@ -756,29 +839,33 @@ __global__ __launch_bounds__(kThreads) void weights_kernel(const AttendParams p,
             const uint32_t left = s.kv - x * 64u;
             const uint64_t live = left < 64 ? (1ull << left) - 1 : ~0ull;
             const bool masked = x * 64u + 64u > clear;
-            if (masked) clean_tile(tile, live);
+            float* scales = &sh.scales[x % kRing][0][0];
+            uint64_t on = ~0ull;
+            if (masked) {
+                on = live & sees<false>(p, s, i).bits(x * 64u);
+                clean_tile(tile, scales, live);
+            }
 #pragma unroll 1
-            for (uint32_t u = 0; u < 4; ++u) {
-                f32x4 v[1];
-                scores16<1>(v, tile + u * 16 * kRow, q, l16, g);
-                v[0] *= p.scale_log2;
-                if (masked) {
-                    const Sees see = sees<false>(p, s, i);
+            for (uint32_t half = 0; half < 2; ++half) {
+                f32x4 v[2][1];
+                scores32<1>(v, tile + half * 32 * kRow, scales + half * 32, q, l16, g);
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    v[u][0] *= p.scale_log2;
+                    if (masked) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            v[u][0][k] = (on >> (half * 32 + u * 16 + 4 * g + k)) & 1u ? v[u][0][k] : -INFINITY;
+                    }
+                    float keep = 0.f;
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const uint32_t key = u * 16 + 4 * g + k;
-                        const bool on = ((live >> key) & 1u) && see(x * 64u + key);
-                        v[0][k] = on ? v[0][k] : -INFINITY;
+                        const float w = adds ? __builtin_amdgcn_exp2f(v[u][0][k] - lse2) : 0.f;
+                        const float total = sum16(w);
+                        keep = (int)l16 == k ? total : keep;
                     }
+                    if (l16 < 4) sh.sums[wave][(x - t0) * 64 + half * 32 + u * 16 + 4 * g + l16] += keep;
                 }
-                float keep = 0.f;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float w = adds ? __builtin_amdgcn_exp2f(v[0][k] - lse2) : 0.f;
-                    const float total = sum16(w);
-                    keep = (int)l16 == k ? total : keep;
-                }
-                if (l16 < 4) sh.sums[wave][(x - t0) * 64 + u * 16 + 4 * g + l16] += keep;
             }
         }
     }
@@ -813,15 +900,19 @@ hipError_t launch_shape(const AttendParams& p, uint32_t blocks, hipStream_t stre
 
 }  // namespace
 
-AttendPlan plan_attend(uint64_t rows, uint64_t num_seqs, uint64_t max_kv) {
+AttendPlan plan_attend(uint64_t rows, uint64_t num_seqs, uint64_t num_tokens, uint64_t heads, uint64_t max_kv) {
     AttendPlan a;
     a.rows = rows <= 16 ? 16u : rows <= 32 ? 32u : rows <= 64 ? 64u : 128u;
-    const uint64_t units = num_seqs * ((rows + a.rows - 1) / a.rows);
+    uint64_t units = num_seqs * ((rows + a.rows - 1) / a.rows);
+    const uint64_t by_tokens = num_tokens * heads / a.rows + num_seqs;      // ragged: no more units than that
+    units = units < by_tokens ? units : by_tokens;
     const uint64_t tiles = max_kv ? (max_kv + 63) / 64 : 1;
-    // one block a CU; never more than the line has runs of two tiles
-    const uint64_t runs = units * ((tiles + 1) / 2) + 1;
+    a.fits = units * tiles < (1ull << 31);
+    // one block a CU; never more than the line has runs
+    a.least = 2;
+    const uint64_t runs = units * ((tiles + a.least - 1) / a.least) + 1;
     a.blocks = (uint32_t)(units >= 256 || runs >= 256 ? 256 : runs);
-    a.line_bytes = ((num_seqs + 1) * 8 + 255) / 256 * 256;
+    a.line_bytes = ((num_seqs + 1) * 4 + 255) / 256 * 256;
     a.lse_bytes = (uint64_t)a.blocks * 2 * a.rows * 4;
     a.bytes = a.line_bytes + a.lse_bytes + (uint64_t)a.blocks * 2 * a.rows * 512 * 4;
     return a;
@@ -829,9 +920,11 @@ AttendPlan plan_attend(uint64_t rows, uint64_t num_seqs, uint64_t max_kv) {
 
 hipError_t launch_attend(const AttendParams& given, void* workspace, hipStream_t stream) {
     AttendParams p = given;
-    const AttendPlan a = plan_attend((uint64_t)p.max_q * p.heads, p.num_seqs, p.by_slots ? p.num_slots : p.max_kv);
+    const AttendPlan a = plan_attend((uint64_t)p.max_q * p.heads, p.num_seqs, p.num_tokens, p.heads,
+                                     p.by_slots ? p.num_slots : p.max_kv);
+    p.least = a.least;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    p.line = reinterpret_cast<uint64_t*>(ws);
+    p.line = reinterpret_cast<uint32_t*>(ws);
     p.part_lse = reinterpret_cast<float*>(ws + a.line_bytes);
     p.part = reinterpret_cast<float*>(ws + a.line_bytes + a.lse_bytes);
     switch (a.rows) {

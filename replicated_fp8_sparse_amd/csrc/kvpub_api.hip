@@ -346,8 +346,13 @@ void set_pages(kvpub::AttendParams& a, const kvpub_pages* g) {
     a.tree_words = g->tree_words;
 }
 
-uint64_t query_rows(const kvpub_queries* q, const kvpub_pages* g) {
-    return (uint64_t)std::min<int64_t>(g->q_start ? g->max_q_len : 1, q->num_tokens) * q->num_heads;
+kvpub::AttendPlan page_plan(const kvpub_queries* q, const kvpub_pages* g) {
+    const uint64_t tokens = (uint64_t)std::min<int64_t>(g->q_start ? g->max_q_len : 1, q->num_tokens);
+    return kvpub::plan_attend(tokens * q->num_heads, g->num_seqs, q->num_tokens, q->num_heads, g->max_kv_len);
+}
+
+kvpub::AttendPlan slot_plan(const kvpub_queries* q, uint32_t num_slots) {
+    return kvpub::plan_attend(q->num_heads, q->num_tokens, q->num_tokens, q->num_heads, num_slots);
 }
 
 }  // namespace
@@ -623,12 +628,12 @@ KVPUB_API kvpub_status kvpub_gather(kvpub_ctx* ctx, uint32_t replica, uint32_t l
 
 KVPUB_API uint64_t kvpub_attend_workspace(const kvpub_queries* q, const kvpub_pages* pages) {
     if (!good_queries(q) || !good_pages(pages) || q->num_tokens == 0 || pages->num_seqs == 0) return 0;
-    return kvpub::plan_attend(query_rows(q, pages), pages->num_seqs, pages->max_kv_len).bytes;
+    return page_plan(q, pages).bytes;
 }
 
 KVPUB_API uint64_t kvpub_attend_slots_workspace(const kvpub_queries* q, uint32_t num_slots) {
     if (!good_queries(q) || num_slots > (1u << 24) || q->num_tokens == 0) return 0;
-    return kvpub::plan_attend(q->num_heads, q->num_tokens, num_slots).bytes;
+    return slot_plan(q, num_slots).bytes;
 }
 
 KVPUB_API kvpub_status kvpub_attend(kvpub_ctx* ctx, uint32_t replica, uint32_t layer, const kvpub_queries* q,
@@ -642,6 +647,7 @@ KVPUB_API kvpub_status kvpub_attend(kvpub_ctx* ctx, uint32_t replica, uint32_t l
     if (!good_output(out, out_token_stride, out_head_stride, KVPUB_LATENT_DIM, q->num_heads, q->num_tokens) ||
         !good_lse(lse, lse_token_stride, q->num_heads, q->num_tokens))
         return KVPUB_ERR_INVALID_ARG;
+    if (!page_plan(q, pages).fits) return KVPUB_ERR_INVALID_ARG;
     if (!workspace || !aligned(workspace, 16) || workspace_bytes < kvpub_attend_workspace(q, pages))
         return KVPUB_ERR_INVALID_ARG;
     DeviceGuard guard(ctx->cfg.device);
@@ -671,6 +677,7 @@ KVPUB_API kvpub_status kvpub_attend_slots(kvpub_ctx* ctx, uint32_t replica, uint
     if (!good_output(out, out_token_stride, out_head_stride, KVPUB_LATENT_DIM, q->num_heads, q->num_tokens) ||
         !good_lse(lse, lse_token_stride, q->num_heads, q->num_tokens))
         return KVPUB_ERR_INVALID_ARG;
+    if (!slot_plan(q, num_slots).fits) return KVPUB_ERR_INVALID_ARG;
     if (!workspace || !aligned(workspace, 16) || workspace_bytes < kvpub_attend_slots_workspace(q, num_slots))
         return KVPUB_ERR_INVALID_ARG;
     DeviceGuard guard(ctx->cfg.device);

@@ -118,7 +118,8 @@ struct AttendParams {
     float* weights_out;
     int64_t weights_stride;
     uint32_t first_seq;          // weights only: sequence of the grid's first row
-    uint64_t* line;              // workspace: prefix of each sequence's work, then the blocks' share
+    uint32_t least;              // fewest tiles of a block
+    uint32_t* line;              // workspace: prefix of each sequence's work, then the blocks' share
     float* part_lse;             // workspace: [blocks * 2][rows]
     float* part;                 // workspace: [blocks * 2][rows][512]
 };
@@ -127,12 +128,14 @@ struct AttendParams {
 struct AttendPlan {
     uint32_t rows;
     uint32_t blocks;
+    uint32_t least;
+    bool fits;                   // fewer than 2^31 tiles in all
     uint64_t line_bytes;
     uint64_t lse_bytes;
     uint64_t bytes;
 };
 // rows: the most (token, head) rows of one sequence.
-AttendPlan plan_attend(uint64_t rows, uint64_t num_seqs, uint64_t max_kv);
+AttendPlan plan_attend(uint64_t rows, uint64_t num_seqs, uint64_t num_tokens, uint64_t heads, uint64_t max_kv);
 // Enqueue latent attention on `stream`; returns the launch status.
 hipError_t launch_attend(const AttendParams& p, void* workspace, hipStream_t stream);
 hipError_t launch_attend_weights(const AttendParams& p, hipStream_t stream);
