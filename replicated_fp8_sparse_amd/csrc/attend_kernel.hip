@@ -48,17 +48,16 @@ constexpr int kThreads = kWaves * 64;
 constexpr float kLn2 = 0.693147180559945309f;
 constexpr float kLazy = 8.0f;                    // rescale when a maximum grows past 2^8
 
-// LDS: the tile ring (after the last tile the waves' exchange area), the tiles'
-// scales by tile of 128 (a lane's 4 keys are then one read), each wave's copies of
-// slot lists (4 tiles deep).
+// LDS: the tile ring and the waves' exchange of partial scores (after the last
+// tile both hold the join of key halves), the tiles' scales by tile of 128, slot
+// lists 4 tiles deep.  160 KB in all.
 constexpr int kSlotRing = 4;
+constexpr int kExchange = 32768;
 struct Shared {
-    alignas(16) uint8_t ring[131072];
+    alignas(16) uint8_t ring[kRing * kTileBytes];
+    alignas(16) uint8_t exchange[kExchange];
     alignas(16) float scales[kRing][4][64];
-    alignas(16) int64_t slots[kWaves][kSlotRing][64];
-    float stat[2][kWaves / 2][64];
-    uint32_t scan[kWaves];
-    uint32_t found[2];
+    alignas(16) int64_t slots[kSlotRing][64];
 };
 static_assert(sizeof(Shared) <= 163840, "160 KB of LDS");
 
@@ -87,19 +86,20 @@ __device__ __forceinline__ void wait_tile(uint32_t wave, bool newer) {
 }
 __device__ __forceinline__ void barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
-// One 16-row group of queries as operands: lane (l%16, l/16) = (row, 16 values of
-// each 64: the first 8 go with one matrix instruction, the others with the next).
+// One 16-row group of queries as operands, T tiles of 128 and P of the two RoPE
+// halves: lane (l%16, l/16) = (row, 16 of each 64 values: the first 8 go with one
+// matrix instruction, the others with the next), and 8 of each 32 RoPE values.
+template <int T, int P>
 struct QFrag {
-    bf16x8 lat[16];
-    bf16x8 rope[2];
+    bf16x8 lat[4 * T];
+    bf16x8 rope[P];
+    __device__ __forceinline__ void load(const uint16_t* latent, const uint16_t* rp, uint32_t g) {
+#pragma unroll
+        for (int c = 0; c < 4 * T; ++c) lat[c] = *(const bf16x8*)(latent + (c >> 1) * 64 + g * 16 + (c & 1) * 8);
+#pragma unroll
+        for (int c = 0; c < P; ++c) rope[c] = *(const bf16x8*)(rp + c * 32 + g * 8);
+    }
 };
-
-__device__ __forceinline__ void load_query(QFrag& f, const uint16_t* lat, const uint16_t* rope, uint32_t g) {
-#pragma unroll
-    for (int c = 0; c < 16; ++c) f.lat[c] = *(const bf16x8*)(lat + (c >> 1) * 64 + g * 16 + (c & 1) * 8);
-#pragma unroll
-    for (int c = 0; c < 2; ++c) f.rope[c] = *(const bf16x8*)(rope + c * 32 + g * 8);
-}
 
 // 8 codes as bf16 (exact).
 __device__ __forceinline__ bf16x8 widen(int c0, int c1) {
@@ -110,66 +110,87 @@ __device__ __forceinline__ bf16x8 widen(int c0, int c1) {
     return bf16x8{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
 }
 
-// Raw scores of 32 keys x 16 query rows: x[u][r], keys u * 16 + 4 * (l/16) + i of
-// query row l%16.  rows: the keys' LDS rows; scales: the first one's in [tile][64].
-// The next tile's codes are read while the current one is in the matrix units.
-template <int R16>
-__device__ __forceinline__ void scores32(f32x4 (*x)[R16], const uint8_t* rows, const float* scales, const QFrag* q,
-                                         uint32_t l16, uint32_t g) {
-    const uint8_t* mine = rows + l16 * kRow + g * 16;
-    const float* scale = scales + 4 * g;
-    bf16x8 rope[2][2];
-    i32x4 raw[2][2];
+// The 32 keys of a step in the order of the matrix units: row m of half u is key
+// u * 16 + (m ^ 8 u).  The 8 keys that a lane group's column read takes (4 of each
+// half) and its neighbour group's then fall on distinct LDS banks, as rows 16 apart
+// do not.
+__device__ __forceinline__ uint32_t key_of(uint32_t u, uint32_t g) { return u * 16 + 4 * (u ? g ^ 2 : g); }   // of lane group g: + 0..3
+
+// Value i of this lane's quad: scales are read one a lane and spread by the
+// multiply itself, a quarter of the LDS time of reading 4 a lane.
+template <int I>
+__device__ __forceinline__ float quad(float v) {
+    return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), I | (I << 2) | (I << 4) | (I << 6), 15, 15, true));
+}
+__device__ __forceinline__ f32x4 quads(float v) { return f32x4{quad<0>(v), quad<1>(v), quad<2>(v), quad<3>(v)}; }
+
+// Scores times `scale` of 32 keys x 16 query rows over T tiles of 128 (and the
+// RoPE halves of q, if `ropes`): x[u][r], keys key_of(u, l/16) + i of query row
+// l%16.  rows: the keys' LDS rows from the first tile's codes on; rope: its RoPE
+// values; scales: the first key's in [tile][64].  The codes of the next two matrix
+// steps are read while the last two are in the matrix units.
+template <int R16, int T, int P>
+__device__ __forceinline__ void scores32(f32x4 (*x)[R16], const uint8_t* rows, const uint8_t* rope, const float* scales,
+                                         const QFrag<T, P>* q, float scale, bool ropes, uint32_t l16, uint32_t g) {
+    const uint32_t at[2] = {l16 * kRow + g * 16, (16 + (l16 ^ 8)) * kRow + g * 16};
+    const float* sc[2] = {scales + key_of(0, g) + (l16 & 3), scales + key_of(1, g) + (l16 & 3)};
+    i32x4 raw[2];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-        rope[u][0] = *(const bf16x8*)(mine + u * 16 * kRow + 528);
-        rope[u][1] = *(const bf16x8*)(mine + u * 16 * kRow + 592);
+    for (int u = 0; u < 2; ++u) raw[u] = *(const i32x4*)(rows + at[u]);
+    if (ropes) {
+        bf16x8 k[2][P];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int h = 0; h < P; ++h) k[u][h] = *(const bf16x8*)(rope + at[u] + h * 64);
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int r = 0; r < R16; ++r) {
+                f32x4 c = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int h = 0; h < P; ++h) c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k[u][h], q[r].rope[h], c, 0, 0, 0);
+                x[u][r] = c * scale;
+            }
+    } else {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int r = 0; r < R16; ++r) x[u][r] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) raw[u][h] = *(const i32x4*)(mine + u * 16 * kRow + h * 64);
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int r = 0; r < R16; ++r) {
-            const f32x4 z = {0.f, 0.f, 0.f, 0.f};
-            x[u][r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(rope[u][0], q[r].rope[0], z, 0, 0, 0);
-            x[u][r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(rope[u][1], q[r].rope[1], x[u][r], 0, 0, 0);
-        }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        __builtin_amdgcn_sched_barrier(0);
-        i32x4 next[2][2];
-        f32x4 a[2];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            a[u] = *(const f32x4*)(scale + j * 64 + u * 16);
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                next[u][h] = j < 3 ? *(const i32x4*)(mine + u * 16 * kRow + (j + 1) * 128 + h * 64) : raw[u][h];
-        }
+    for (int j = 0; j < T; ++j) {
         f32x4 c[2][R16];
+        float a[2];
 #pragma unroll
-        for (int h = 0; h < 4; ++h)
+        for (int u = 0; u < 2; ++u) a[u] = sc[u][j * 64];
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const bf16x8 k = widen(raw[u][h >> 1][(h & 1) * 2], raw[u][h >> 1][(h & 1) * 2 + 1]);
+        for (int h = 0; h < 2; ++h) {
+            __builtin_amdgcn_sched_barrier(0);
+            i32x4 next[2];
 #pragma unroll
-                for (int r = 0; r < R16; ++r) {
-                    const f32x4 z = {0.f, 0.f, 0.f, 0.f};
-                    c[u][r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, q[r].lat[j * 4 + h], h ? c[u][r] : z, 0, 0, 0);
+            for (int u = 0; u < 2; ++u) next[u] = j * 2 + h + 1 < 2 * T ? *(const i32x4*)(rows + at[u] + (j * 2 + h + 1) * 64) : raw[u];
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const bf16x8 w = widen(raw[u][k * 2], raw[u][k * 2 + 1]);
+#pragma unroll
+                    for (int r = 0; r < R16; ++r) {
+                        const f32x4 z = {0.f, 0.f, 0.f, 0.f};
+                        c[u][r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, q[r].lat[j * 4 + h * 2 + k], h + k ? c[u][r] : z, 0, 0, 0);
+                    }
                 }
-            }
+#pragma unroll
+            for (int u = 0; u < 2; ++u) raw[u] = next[u];
+        }
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
+            const f32x4 s = quads(a[u] * scale);
 #pragma unroll
             for (int r = 0; r < R16; ++r)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) x[u][r][i] = fmaf(c[u][r][i], a[u][i], x[u][r][i]);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) raw[u][h] = next[u][h];
+                for (int i = 0; i < 4; ++i) x[u][r][i] = fmaf(s[i], c[u][r][i], x[u][r][i]);
         }
     }
 }
@@ -268,6 +289,7 @@ __device__ __forceinline__ Place place(const AttendParams& p, uint32_t M, bool e
         r.off = at - __builtin_amdgcn_readlane(first, r.b);
         if (first_block && tid < p.num_seqs) p.line[tid] = first;
     } else {
+        uint32_t* scan = (uint32_t*)sh.exchange;
         uint32_t carry = 0, at = 0;
         for (int pass = 0; pass < 2; ++pass) {       // the total, then the place
             carry = 0;
@@ -280,18 +302,18 @@ __device__ __forceinline__ Place place(const AttendParams& p, uint32_t M, bool e
                 }
                 const uint32_t x = scan64(w, lane);
                 __syncthreads();
-                if (lane == 63) sh.scan[wave] = x;
+                if (lane == 63) scan[wave] = x;
                 __syncthreads();
                 uint32_t before = carry;
                 for (uint32_t v = 0; v < kWaves; ++v) {
-                    if (v < wave) before += sh.scan[v];
-                    carry += sh.scan[v];
+                    if (v < wave) before += scan[v];
+                    carry += scan[v];
                 }
                 const uint32_t first = before + x - w;
                 if (pass == 0 && first_block && b < p.num_seqs) p.line[b] = first;
                 if (pass == 1 && w && at >= first && at < first + w) {
-                    sh.found[0] = b;
-                    sh.found[1] = at - first;
+                    scan[kWaves] = b;
+                    scan[kWaves + 1] = at - first;
                 }
             }
             if (pass == 0) at = share(p, carry, gridDim.x) * blockIdx.x;
@@ -299,8 +321,9 @@ __device__ __forceinline__ Place place(const AttendParams& p, uint32_t M, bool e
         __syncthreads();
         r.total = __builtin_amdgcn_readfirstlane(carry);
         r.each = share(p, r.total, gridDim.x);
-        r.b = __builtin_amdgcn_readfirstlane(sh.found[0]);
-        r.off = __builtin_amdgcn_readfirstlane(sh.found[1]);
+        r.b = __builtin_amdgcn_readfirstlane(scan[kWaves]);
+        r.off = __builtin_amdgcn_readfirstlane(scan[kWaves + 1]);
+        __syncthreads();
     }
     return r;
 }
@@ -322,11 +345,12 @@ struct Source {
         const int64_t g = uniform_load(table, t);
         return g >= 0 && g < capacity / 64 ? g : -1;
     }
-    // Slots of tile t into this wave's copy (clamped to the list: always in bounds).
+    // Slots of tile t (clamped to the list: always in bounds); by wave 5.
     __device__ __forceinline__ void fetch_slots(uint32_t t) const {
+        if (wave != 5) return;
         const uint32_t last = 2u * kv - 1u;
         uint32_t i = t * 128u + lane;
-        const uint32_t at = lds_offset(&sh.slots[wave][t % kSlotRing][0]);
+        const uint32_t at = lds_offset(&sh.slots[t % kSlotRing][0]);
         copy4_to_lds((const uint8_t*)list + 4ull * (i < last ? i : last), at);
         i += 64;
         copy4_to_lds((const uint8_t*)list + 4ull * (i < last ? i : last), at + 256);
@@ -341,7 +365,7 @@ struct Source {
         const uint32_t buf = lds_offset(sh.ring) + (t % kRing) * kTileBytes;
         const uint32_t at = lds_offset(&sh.scales[t % kRing][0][0]) + (wave - 1) * 256u;
         if (Slots) {
-            const int64_t* my = &sh.slots[wave][t % kSlotRing][0];
+            const int64_t* my = &sh.slots[t % kSlotRing][0];
 #pragma unroll
             for (int i = 0; i < 6; ++i) {
                 const uint32_t c = wave + kWaves * i;
@@ -436,17 +460,24 @@ __device__ __forceinline__ Sees sees(const AttendParams& p, const Seq& s, uint32
 
 // ---- attention ---------------------------------------------------------------------
 
-// R16: 16-row groups of a wave; RW waves split the rows, KW the keys of a tile,
-// DW the value columns (those waves form the same scores).
-template <int R16, int RW, int KW, int DW, bool Slots>
+// R16: 16-row groups of a wave.  RW waves split the rows, KW the keys of a tile, TW
+// the row's 512 values: such a wave forms its tiles' part of the scores, adds up
+// the others' through LDS, and takes its tiles' columns of the output.  Each code
+// is widened once a wave for 16 * R16 rows in either product; the widening (4
+// instructions for 8 codes) is what the vector unit spends most of its time on.
+template <int R16, int RW, int TW, int KW, bool Slots>
 __global__ __launch_bounds__(kThreads) void attend_kernel(const AttendParams p) {
-    static_assert(RW * KW * DW == kWaves, "every wave has its part");
+    static_assert(RW * KW * TW == kWaves, "every wave has its part");
     constexpr int M = 16 * R16 * RW;
-    constexpr int NB = 32 / DW;                     // 16-column blocks of a wave
+    constexpr int T = 4 / TW;                       // tiles of 128 of a wave
+    constexpr int NB = 8 * T;                       // 16-column blocks of a wave
+    static_assert(kWaves * R16 * 2048 <= kExchange, "partial scores of a step");
+    static_assert(KW == 1 || kWaves / 2 * R16 * (NB * 1024 + 512) <= kRing * kTileBytes + kExchange, "join of key halves");
     __shared__ Shared sh;
     const uint32_t lane = threadIdx.x & 63u, l16 = lane & 15u, g = lane >> 4;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const uint32_t rw = wave % RW, kw = (wave / RW) % KW, dw = wave / (RW * KW);
+    const uint32_t rw = wave % RW, kw = (wave / RW) % KW, tw = wave / (RW * KW);
+    const bool ropes = tw < 2;                      // RoPE half tw
     const int64_t capacity = p.head->capacity;
     const bool empty = capacity <= 0;
 
@@ -483,7 +514,7 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(const AttendParams p) 
         // this wave's query rows
         const uint32_t m = s.n > p.max_q ? p.max_q : s.n;
         const uint32_t rows = m * p.heads, row0 = unit * M;
-        QFrag q[R16];
+        QFrag<T, 1> q[R16];
         uint32_t token[R16];
 #pragma unroll
         for (int r = 0; r < R16; ++r) {
@@ -491,8 +522,8 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(const AttendParams p) 
             const uint32_t at = row0 + (rw * R16 + r) * 16u + l16, row = at < rows ? at : rows - 1;
             const uint32_t i = row / p.heads, h = row - i * p.heads;
             const uint64_t t = (uint64_t)s.q0 + i;
-            load_query(q[r], p.q_latent + t * p.q_latent_token + h * p.q_latent_head,
-                       p.q_rope + t * p.q_rope_token + h * p.q_rope_head, g);
+            q[r].load(p.q_latent + t * p.q_latent_token + h * p.q_latent_head + tw * T * 128,
+                      p.q_rope + t * p.q_rope_token + h * p.q_rope_head + (tw & 1) * 32, g);
             token[r] = i;
         }
         // positions below `clear` are seen by every row of the unit
@@ -526,6 +557,7 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(const AttendParams p) 
                 for (uint32_t t = t0; t < t0 + 3; ++t)
                     if (t < t_end) src.fetch_slots(t);
                 asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+                barrier();
             } else {
                 pg[0] = src.page(t0);
                 if (t0 + 1 < t_end) pg[1] = src.page(t0 + 1);
@@ -549,7 +581,7 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(const AttendParams p) 
             bool masked;
             if (Slots) {
                 const uint32_t left = s.kv - t * 64u;
-                const int64_t v = sh.slots[wave][t % kSlotRing][lane];
+                const int64_t v = sh.slots[t % kSlotRing][lane];
                 const bool in = lane < left;
                 live = __ballot(in && src.good(v));
                 const uint64_t wrong = __ballot(in && v != -1 && !src.good(v));
@@ -572,21 +604,40 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(const AttendParams p) 
                 const uint32_t k0 = (KW == 2 ? kw : (uint32_t)half) * 32u;
                 const uint8_t* rows32 = tile + k0 * kRow;
                 f32x4 x[2][R16];
-                scores32<R16>(x, rows32, scales + k0, q, l16, g);
+                scores32<R16, T, 1>(x, rows32 + tw * T * 128, rows32 + 528 + (tw & 1) * 64, scales + tw * T * 64 + k0, q,
+                                    p.scale_log2, ropes, l16, g);
+                // add up the parts of the waves that share these rows and keys, in one order
+                f32x4* part = (f32x4*)sh.exchange + lane;
+                if (half > 0) barrier();                 // the last parts have been read
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
 #pragma unroll
-                    for (int r = 0; r < R16; ++r) x[u][r] *= p.scale_log2;
+                    for (int r = 0; r < R16; ++r) part[((wave * 2 + u) * R16 + r) * 64] = x[u][r];
+                barrier();
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int r = 0; r < R16; ++r) {
+                        if (TW == 2) {
+                            x[u][r] += part[(((wave ^ (RW * KW)) * 2 + u) * R16 + r) * 64];
+                        } else {
+                            const uint32_t w0 = wave % (RW * KW);
+                            f32x4 sum4 = part[((w0 * 2 + u) * R16 + r) * 64];
+#pragma unroll
+                            for (int k = 1; k < TW; ++k) sum4 += part[(((w0 + k * RW * KW) * 2 + u) * R16 + r) * 64];
+                            x[u][r] = sum4;
+                        }
+                    }
                 if (masked) {
 #pragma unroll
                     for (int r = 0; r < R16; ++r) {
                         uint64_t on = live;
                         if (!Slots) on &= sees<Slots>(p, s, token[r]).bits(t * 64u);
-                        on >>= k0 + 4 * g;
+                        on >>= k0;
 #pragma unroll
                         for (int u = 0; u < 2; ++u)
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) x[u][r][i] = (on >> (u * 16 + i)) & 1u ? x[u][r][i] : -INFINITY;
+                            for (int i = 0; i < 4; ++i) x[u][r][i] = (on >> (key_of(u, g) + i)) & 1u ? x[u][r][i] : -INFINITY;
                     }
                 }
 #pragma unroll
@@ -617,10 +668,10 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(const AttendParams p) 
 #pragma unroll
                         for (int i = 0; i < 4; ++i) x[u][r][i] = e[u][i];
                 }
-                // values: 8 keys of this lane group (4 of each 16) x 16 columns
-                const uint32_t vk = (l16 >> 1) < 4 ? 4 * g + (l16 >> 1) : 12 + 4 * g + (l16 >> 1);
-                const uint8_t* vrow = rows32 + vk * kRow + (l16 & 1u) * 8u + dw * NB * 16;
-                const float* scale = scales + k0 + 4 * g;
+                // values: 8 keys of this lane group (4 of each half) x 16 columns
+                const uint32_t vk = key_of(l16 >> 3, g) + ((l16 >> 1) & 3u);
+                const uint8_t* vrow = rows32 + vk * kRow + (l16 & 1u) * 8u + tw * NB * 16;
+                const float* scale[2] = {scales + k0 + key_of(0, g) + (l16 & 3), scales + k0 + key_of(1, g) + (l16 & 3)};
                 constexpr int G = 4;                     // columns blocks read ahead
                 i32x2 c[G];
 #pragma unroll
@@ -634,14 +685,14 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(const AttendParams p) 
                     for (int d = 0; d < G; ++d)
                         next[d] = d0 + G < NB ? __builtin_amdgcn_ds_read_tr8_b64_v2i32((lptr<i32x2>)(vrow + (d0 + G + d) * 16)) : c[d];
                     if (d0 % 8 == 0) {                   // a tile of 128 values: its scales
-                        const uint32_t tj = (dw * NB + d0) / 8;
+                        const uint32_t tj = tw * T + d0 / 8;
 #pragma unroll
                         for (int u = 0; u < 2; ++u) {
-                            const f32x4 a = *(const f32x4*)(scale + tj * 64 + u * 16);
+                            const f32x4 a = quads(scale[u][tj * 64]);
 #pragma unroll
                             for (int r = 0; r < R16; ++r)
 #pragma unroll
-                                for (int i = 0; i < 4; ++i) w[r][u * 4 + i] = (__bf16)(x[u][r][i] * a[i]);
+                                for (int i = 0; i < 4; ++i) w[r][u * 4 + i] = (__bf16)(a[i] * x[u][r][i]);
                         }
                     }
 #pragma unroll
@@ -663,16 +714,17 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(const AttendParams p) 
             sum[r] += __shfl_xor(sum[r], 16);
             sum[r] += __shfl_xor(sum[r], 32);
             if (KW == 2) {
-                f32x4* ex = (f32x4*)sh.ring + (uint32_t)((dw * RW + rw) * R16 + r) * (NB * 64) + lane;
+                f32x4* ex = (f32x4*)sh.ring + (uint32_t)((tw * RW + rw) * R16 + r) * (NB * 64) + lane;
+                float* stat = (float*)(sh.ring + kWaves / 2 * R16 * NB * 1024) + (uint32_t)((tw * RW + rw) * R16 + r) * 128 + lane;
                 if (kw == 1) {
 #pragma unroll
                     for (int d = 0; d < NB; ++d) ex[d * 64] = o[r][d];
-                    sh.stat[0][(dw * RW + rw) * R16 + r][lane] = mx[r];
-                    sh.stat[1][(dw * RW + rw) * R16 + r][lane] = sum[r];
+                    stat[0] = mx[r];
+                    stat[64] = sum[r];
                 }
                 barrier();
                 if (kw == 0) {
-                    const float m2 = sh.stat[0][(dw * RW + rw) * R16 + r][lane], s2 = sh.stat[1][(dw * RW + rw) * R16 + r][lane];
+                    const float m2 = stat[0], s2 = stat[64];
                     const float next = fmaxf(mx[r], m2);
                     const float k1 = mx[r] == -INFINITY ? 0.f : exp2f(mx[r] - next), k2 = m2 == -INFINITY ? 0.f : exp2f(m2 - next);
                     // a NaN sum with no maximum (every weight of a half a NaN) has to stay one
@@ -693,19 +745,19 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(const AttendParams p) 
                 if (whole) {
                     const uint32_t i = row / p.heads, h = row - i * p.heads;
                     const uint64_t t = (uint64_t)s.q0 + i;
-                    uint16_t* out = p.out + t * p.out_token + h * p.out_head + dw * NB * 16;
+                    uint16_t* out = p.out + t * p.out_token + h * p.out_head + tw * NB * 16;
 #pragma unroll
                     for (int d = 0; d < NB; ++d) {
                         const f32x4 v = o[r][d] * inv;
                         *(bf16x4*)(out + d * 16 + g * 4) = __builtin_convertvector(v, bf16x4);
                     }
-                    if (p.lse && g == 0 && dw == 0) p.lse[t * p.lse_token + h] = lse2 * kLn2;
+                    if (p.lse && g == 0 && tw == 0) p.lse[t * p.lse_token + h] = lse2 * kLn2;
                 } else {
                     const uint64_t at = (uint64_t)slot * M + (rw * R16 + r) * 16u + l16;
-                    float* out = p.part + at * 512 + dw * NB * 16;
+                    float* out = p.part + at * 512 + tw * NB * 16;
 #pragma unroll
                     for (int d = 0; d < NB; ++d) *(f32x4*)(out + d * 16 + g * 4) = o[r][d] * inv;
-                    if (g == 0 && dw == 0) p.part_lse[at] = lse2;
+                    if (g == 0 && tw == 0) p.part_lse[at] = lse2;
                 }
             }
         }
@@ -813,9 +865,9 @@ __global__ __launch_bounds__(kThreads) void weights_kernel(const AttendParams p,
         const uint32_t at = row0 + wave * 16u + l16, row = at < rows ? at : rows - 1;
         const uint32_t i = row / p.heads, h = row - i * p.heads;
         const uint64_t t = (uint64_t)s.q0 + i;
-        QFrag q[1];
-        load_query(q[0], p.q_latent + t * p.q_latent_token + h * p.q_latent_head,
-                   p.q_rope + t * p.q_rope_token + h * p.q_rope_head, g);
+        QFrag<4, 2> q[1];
+        q[0].load(p.q_latent + t * p.q_latent_token + h * p.q_latent_head,
+                  p.q_rope + t * p.q_rope_token + h * p.q_rope_head, g);
         const float lse = p.lse[t * p.lse_token + h];
         // a row of -inf saw nothing; rows behind the last one add nothing
         const bool adds = at < rows && lse != -INFINITY;
@@ -848,14 +900,14 @@ __global__ __launch_bounds__(kThreads) void weights_kernel(const AttendParams p,
 #pragma unroll 1
             for (uint32_t half = 0; half < 2; ++half) {
                 f32x4 v[2][1];
-                scores32<1>(v, tile + half * 32 * kRow, scales + half * 32, q, l16, g);
+                const uint8_t* rows32 = tile + half * 32 * kRow;
+                scores32<1, 4, 2>(v, rows32, rows32 + 528, scales + half * 32, q, p.scale_log2, true, l16, g);
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    v[u][0] *= p.scale_log2;
                     if (masked) {
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            v[u][0][k] = (on >> (half * 32 + u * 16 + 4 * g + k)) & 1u ? v[u][0][k] : -INFINITY;
+                            v[u][0][k] = (on >> (half * 32 + key_of(u, g) + k)) & 1u ? v[u][0][k] : -INFINITY;
                     }
                     float keep = 0.f;
 #pragma unroll
@@ -864,7 +916,7 @@ __global__ __launch_bounds__(kThreads) void weights_kernel(const AttendParams p,
                         const float total = sum16(w);
                         keep = (int)l16 == k ? total : keep;
                     }
-                    if (l16 < 4) sh.sums[wave][(x - t0) * 64 + half * 32 + u * 16 + 4 * g + l16] += keep;
+                    if (l16 < 4) sh.sums[wave][(x - t0) * 64 + half * 32 + key_of(u, g) + l16] += keep;
                 }
             }
         }
@@ -882,17 +934,17 @@ __global__ __launch_bounds__(kThreads) void weights_kernel(const AttendParams p,
     }
 }
 
-template <int R16, int RW, int KW, int DW>
+template <int R16, int RW, int TW, int KW>
 hipError_t launch_shape(const AttendParams& p, uint32_t blocks, hipStream_t stream) {
     constexpr uint32_t M = 16 * R16 * RW;
     const uint64_t rows = (uint64_t)p.max_q * p.heads * p.num_seqs;
     const uint32_t joins = (uint32_t)(rows / 2 + 1 < 4096 ? rows / 2 + 1 : 4096);
     (void)hipGetLastError();
     if (p.by_slots) {
-        attend_kernel<R16, RW, KW, DW, true><<<dim3(blocks), dim3(kThreads), 0, stream>>>(p);
+        attend_kernel<R16, RW, TW, KW, true><<<dim3(blocks), dim3(kThreads), 0, stream>>>(p);
         combine_kernel<true><<<dim3(joins), dim3(256), 0, stream>>>(p, M);
     } else {
-        attend_kernel<R16, RW, KW, DW, false><<<dim3(blocks), dim3(kThreads), 0, stream>>>(p);
+        attend_kernel<R16, RW, TW, KW, false><<<dim3(blocks), dim3(kThreads), 0, stream>>>(p);
         combine_kernel<false><<<dim3(joins), dim3(256), 0, stream>>>(p, M);
     }
     return hipGetLastError();
@@ -902,7 +954,7 @@ hipError_t launch_shape(const AttendParams& p, uint32_t blocks, hipStream_t stre
 
 AttendPlan plan_attend(uint64_t rows, uint64_t num_seqs, uint64_t num_tokens, uint64_t heads, uint64_t max_kv) {
     AttendPlan a;
-    a.rows = rows <= 16 ? 16u : rows <= 32 ? 32u : rows <= 64 ? 64u : 128u;
+    a.rows = rows <= 16 ? 16u : rows <= 32 ? 32u : 64u;
     uint64_t units = num_seqs * ((rows + a.rows - 1) / a.rows);
     const uint64_t by_tokens = num_tokens * heads / a.rows + num_seqs;      // ragged: no more units than that
     units = units < by_tokens ? units : by_tokens;
@@ -928,10 +980,9 @@ hipError_t launch_attend(const AttendParams& given, void* workspace, hipStream_t
     p.part_lse = reinterpret_cast<float*>(ws + a.line_bytes);
     p.part = reinterpret_cast<float*>(ws + a.line_bytes + a.lse_bytes);
     switch (a.rows) {
-        case 16: return launch_shape<1, 1, 2, 4>(p, a.blocks, stream);
-        case 32: return launch_shape<1, 2, 2, 2>(p, a.blocks, stream);
-        case 64: return launch_shape<1, 4, 2, 1>(p, a.blocks, stream);
-        default: return launch_shape<1, 8, 1, 1>(p, a.blocks, stream);
+        case 16: return launch_shape<1, 1, 4, 2>(p, a.blocks, stream);
+        case 32: return launch_shape<2, 1, 4, 2>(p, a.blocks, stream);
+        default: return launch_shape<2, 2, 4, 1>(p, a.blocks, stream);
     }
 }
 
