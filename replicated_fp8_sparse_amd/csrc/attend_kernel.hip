@@ -99,6 +99,14 @@ struct QFrag {
 #pragma unroll
         for (int c = 0; c < P; ++c) rope[c] = *(const bf16x8*)(rp + c * 32 + g * 8);
     }
+    // The loads have landed: without this the compiler waits for them where they
+    // are used, in the loop, and with them for every tile in flight.
+    __device__ __forceinline__ void landed() {
+#pragma unroll
+        for (int c = 0; c < 4 * T; ++c) asm volatile("" : "+v"(lat[c]));
+#pragma unroll
+        for (int c = 0; c < P; ++c) asm volatile("" : "+v"(rope[c]));
+    }
 };
 
 // 8 codes as bf16 (exact).
@@ -526,6 +534,8 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(const AttendParams p) 
                       p.q_rope + t * p.q_rope_token + h * p.q_rope_head + (tw & 1) * 32, g);
             token[r] = i;
         }
+#pragma unroll
+        for (int r = 0; r < R16; ++r) q[r].landed();
         // positions below `clear` are seen by every row of the unit
         const Sees lowest = sees<Slots>(p, s, row0 / p.heads);
         const uint32_t clear = lowest.lim;
@@ -868,10 +878,12 @@ __global__ __launch_bounds__(kThreads) void weights_kernel(const AttendParams p,
         QFrag<4, 2> q[1];
         q[0].load(p.q_latent + t * p.q_latent_token + h * p.q_latent_head,
                   p.q_rope + t * p.q_rope_token + h * p.q_rope_head, g);
+        q[0].landed();
         const float lse = p.lse[t * p.lse_token + h];
         // a row of -inf saw nothing; rows behind the last one add nothing
         const bool adds = at < rows && lse != -INFINITY;
-        const float lse2 = adds ? lse * 1.44269504088896341f : INFINITY;
+        float lse2 = adds ? lse * 1.44269504088896341f : INFINITY;
+        asm volatile("" : "+v"(lse2));
         barrier();                        // the ring is free
         int64_t pg[3] = {page(t0), page(t0 + 1), page(t0 + 2)};
         fetch(t0, pg[0]);
