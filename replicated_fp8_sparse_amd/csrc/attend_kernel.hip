@@ -75,14 +75,13 @@ __device__ __forceinline__ void copy4_to_lds(const uint8_t* src, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(lds), "v"(src) : "memory");
 }
 
-// Every wave's own copies of all but the newest tile have landed, then all waves'.
-// A tile is 41 copies of rows, wave, wave + 8, ..., and one of each tile's scales
-// by waves 1..4: 6 copies for waves 0..4 and 5 for the others.
-__device__ __forceinline__ void wait_tile(uint32_t wave, bool newer) {
-    if (!newer) asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-    else if (wave <= 4) asm volatile("s_waitcnt vmcnt(6) lgkmcnt(0)" ::: "memory");
-    else asm volatile("s_waitcnt vmcnt(5) lgkmcnt(0)" ::: "memory");
-    asm volatile("s_barrier" ::: "memory");
+// This wave's own copies of all but the newest tile have landed.  A tile is 41
+// copies of rows, wave, wave + 8, ..., and one of each tile's scales by waves
+// 1..4: 6 copies for waves 0..4 and 5 for the others.
+__device__ __forceinline__ void wait_own(uint32_t wave, bool newer) {
+    if (!newer) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    else if (wave <= 4) asm volatile("s_waitcnt vmcnt(6)" ::: "memory");
+    else asm volatile("s_waitcnt vmcnt(5)" ::: "memory");
 }
 __device__ __forceinline__ void barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
@@ -174,8 +173,7 @@ __device__ __forceinline__ void scores32(f32x4 (*x)[R16], const uint8_t* rows, c
         for (int u = 0; u < 2; ++u) a[u] = sc[u][j * 64];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            __builtin_amdgcn_sched_barrier(0);
-            i32x4 next[2];
+                i32x4 next[2];
 #pragma unroll
             for (int u = 0; u < 2; ++u) next[u] = j * 2 + h + 1 < 2 * T ? *(const i32x4*)(rows + at[u] + (j * 2 + h + 1) * 64) : raw[u];
 #pragma unroll
@@ -478,14 +476,15 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(const AttendParams p) 
     static_assert(RW * KW * TW == kWaves, "every wave has its part");
     constexpr int M = 16 * R16 * RW;
     constexpr int T = 4 / TW;                       // tiles of 128 of a wave
+    constexpr int P = TW == 1 ? 2 : 1;              // RoPE halves of a wave
     constexpr int NB = 8 * T;                       // 16-column blocks of a wave
-    static_assert(kWaves * R16 * 2048 <= kExchange, "partial scores of a step");
+    static_assert(TW == 1 || 2 * kWaves * R16 * 2048 <= kExchange, "partial scores of two steps");
     static_assert(KW == 1 || kWaves / 2 * R16 * (NB * 1024 + 512) <= kRing * kTileBytes + kExchange, "join of key halves");
     __shared__ Shared sh;
     const uint32_t lane = threadIdx.x & 63u, l16 = lane & 15u, g = lane >> 4;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t rw = wave % RW, kw = (wave / RW) % KW, tw = wave / (RW * KW);
-    const bool ropes = tw < 2;                      // RoPE half tw
+    const bool ropes = TW == 1 || tw < 2;           // RoPE half tw
     const int64_t capacity = p.head->capacity;
     const bool empty = capacity <= 0;
 
@@ -522,7 +521,7 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(const AttendParams p) 
         // this wave's query rows
         const uint32_t m = s.n > p.max_q ? p.max_q : s.n;
         const uint32_t rows = m * p.heads, row0 = unit * M;
-        QFrag<T, 1> q[R16];
+        QFrag<T, P> q[R16];
         uint32_t token[R16];
 #pragma unroll
         for (int r = 0; r < R16; ++r) {
@@ -531,7 +530,7 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(const AttendParams p) 
             const uint32_t i = row / p.heads, h = row - i * p.heads;
             const uint64_t t = (uint64_t)s.q0 + i;
             q[r].load(p.q_latent + t * p.q_latent_token + h * p.q_latent_head + tw * T * 128,
-                      p.q_rope + t * p.q_rope_token + h * p.q_rope_head + (tw & 1) * 32, g);
+                      p.q_rope + t * p.q_rope_token + h * p.q_rope_head + (TW == 1 ? 0 : (tw & 1) * 32), g);
             token[r] = i;
         }
 #pragma unroll
@@ -576,21 +575,10 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(const AttendParams p) 
             src.fetch(t0, pg[0]);
             if (t0 + 1 < t_end) src.fetch(t0 + 1, pg[1]);
         }
-        for (uint32_t t = t0; t < t_end; ++t) {
-            wait_tile(wave, t + 1 < t_end);
-            if (Slots && t + 3 < t_end) src.fetch_slots(t + 3);
-            if (t + 2 < t_end) src.fetch(t + 2, pg[2]);
-            const int64_t page = pg[0];
-            pg[0] = pg[1];
-            pg[1] = pg[2];
-            if (!Slots) pg[2] = t + 3 < t_end ? src.page(t + 3) : -1;
-            uint8_t* tile = sh.ring + (t % kRing) * kTileBytes;
-            float* scales = &sh.scales[t % kRing][0][0];
-
-            uint64_t live = ~0ull;
-            bool masked;
+        // the rows of tile t that exist, and whether some row of the unit may not see it whole
+        auto inspect = [&](uint32_t t, int64_t page, uint64_t& live, bool& masked) {
+            const uint32_t left = s.kv - t * 64u;
             if (Slots) {
-                const uint32_t left = s.kv - t * 64u;
                 const int64_t v = sh.slots[t % kSlotRing][lane];
                 const bool in = lane < left;
                 live = __ballot(in && src.good(v));
@@ -598,8 +586,7 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(const AttendParams p) 
                 if (wrong && unit == 0 && threadIdx.x == 0) atomicAdd(p.invalid_count, (unsigned long long)__popcll(wrong));
                 masked = live != ~0ull;
             } else {
-                const uint32_t left = s.kv - t * 64u;
-                if (left < 64) live = (1ull << left) - 1;
+                live = left < 64 ? (1ull << left) - 1 : ~0ull;
                 masked = t * 64u + 64u > clear;
                 if (page < 0) {                          // page 0 was copied in its place
                     if (unit == 0 && threadIdx.x == 0) atomicAdd(p.invalid_count, 1ull);
@@ -607,113 +594,149 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(const AttendParams p) 
                     masked = true;
                 }
             }
-            if (masked) clean_tile(tile, scales, live);
-
-#pragma unroll 1
-            for (int half = 0; half < 2 / KW; ++half) {
-                const uint32_t k0 = (KW == 2 ? kw : (uint32_t)half) * 32u;
-                const uint8_t* rows32 = tile + k0 * kRow;
-                f32x4 x[2][R16];
-                scores32<R16, T, 1>(x, rows32 + tw * T * 128, rows32 + 528 + (tw & 1) * 64, scales + tw * T * 64 + k0, q,
-                                    p.scale_log2, ropes, l16, g);
-                // add up the parts of the waves that share these rows and keys, in one order
-                f32x4* part = (f32x4*)sh.exchange + lane;
-                if (half > 0) barrier();                 // the last parts have been read
+            if (masked) clean_tile(sh.ring + (t % kRing) * kTileBytes, &sh.scales[t % kRing][0][0], live);
+        };
+        auto first_key = [&](uint32_t half) { return (KW == 2 ? kw : half) * 32u; };
+        // this wave's part of the scores of a step
+        auto part_of = [&](uint32_t t, uint32_t half, f32x4 (*x)[R16]) {
+            const uint32_t k0 = first_key(half);
+            const uint8_t* rows32 = sh.ring + (t % kRing) * kTileBytes + k0 * kRow;
+            scores32<R16, T, P>(x, rows32 + tw * T * 128, rows32 + 528 + (TW == 1 ? 0 : (tw & 1) * 64),
+                                &sh.scales[t % kRing][tw * T][k0], q, p.scale_log2, ropes, l16, g);
+        };
+        f32x4* const part = (f32x4*)sh.exchange + lane;  // [step & 1][wave][half u][r][lane]
+        auto give = [&](uint32_t step, f32x4 (*x)[R16]) {
+            if (TW == 1) return;
 #pragma unroll
-                for (int u = 0; u < 2; ++u)
+            for (int u = 0; u < 2; ++u)
 #pragma unroll
-                    for (int r = 0; r < R16; ++r) part[((wave * 2 + u) * R16 + r) * 64] = x[u][r];
-                barrier();
+                for (int r = 0; r < R16; ++r) part[((((step & 1u) * kWaves + wave) * 2 + u) * R16 + r) * 64] = x[u][r];
+        };
+        // add up the parts of the waves that share rows and keys, in one order
+        auto gather = [&](uint32_t step, f32x4 (*x)[R16]) {
 #pragma unroll
-                for (int u = 0; u < 2; ++u)
-#pragma unroll
-                    for (int r = 0; r < R16; ++r) {
-                        if (TW == 2) {
-                            x[u][r] += part[(((wave ^ (RW * KW)) * 2 + u) * R16 + r) * 64];
-                        } else {
-                            const uint32_t w0 = wave % (RW * KW);
-                            f32x4 sum4 = part[((w0 * 2 + u) * R16 + r) * 64];
-#pragma unroll
-                            for (int k = 1; k < TW; ++k) sum4 += part[(((w0 + k * RW * KW) * 2 + u) * R16 + r) * 64];
-                            x[u][r] = sum4;
-                        }
-                    }
-                if (masked) {
-#pragma unroll
-                    for (int r = 0; r < R16; ++r) {
-                        uint64_t on = live;
-                        if (!Slots) on &= sees<Slots>(p, s, token[r]).bits(t * 64u);
-                        on >>= k0;
-#pragma unroll
-                        for (int u = 0; u < 2; ++u)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) x[u][r][i] = (on >> (key_of(u, g) + i)) & 1u ? x[u][r][i] : -INFINITY;
-                    }
-                }
+            for (int u = 0; u < 2; ++u)
 #pragma unroll
                 for (int r = 0; r < R16; ++r) {
-                    float top = fmaxf(fmaxf(fmaxf(x[0][r][0], x[0][r][1]), fmaxf(x[0][r][2], x[0][r][3])),
-                                      fmaxf(fmaxf(x[1][r][0], x[1][r][1]), fmaxf(x[1][r][2], x[1][r][3])));
-                    if (__any(top > mx[r] + kLazy || (mx[r] == -INFINITY && top > mx[r]))) {
-                        top = fmaxf(top, __shfl_xor(top, 16));
-                        top = fmaxf(top, __shfl_xor(top, 32));
-                        const float next = fmaxf(mx[r], top);
-                        const float keep = mx[r] == -INFINITY ? 0.f : exp2f(mx[r] - next);
-                        mx[r] = next;
-                        sum[r] *= keep;
+                    const f32x4* from = part + ((((step & 1u) * kWaves + wave) * 2 + u) * R16 + r) * 64;
+                    if (TW == 2) {
+                        x[u][r] += from[(int)((wave ^ (RW * KW)) - wave) * 2 * R16 * 64];
+                    } else if (TW > 2) {
+                        from -= tw * RW * KW * 2 * R16 * 64;
+                        f32x4 total = from[0];
 #pragma unroll
-                        for (int d = 0; d < NB; ++d) o[r][d] *= keep;
+                        for (int k = 1; k < TW; ++k) total += from[k * RW * KW * 2 * R16 * 64];
+                        x[u][r] = total;
                     }
-                    const float ref = mx[r] == -INFINITY ? 0.f : mx[r];
-                    float e[2][4];
-#pragma unroll
-                    for (int u = 0; u < 2; ++u)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            e[u][i] = __builtin_amdgcn_exp2f(x[u][r][i] - ref);
-                            sum[r] += e[u][i];
-                        }
-#pragma unroll
-                    for (int u = 0; u < 2; ++u)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) x[u][r][i] = e[u][i];
                 }
-                // values: 8 keys of this lane group (4 of each half) x 16 columns
-                const uint32_t vk = key_of(l16 >> 3, g) + ((l16 >> 1) & 3u);
-                const uint8_t* vrow = rows32 + vk * kRow + (l16 & 1u) * 8u + tw * NB * 16;
-                const float* scale[2] = {scales + k0 + key_of(0, g) + (l16 & 3), scales + k0 + key_of(1, g) + (l16 & 3)};
-                constexpr int G = 4;                     // columns blocks read ahead
-                i32x2 c[G];
+        };
+
+        // A step is 32 keys a wave.  The next step's scores are formed beside this
+        // one's weights and values, so their waits overlap; one barrier a step
+        // publishes the parts, the next tile and that the last one is done with.
+        f32x4 x[2][R16];
+        uint64_t live = ~0ull;
+        bool masked = false;
+        constexpr uint32_t H = 2 / KW;                   // steps of a tile
+        if (t0 < t_end) {
+            wait_own(wave, t0 + 1 < t_end);
+            barrier();
+            inspect(t0, pg[0], live, masked);
+            part_of(t0, 0, x);
+            give(0, x);
+        }
+        uint32_t t = t0, half = 0;
+        for (uint32_t step = 0; t < t_end; ++step) {
+            const bool last = half + 1 == H, more = !last || t + 1 < t_end, fresh = last && more;
+            const uint32_t tn = fresh ? t + 1 : t, hn = !more ? half : last ? 0u : half + 1;
+            if (fresh) wait_own(wave, H == 2 && t + 2 < t_end);
+            barrier();
+            if (half == 0 && t + 2 < t_end) {
+                if (Slots && t + 3 < t_end) src.fetch_slots(t + 3);
+                src.fetch(t + 2, pg[2]);
+            }
+            gather(step, x);
+            const uint32_t k0 = first_key(half);
+            if (masked) {
 #pragma unroll
-                for (int d = 0; d < G; ++d) c[d] = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lptr<i32x2>)(vrow + d * 16));
+                for (int r = 0; r < R16; ++r) {
+                    uint64_t on = live;
+                    if (!Slots) on &= sees<Slots>(p, s, token[r]).bits(t * 64u);
+                    on >>= k0;
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) x[u][r][i] = (on >> (key_of(u, g) + i)) & 1u ? x[u][r][i] : -INFINITY;
+                }
+            }
+            if (fresh) inspect(t + 1, pg[1], live, masked);
+#pragma unroll
+            for (int r = 0; r < R16; ++r) {
+                float top = fmaxf(fmaxf(fmaxf(x[0][r][0], x[0][r][1]), fmaxf(x[0][r][2], x[0][r][3])),
+                                  fmaxf(fmaxf(x[1][r][0], x[1][r][1]), fmaxf(x[1][r][2], x[1][r][3])));
+                if (__any(top > mx[r] + kLazy || (mx[r] == -INFINITY && top > mx[r]))) {
+                    top = fmaxf(top, __shfl_xor(top, 16));
+                    top = fmaxf(top, __shfl_xor(top, 32));
+                    const float next = fmaxf(mx[r], top);
+                    const float keep = mx[r] == -INFINITY ? 0.f : exp2f(mx[r] - next);
+                    mx[r] = next;
+                    sum[r] *= keep;
+#pragma unroll
+                    for (int d = 0; d < NB; ++d) o[r][d] *= keep;
+                }
+            }
+            // the next step's scores (behind the last step: this one's again, not used)
+            f32x4 xn[2][R16];
+            part_of(tn, hn, xn);
+            // weights
+#pragma unroll
+            for (int r = 0; r < R16; ++r) {
+                const float ref = mx[r] == -INFINITY ? 0.f : mx[r];
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        x[u][r][i] = __builtin_amdgcn_exp2f(x[u][r][i] - ref);
+                        sum[r] += x[u][r][i];
+                    }
+            }
+            // values: 8 keys of this lane group (4 of each half) x 16 columns
+            const uint32_t vk = key_of(l16 >> 3, g) + ((l16 >> 1) & 3u);
+            const uint8_t* vrow = sh.ring + (t % kRing) * kTileBytes + (k0 + vk) * kRow + (l16 & 1u) * 8u + tw * NB * 16;
+            const float* scale[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) scale[u] = &sh.scales[t % kRing][tw * T][k0 + key_of(u, g) + (l16 & 3)];
+#pragma unroll
+            for (int j = 0; j < T; ++j) {
                 bf16x8 w[R16];
 #pragma unroll
-                for (int d0 = 0; d0 < NB; d0 += G) {
-                    __builtin_amdgcn_sched_barrier(0);
-                    i32x2 next[G];
+                for (int u = 0; u < 2; ++u) {
+                    const f32x4 a = quads(scale[u][j * 64]);
 #pragma unroll
-                    for (int d = 0; d < G; ++d)
-                        next[d] = d0 + G < NB ? __builtin_amdgcn_ds_read_tr8_b64_v2i32((lptr<i32x2>)(vrow + (d0 + G + d) * 16)) : c[d];
-                    if (d0 % 8 == 0) {                   // a tile of 128 values: its scales
-                        const uint32_t tj = tw * T + d0 / 8;
+                    for (int r = 0; r < R16; ++r)
 #pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            const f32x4 a = quads(scale[u][tj * 64]);
-#pragma unroll
-                            for (int r = 0; r < R16; ++r)
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) w[r][u * 4 + i] = (__bf16)(a[i] * x[u][r][i]);
-                        }
-                    }
-#pragma unroll
-                    for (int d = 0; d < G; ++d) {
-                        const bf16x8 v = widen(c[d].x, c[d].y);
-#pragma unroll
-                        for (int r = 0; r < R16; ++r)
-                            o[r][d0 + d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, w[r], o[r][d0 + d], 0, 0, 0);
-                        c[d] = next[d];
-                    }
+                        for (int i = 0; i < 4; ++i) w[r][u * 4 + i] = (__bf16)(a[i] * x[u][r][i]);
                 }
+#pragma unroll
+                for (int d = j * 8; d < j * 8 + 8; ++d) {
+                    const i32x2 c = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lptr<i32x2>)(vrow + d * 16));
+                    const bf16x8 v = widen(c.x, c.y);
+#pragma unroll
+                    for (int r = 0; r < R16; ++r) o[r][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, w[r], o[r][d], 0, 0, 0);
+                }
+            }
+            if (!more) break;
+            give(step + 1, xn);
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int r = 0; r < R16; ++r) x[u][r] = xn[u][r];
+            half = hn;
+            if (fresh) {
+                t = tn;
+                pg[0] = pg[1];
+                pg[1] = pg[2];
+                if (!Slots) pg[2] = t + 2 < t_end ? src.page(t + 2) : -1;
             }
         }
         barrier();    // the ring is free
@@ -889,7 +912,8 @@ __global__ __launch_bounds__(kThreads) void weights_kernel(const AttendParams p,
         fetch(t0, pg[0]);
         if (t0 + 1 < t1) fetch(t0 + 1, pg[1]);
         for (uint32_t x = t0; x < t1; ++x) {
-            wait_tile(wave, x + 1 < t1);
+            wait_own(wave, x + 1 < t1);
+            barrier();
             if (x + 2 < t1) fetch(x + 2, pg[2]);
             const int64_t now = pg[0];
             pg[0] = pg[1];
@@ -993,8 +1017,8 @@ hipError_t launch_attend(const AttendParams& given, void* workspace, hipStream_t
     p.part = reinterpret_cast<float*>(ws + a.line_bytes + a.lse_bytes);
     switch (a.rows) {
         case 16: return launch_shape<1, 1, 4, 2>(p, a.blocks, stream);
-        case 32: return launch_shape<2, 1, 4, 2>(p, a.blocks, stream);
-        default: return launch_shape<2, 2, 4, 1>(p, a.blocks, stream);
+        case 32: return launch_shape<1, 2, 2, 2>(p, a.blocks, stream);
+        default: return launch_shape<1, 4, 2, 1>(p, a.blocks, stream);
     }
 }
 
