@@ -50,8 +50,8 @@ constexpr float kLazy = 8.0f;                    // rescale when a maximum grows
 
 // LDS: the tile ring and the waves' exchange of partial scores (after the last
 // tile both hold the join of key halves), the tiles' scales by tile of 128, slot
-// lists 4 tiles deep.  160 KB in all.
-constexpr int kSlotRing = 4;
+// lists 3 tiles deep.  160 KB in all.
+constexpr int kSlotRing = 3;
 constexpr int kExchange = 32768;
 struct Shared {
     alignas(16) uint8_t ring[kRing * kTileBytes];
@@ -60,6 +60,14 @@ struct Shared {
     alignas(16) int64_t slots[kSlotRing][64];
 };
 static_assert(sizeof(Shared) <= 163840, "160 KB of LDS");
+
+// Tile t's place in the ring; opaque, so that addresses stay a base and immediate
+// offsets instead of one induction variable each.
+__device__ __forceinline__ uint32_t ring_of(uint32_t t) {
+    uint32_t r = t % kRing;
+    asm("" : "+s"(r));
+    return r;
+}
 
 __device__ __forceinline__ uint32_t lds_offset(const void* p) {
     return (uint32_t)(uintptr_t)(lptr<const uint8_t>)(const uint8_t*)p;
@@ -276,7 +284,7 @@ struct Place {
 // Where this block's run begins, from prefix sums of the sequences' work: by each
 // wave alone up to 64 sequences, else by the whole block.  Block 0 leaves the
 // prefixes and the share for combine_kernel.
-__device__ __forceinline__ Place place(const AttendParams& p, uint32_t M, bool empty, Shared& sh) {
+__device__ __forceinline__ Place place(const AttendParams& p, uint32_t M, bool empty, uint8_t* scratch) {
     const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = tid >> 6;
     const bool first_block = blockIdx.x == 0;
     Place r;
@@ -295,7 +303,7 @@ __device__ __forceinline__ Place place(const AttendParams& p, uint32_t M, bool e
         r.off = at - __builtin_amdgcn_readlane(first, r.b);
         if (first_block && tid < p.num_seqs) p.line[tid] = first;
     } else {
-        uint32_t* scan = (uint32_t*)sh.exchange;
+        uint32_t* scan = (uint32_t*)scratch;
         uint32_t carry = 0, at = 0;
         for (int pass = 0; pass < 2; ++pass) {       // the total, then the place
             carry = 0;
@@ -334,6 +342,60 @@ __device__ __forceinline__ Place place(const AttendParams& p, uint32_t M, bool e
     return r;
 }
 
+// One run of tiles of one unit.
+struct Segment {
+    Seq s;
+    uint32_t b, unit;
+    uint32_t t0, t1;         // tiles
+    uint32_t slot;           // of partial results
+    bool whole;              // all of the unit's tiles
+};
+
+// The block's run of the line, segment by segment.
+template <bool Slots>
+struct Line {
+    const AttendParams& p;
+    uint32_t M;
+    bool empty;
+    uint32_t begin, end, pos, b, off;
+
+    __device__ __forceinline__ Line(const AttendParams& p_, uint32_t M_, bool empty_, uint8_t* scratch) : p(p_), M(M_), empty(empty_) {
+        Place at;
+        if (Slots) {
+            const Seq s = sequence<true, true>(p, 0, M, empty);
+            const uint32_t w = s.units * s.tiles;
+            at.total = p.num_seqs * w;
+            at.each = share(p, at.total, gridDim.x);
+            at.b = at.each * blockIdx.x / w;
+            at.off = at.each * blockIdx.x - at.b * w;
+        } else {
+            at = place(p, M, empty, scratch);
+        }
+        b = __builtin_amdgcn_readfirstlane(at.b);      // the same for the block: kept in scalar registers
+        off = __builtin_amdgcn_readfirstlane(at.off);
+        const uint32_t each = __builtin_amdgcn_readfirstlane(at.each), total = __builtin_amdgcn_readfirstlane(at.total);
+        if (blockIdx.x == 0 && threadIdx.x == 0) p.line[p.num_seqs] = each;
+        pos = begin = each * blockIdx.x;
+        end = begin + each < total ? begin + each : total;
+    }
+    __device__ __forceinline__ bool next(Segment& g) {
+        while (pos < end) {
+            g.s = sequence<Slots, true>(p, b, M, empty);
+            if (off >= g.s.units * g.s.tiles) { ++b; off = 0; continue; }     // pos < end <= total: a later sequence has work
+            g.b = b;
+            g.unit = off / g.s.tiles;
+            g.t0 = off - g.unit * g.s.tiles;
+            g.t1 = g.s.tiles - g.t0 < end - pos ? g.s.tiles : g.t0 + (end - pos);
+            g.whole = g.t0 == 0 && g.t1 == g.s.tiles;
+            g.slot = 2u * blockIdx.x + (pos == begin ? 0u : 1u);
+            pos += g.t1 - g.t0;
+            off += g.t1 - g.t0;
+            return true;
+        }
+        return false;
+    }
+};
+
 // ---- tiles -----------------------------------------------------------------------
 
 // Where a unit's tiles come from, and which keys of a tile exist.
@@ -344,7 +406,9 @@ struct Source {
     const int64_t* list;       // this token's slots
     uint32_t kv;
     int64_t capacity;
-    Shared& sh;
+    uint8_t* ring;
+    float (*scales)[4][64];
+    int64_t (*slots)[64];
     uint32_t wave, lane;
 
     __device__ __forceinline__ int64_t page(uint32_t t) const {   // -1: no such page
@@ -356,7 +420,7 @@ struct Source {
         if (wave != 5) return;
         const uint32_t last = 2u * kv - 1u;
         uint32_t i = t * 128u + lane;
-        const uint32_t at = lds_offset(&sh.slots[t % kSlotRing][0]);
+        const uint32_t at = lds_offset(&slots[t % kSlotRing][0]);
         copy4_to_lds((const uint8_t*)list + 4ull * (i < last ? i : last), at);
         i += 64;
         copy4_to_lds((const uint8_t*)list + 4ull * (i < last ? i : last), at + 256);
@@ -366,12 +430,39 @@ struct Source {
         const uint64_t v = good(s) ? (uint64_t)s : 0u;
         return (v >> 6) * p.main_page_stride + (v & 63u) * (uint64_t)kRow;
     }
+    // Pages of the first three tiles (or their slots), and the first two tiles on their way.
+    __device__ __forceinline__ void start(uint32_t t0, uint32_t t_end, int64_t* pg) const {
+        pg[0] = pg[1] = pg[2] = -1;
+        if (t0 >= t_end) return;
+        if (Slots) {
+            for (uint32_t t = t0; t < t0 + 3 && t < t_end; ++t) fetch_slots(t);
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            barrier();
+        } else {
+            pg[0] = page(t0);
+            if (t0 + 1 < t_end) pg[1] = page(t0 + 1);
+            if (t0 + 2 < t_end) pg[2] = page(t0 + 2);
+        }
+        fetch(t0, pg[0]);
+        if (t0 + 1 < t_end) fetch(t0 + 1, pg[1]);
+    }
+    // Tile t + 2 on its way, and the slots of the one behind it.
+    __device__ __forceinline__ void ahead(uint32_t t, uint32_t t_end, const int64_t* pg) const {
+        if (t + 2 >= t_end) return;
+        if (Slots && t + 3 < t_end) fetch_slots(t + 3);
+        fetch(t + 2, pg[2]);
+    }
+    __device__ __forceinline__ void turn(uint32_t t, uint32_t t_end, int64_t* pg) const {    // t: the new first tile
+        pg[0] = pg[1];
+        pg[1] = pg[2];
+        if (!Slots) pg[2] = t + 2 < t_end ? page(t + 2) : -1;
+    }
     // This wave's share of tile t: chunks wave, wave + 8, ..., and a tile's scales.
     __device__ __forceinline__ void fetch(uint32_t t, int64_t pg) const {
-        const uint32_t buf = lds_offset(sh.ring) + (t % kRing) * kTileBytes;
-        const uint32_t at = lds_offset(&sh.scales[t % kRing][0][0]) + (wave - 1) * 256u;
+        const uint32_t buf = lds_offset(ring) + ring_of(t) * kTileBytes;
+        const uint32_t at = lds_offset(&scales[ring_of(t)][0][0]) + (wave - 1) * 256u;
         if (Slots) {
-            const int64_t* my = &sh.slots[t % kSlotRing][0];
+            const int64_t* my = &slots[t % kSlotRing][0];
 #pragma unroll
             for (int i = 0; i < 6; ++i) {
                 const uint32_t c = wave + kWaves * i;
@@ -464,7 +555,77 @@ __device__ __forceinline__ Sees sees(const AttendParams& p, const Seq& s, uint32
     return v;
 }
 
+// What a unit's rows see of its tiles.
+struct View {
+    uint32_t clear;            // positions below are seen by every row
+    uint32_t t_end;            // none of the segment's tiles from here on is seen by any row
+};
+
+template <bool Slots>
+__device__ __forceinline__ View view_of(const AttendParams& p, const Segment& g, uint32_t M, uint32_t rows, uint32_t row0) {
+    View v;
+    v.clear = sees<Slots>(p, g.s, row0 / p.heads).lim;
+    v.t_end = g.s.kv ? g.t1 : g.t0;
+    if (!Slots && !p.tree) {
+        const uint32_t last = (row0 + M < rows ? row0 + M : rows) - 1;
+        const uint32_t tl = (sees<Slots>(p, g.s, last / p.heads).lim + 63) / 64;
+        v.t_end = v.t_end < tl ? v.t_end : tl;
+    }
+    return v;
+}
+
+// The rows of tile t that exist (bits of live) and whether some row of the unit may
+// not see it whole; such a tile is cleaned.  Bad pages and slots are counted by the
+// unit that has the sequence's first rows.
+template <bool Slots, class Src>
+__device__ __forceinline__ void inspect(const AttendParams& p, const Src& src, const Segment& g, const View& view, uint32_t t,
+                                        int64_t page, uint8_t* tile, float* scales, uint64_t& live, bool& masked) {
+    const uint32_t left = g.s.kv - t * 64u;
+    if (Slots) {
+        const int64_t v = src.slots[t % kSlotRing][src.lane];
+        const bool in = src.lane < left;
+        live = __ballot(in && src.good(v));
+        const uint64_t wrong = __ballot(in && v != -1 && !src.good(v));
+        if (wrong && g.unit == 0 && threadIdx.x == 0) atomicAdd(p.invalid_count, (unsigned long long)__popcll(wrong));
+        masked = live != ~0ull;
+    } else {
+        live = left < 64 ? (1ull << left) - 1 : ~0ull;
+        masked = t * 64u + 64u > view.clear;
+        if (page < 0) {                              // page 0 was copied in its place
+            if (g.unit == 0 && threadIdx.x == 0) atomicAdd(p.invalid_count, 1ull);
+            live = 0;
+            masked = true;
+        }
+    }
+    if (masked) clean_tile(tile, scales, live);
+}
+
 // ---- attention ---------------------------------------------------------------------
+
+// Row `at` of the unit, values col .. col + 16 * NB - 1: the result, or the segment's part of it.
+template <int M, int NB>
+__device__ __forceinline__ void write_row(const AttendParams& p, const Segment& s, uint32_t at, uint32_t col, const f32x4* o,
+                                          float mx, float sum, uint32_t g) {
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const float lse2 = sum == 0.f ? -INFINITY : (mx == -INFINITY ? 0.f : mx) + log2f(sum);
+    if (s.whole) {
+        const uint32_t row = s.unit * M + at, i = row / p.heads, h = row - i * p.heads;
+        const uint64_t t = (uint64_t)s.s.q0 + i;
+        uint16_t* out = p.out + t * p.out_token + h * p.out_head + col;
+#pragma unroll
+        for (int d = 0; d < NB; ++d) {
+            const f32x4 v = o[d] * inv;
+            *(bf16x4*)(out + d * 16 + g * 4) = __builtin_convertvector(v, bf16x4);
+        }
+        if (p.lse && g == 0 && col == 0) p.lse[t * p.lse_token + h] = lse2 * kLn2;
+    } else {
+        const uint64_t x = (uint64_t)s.slot * M + at;
+        float* out = p.part + x * 512 + col;
+#pragma unroll
+        for (int d = 0; d < NB; ++d) *(f32x4*)(out + d * 16 + g * 4) = o[d] * inv;
+        if (g == 0 && col == 0) p.part_lse[x] = lse2;
+    }
+}
 
 // R16: 16-row groups of a wave.  RW waves split the rows, KW the keys of a tile, TW
 // the row's 512 values: such a wave forms its tiles' part of the scores, adds up
@@ -486,37 +647,11 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(const AttendParams p) 
     const uint32_t rw = wave % RW, kw = (wave / RW) % KW, tw = wave / (RW * KW);
     const bool ropes = TW == 1 || tw < 2;           // RoPE half tw
     const int64_t capacity = p.head->capacity;
-    const bool empty = capacity <= 0;
-
-    Place at;
-    if (Slots) {
-        const Seq s = sequence<true, true>(p, 0, M, empty);
-        const uint32_t w = s.units * s.tiles;
-        at.total = p.num_seqs * w;
-        at.each = share(p, at.total, gridDim.x);
-        at.b = at.each * blockIdx.x / w;
-        at.off = at.each * blockIdx.x - at.b * w;
-    } else {
-        at = place(p, M, empty, sh);
-    }
-    at.b = __builtin_amdgcn_readfirstlane(at.b);      // the same for the block: keep what follows in scalar registers
-    at.off = __builtin_amdgcn_readfirstlane(at.off);
-    at.each = __builtin_amdgcn_readfirstlane(at.each);
-    at.total = __builtin_amdgcn_readfirstlane(at.total);
-    if (blockIdx.x == 0 && threadIdx.x == 0) p.line[p.num_seqs] = at.each;
-    const uint32_t begin = at.each * blockIdx.x;
-    const uint32_t end = begin + at.each < at.total ? begin + at.each : at.total;
-    uint32_t pos = begin, b = at.b, off = at.off;
-
-    while (pos < end) {
-        const Seq s = sequence<Slots, true>(p, b, M, empty);
-        if (off >= s.units * s.tiles) { ++b; off = 0; continue; }     // pos < end <= total: a later sequence has work
-        const uint32_t unit = off / s.tiles, t0 = off - unit * s.tiles;
-        const uint32_t t1 = s.tiles - t0 < end - pos ? s.tiles : t0 + (end - pos);
-        const bool whole = t0 == 0 && t1 == s.tiles;
-        const uint32_t slot = 2u * blockIdx.x + (pos == begin ? 0u : 1u);
-        pos += t1 - t0;
-        off += t1 - t0;
+    Line<Slots> line(p, M, capacity <= 0, sh.exchange);
+    Segment seg;
+    while (line.next(seg)) {
+        const Seq& s = seg.s;
+        const uint32_t b = seg.b, unit = seg.unit, t0 = seg.t0;
 
         // this wave's query rows
         const uint32_t m = s.n > p.max_q ? p.max_q : s.n;
@@ -535,17 +670,8 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(const AttendParams p) 
         }
 #pragma unroll
         for (int r = 0; r < R16; ++r) q[r].landed();
-        // positions below `clear` are seen by every row of the unit
-        const Sees lowest = sees<Slots>(p, s, row0 / p.heads);
-        const uint32_t clear = lowest.lim;
-        // and none of its rows sees a tile from `t_end` on
-        uint32_t t_end = s.kv ? t1 : t0;
-        if (!Slots && !p.tree) {
-            const uint32_t last_row = (row0 + M < rows ? row0 + M : rows) - 1;
-            const Sees highest = sees<Slots>(p, s, last_row / p.heads);
-            const uint32_t tl = (highest.lim + 63) / 64;
-            t_end = t_end < tl ? t_end : tl;
-        }
+        const View view = view_of<Slots>(p, seg, M, rows, row0);
+        const uint32_t t_end = view.t_end;
 
         __builtin_amdgcn_sched_barrier(0);
         f32x4 o[R16][NB];
@@ -559,50 +685,16 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(const AttendParams p) 
         }
 
         const Source<Slots> src{p, Slots ? nullptr : p.pages + (uint64_t)b * p.pages_stride,
-                                Slots ? p.slots + (uint64_t)b * p.slots_stride : nullptr, s.kv, capacity, sh, wave, lane};
-        int64_t pg[3] = {-1, -1, -1};                    // pages of tiles t, t + 1, t + 2
-        if (t0 < t_end) {
-            if (Slots) {
-                for (uint32_t t = t0; t < t0 + 3; ++t)
-                    if (t < t_end) src.fetch_slots(t);
-                asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-                barrier();
-            } else {
-                pg[0] = src.page(t0);
-                if (t0 + 1 < t_end) pg[1] = src.page(t0 + 1);
-                if (t0 + 2 < t_end) pg[2] = src.page(t0 + 2);
-            }
-            src.fetch(t0, pg[0]);
-            if (t0 + 1 < t_end) src.fetch(t0 + 1, pg[1]);
-        }
-        // the rows of tile t that exist, and whether some row of the unit may not see it whole
-        auto inspect = [&](uint32_t t, int64_t page, uint64_t& live, bool& masked) {
-            const uint32_t left = s.kv - t * 64u;
-            if (Slots) {
-                const int64_t v = sh.slots[t % kSlotRing][lane];
-                const bool in = lane < left;
-                live = __ballot(in && src.good(v));
-                const uint64_t wrong = __ballot(in && v != -1 && !src.good(v));
-                if (wrong && unit == 0 && threadIdx.x == 0) atomicAdd(p.invalid_count, (unsigned long long)__popcll(wrong));
-                masked = live != ~0ull;
-            } else {
-                live = left < 64 ? (1ull << left) - 1 : ~0ull;
-                masked = t * 64u + 64u > clear;
-                if (page < 0) {                          // page 0 was copied in its place
-                    if (unit == 0 && threadIdx.x == 0) atomicAdd(p.invalid_count, 1ull);
-                    live = 0;
-                    masked = true;
-                }
-            }
-            if (masked) clean_tile(sh.ring + (t % kRing) * kTileBytes, &sh.scales[t % kRing][0][0], live);
-        };
+                                Slots ? p.slots + (uint64_t)b * p.slots_stride : nullptr, s.kv, capacity, sh.ring, sh.scales, sh.slots, wave, lane};
+        int64_t pg[3];                                   // pages of tiles t, t + 1, t + 2
+        src.start(t0, t_end, pg);
         auto first_key = [&](uint32_t half) { return (KW == 2 ? kw : half) * 32u; };
         // this wave's part of the scores of a step
         auto part_of = [&](uint32_t t, uint32_t half, f32x4 (*x)[R16]) {
             const uint32_t k0 = first_key(half);
-            const uint8_t* rows32 = sh.ring + (t % kRing) * kTileBytes + k0 * kRow;
+            const uint8_t* rows32 = sh.ring + ring_of(t) * kTileBytes + k0 * kRow;
             scores32<R16, T, P>(x, rows32 + tw * T * 128, rows32 + 528 + (TW == 1 ? 0 : (tw & 1) * 64),
-                                &sh.scales[t % kRing][tw * T][k0], q, p.scale_log2, ropes, l16, g);
+                                &sh.scales[ring_of(t)][tw * T][k0], q, p.scale_log2, ropes, l16, g);
         };
         f32x4* const part = (f32x4*)sh.exchange + lane;  // [step & 1][wave][half u][r][lane]
         auto give = [&](uint32_t step, f32x4 (*x)[R16]) {
@@ -637,11 +729,14 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(const AttendParams p) 
         f32x4 x[2][R16];
         uint64_t live = ~0ull;
         bool masked = false;
+        auto look = [&](uint32_t t, int64_t page) {
+            inspect<Slots>(p, src, seg, view, t, page, sh.ring + ring_of(t) * kTileBytes, &sh.scales[ring_of(t)][0][0], live, masked);
+        };
         constexpr uint32_t H = 2 / KW;                   // steps of a tile
         if (t0 < t_end) {
             wait_own(wave, t0 + 1 < t_end);
             barrier();
-            inspect(t0, pg[0], live, masked);
+            look(t0, pg[0]);
             part_of(t0, 0, x);
             give(0, x);
         }
@@ -651,10 +746,7 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(const AttendParams p) 
             const uint32_t tn = fresh ? t + 1 : t, hn = !more ? half : last ? 0u : half + 1;
             if (fresh) wait_own(wave, H == 2 && t + 2 < t_end);
             barrier();
-            if (half == 0 && t + 2 < t_end) {
-                if (Slots && t + 3 < t_end) src.fetch_slots(t + 3);
-                src.fetch(t + 2, pg[2]);
-            }
+            if (half == 0) src.ahead(t, t_end, pg);
             gather(step, x);
             const uint32_t k0 = first_key(half);
             if (masked) {
@@ -669,7 +761,7 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(const AttendParams p) 
                         for (int i = 0; i < 4; ++i) x[u][r][i] = (on >> (key_of(u, g) + i)) & 1u ? x[u][r][i] : -INFINITY;
                 }
             }
-            if (fresh) inspect(t + 1, pg[1], live, masked);
+            if (fresh) look(t + 1, pg[1]);
 #pragma unroll
             for (int r = 0; r < R16; ++r) {
                 float top = fmaxf(fmaxf(fmaxf(x[0][r][0], x[0][r][1]), fmaxf(x[0][r][2], x[0][r][3])),
@@ -702,10 +794,10 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(const AttendParams p) 
             }
             // values: 8 keys of this lane group (4 of each half) x 16 columns
             const uint32_t vk = key_of(l16 >> 3, g) + ((l16 >> 1) & 3u);
-            const uint8_t* vrow = sh.ring + (t % kRing) * kTileBytes + (k0 + vk) * kRow + (l16 & 1u) * 8u + tw * NB * 16;
+            const uint8_t* vrow = sh.ring + ring_of(t) * kTileBytes + (k0 + vk) * kRow + (l16 & 1u) * 8u + tw * NB * 16;
             const float* scale[2];
 #pragma unroll
-            for (int u = 0; u < 2; ++u) scale[u] = &sh.scales[t % kRing][tw * T][k0 + key_of(u, g) + (l16 & 3)];
+            for (int u = 0; u < 2; ++u) scale[u] = &sh.scales[ring_of(t)][tw * T][k0 + key_of(u, g) + (l16 & 3)];
 #pragma unroll
             for (int j = 0; j < T; ++j) {
                 bf16x8 w[R16];
@@ -734,9 +826,7 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(const AttendParams p) 
             half = hn;
             if (fresh) {
                 t = tn;
-                pg[0] = pg[1];
-                pg[1] = pg[2];
-                if (!Slots) pg[2] = t + 2 < t_end ? src.page(t + 2) : -1;
+                src.turn(t, t_end, pg);
             }
         }
         barrier();    // the ring is free
@@ -771,30 +861,199 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(const AttendParams p) 
                     }
                 }
             }
-            const uint32_t row = row0 + (rw * R16 + r) * 16u + l16;
-            if (kw == 0 && row < rows) {
-                const float inv = sum[r] == 0.f ? 0.f : 1.f / sum[r];
-                const float lse2 = sum[r] == 0.f ? -INFINITY : (mx[r] == -INFINITY ? 0.f : mx[r]) + log2f(sum[r]);
-                if (whole) {
-                    const uint32_t i = row / p.heads, h = row - i * p.heads;
-                    const uint64_t t = (uint64_t)s.q0 + i;
-                    uint16_t* out = p.out + t * p.out_token + h * p.out_head + tw * NB * 16;
-#pragma unroll
-                    for (int d = 0; d < NB; ++d) {
-                        const f32x4 v = o[r][d] * inv;
-                        *(bf16x4*)(out + d * 16 + g * 4) = __builtin_convertvector(v, bf16x4);
-                    }
-                    if (p.lse && g == 0 && tw == 0) p.lse[t * p.lse_token + h] = lse2 * kLn2;
-                } else {
-                    const uint64_t at = (uint64_t)slot * M + (rw * R16 + r) * 16u + l16;
-                    float* out = p.part + at * 512 + tw * NB * 16;
-#pragma unroll
-                    for (int d = 0; d < NB; ++d) *(f32x4*)(out + d * 16 + g * 4) = o[r][d] * inv;
-                    if (g == 0 && tw == 0) p.part_lse[at] = lse2;
-                }
-            }
+            const uint32_t at = (rw * R16 + r) * 16u + l16;
+            if (kw == 0 && row0 + at < rows) write_row<M, NB>(p, seg, at, tw * NB * 16, o[r], mx[r], sum[r], g);
         }
         barrier();    // before the ring takes the next unit's tiles
+    }
+}
+
+// Many rows (units of 64).  A wave forms the scores of 16 rows and 32 keys of a
+// tile, gives their weights to LDS, and takes 32 rows' weights for one tile of 128
+// values: no score is formed twice, and a value's code is widened once for 32 rows.
+// The next tile's scores are formed beside this tile's values; one barrier a tile.
+// The maximum the weights refer to is held by all waves alike: a row that outgrows
+// it raises a flag, and all waves then agree on new ones before the weights are used.
+struct WideShared {
+    alignas(16) uint8_t ring[kRing * kTileBytes];
+    alignas(16) f32x4 weights[2][4][2][2][64];       // [tile & 1][16 rows][32 keys][half u][lane]
+    alignas(16) float scales[kRing][4][64];
+    alignas(16) int64_t slots[kSlotRing][64];
+    uint32_t flag[2];                                // [tile & 1]: a row outgrew its maximum
+};
+static_assert(sizeof(WideShared) <= 163840, "160 KB of LDS");
+
+template <bool Slots>
+__global__ __launch_bounds__(kThreads) void attend_wide_kernel(const AttendParams p) {
+    constexpr int M = 64;
+    using RowStats = float (*)[2][16];                   // [16 rows][32 keys][row]
+    __shared__ WideShared sh;
+    const uint32_t lane = threadIdx.x & 63u, l16 = lane & 15u, g = lane >> 4;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t rw = wave & 3u, kh = wave >> 2;       // scores: rows 16 rw, keys 32 kh
+    const uint32_t rp = wave & 1u, j = wave >> 1;        // values: rows 32 rp, tile j
+    const int64_t capacity = p.head->capacity;
+    Line<Slots> line(p, M, capacity <= 0, (uint8_t*)sh.weights);
+    Segment seg;
+    if (threadIdx.x < 2) sh.flag[threadIdx.x] = 0;       // seen by all after the first barrier of a segment
+    while (line.next(seg)) {
+        const Seq& s = seg.s;
+        const uint32_t t0 = seg.t0;
+        const uint32_t m = s.n > p.max_q ? p.max_q : s.n, rows = m * p.heads, row0 = seg.unit * M;
+        QFrag<4, 2> q[1];
+        uint32_t token;
+        {
+            // rows behind the last one repeat it and are not written
+            const uint32_t at = row0 + rw * 16u + l16, row = at < rows ? at : rows - 1;
+            token = row / p.heads;
+            const uint32_t h = row - token * p.heads;
+            const uint64_t t = (uint64_t)s.q0 + token;
+            q[0].load(p.q_latent + t * p.q_latent_token + h * p.q_latent_head, p.q_rope + t * p.q_rope_token + h * p.q_rope_head, g);
+        }
+        q[0].landed();
+        const View view = view_of<Slots>(p, seg, M, rows, row0);
+        const uint32_t t_end = view.t_end;
+        const Source<Slots> src{p, Slots ? nullptr : p.pages + (uint64_t)seg.b * p.pages_stride,
+                                Slots ? p.slots + (uint64_t)seg.b * p.slots_stride : nullptr, s.kv, capacity, sh.ring, sh.scales,
+                                sh.slots, wave, lane};
+        int64_t pg[3];
+        src.start(t0, t_end, pg);
+
+        f32x4 o[2][8];
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int d = 0; d < 8; ++d) o[r][d] = f32x4{0.f, 0.f, 0.f, 0.f};
+        float mx = -INFINITY, mo[2] = {-INFINITY, -INFINITY};     // of the score rows and of the value rows
+        float sum = 0.f, fresh_sum = 0.f;
+        f32x4 x[2][1];                                   // scores of the tile whose weights are given
+        uint64_t live = ~0ull;
+        bool masked = false;
+
+        auto look = [&](uint32_t t, int64_t page) {
+            inspect<Slots>(p, src, seg, view, t, page, sh.ring + ring_of(t) * kTileBytes, &sh.scales[ring_of(t)][0][0], live, masked);
+        };
+        auto scores = [&](uint32_t t, f32x4 (*to)[1]) {
+            const uint8_t* rows32 = sh.ring + ring_of(t) * kTileBytes + kh * 32 * kRow;
+            scores32<1, 4, 2>(to, rows32, rows32 + 528, &sh.scales[ring_of(t)][0][kh * 32], q, p.scale_log2, true, l16, g);
+        };
+        // masks the scores, gives their weights; raises the flag of tile t if a row outgrew its maximum
+        auto give = [&](uint32_t t) {
+            if (masked) {
+                uint64_t on = live;
+                if (!Slots) on &= sees<Slots>(p, s, token).bits(t * 64u);
+                on >>= kh * 32;
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[u][0][i] = (on >> (key_of(u, g) + i)) & 1u ? x[u][0][i] : -INFINITY;
+            }
+        };
+        auto top_of = [&]() {
+            return fmaxf(fmaxf(fmaxf(x[0][0][0], x[0][0][1]), fmaxf(x[0][0][2], x[0][0][3])),
+                         fmaxf(fmaxf(x[1][0][0], x[1][0][1]), fmaxf(x[1][0][2], x[1][0][3])));
+        };
+        auto publish = [&](uint32_t t) {
+            const float ref = mx == -INFINITY ? 0.f : mx;
+            fresh_sum = 0.f;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                f32x4 e;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    e[i] = __builtin_amdgcn_exp2f(x[u][0][i] - ref);
+                    fresh_sum += e[i];
+                }
+                sh.weights[t & 1u][rw][kh][u][lane] = e;
+            }
+        };
+        auto offer = [&](uint32_t t) {
+            give(t);
+            const float top = top_of();
+            if (__any(top > mx + kLazy || (mx == -INFINITY && top > mx)) && lane == 0) sh.flag[t & 1u] = 1;
+            publish(t);
+        };
+
+        if (t0 < t_end) {
+            wait_own(wave, t0 + 1 < t_end);
+            barrier();
+            look(t0, pg[0]);
+            scores(t0, x);
+            offer(t0);
+        }
+        for (uint32_t t = t0; t < t_end; ++t) {
+            const bool more = t + 1 < t_end;
+            if (more) wait_own(wave, false);
+            barrier();
+            src.ahead(t, t_end, pg);
+            if (__builtin_amdgcn_readfirstlane(sh.flag[t & 1u])) {
+                RowStats tops = (RowStats)sh.weights[(t + 1) & 1u];      // free until the next tile's weights
+                // new maxima, from both key halves; the weights again
+                float top = top_of();
+                top = fmaxf(top, __shfl_xor(top, 16));
+                top = fmaxf(top, __shfl_xor(top, 32));
+                if (g == 0) tops[rw][kh][l16] = top;
+                barrier();
+                if (threadIdx.x == 0) sh.flag[t & 1u] = 0;
+                const float next = fmaxf(mx, fmaxf(tops[rw][0][l16], tops[rw][1][l16]));
+                sum *= mx == -INFINITY ? 0.f : exp2f(mx - next);
+                mx = next;
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const float to = fmaxf(mo[r], fmaxf(tops[rp * 2 + r][0][l16], tops[rp * 2 + r][1][l16]));
+                    const float keep = mo[r] == -INFINITY ? 0.f : exp2f(mo[r] - to);
+                    mo[r] = to;
+#pragma unroll
+                    for (int d = 0; d < 8; ++d) o[r][d] *= keep;
+                }
+                publish(t);
+                barrier();
+            }
+            sum += fresh_sum;
+            if (more) look(t + 1, pg[1]);
+            // this tile's values; the next one's scores (behind the last tile: this one's again, not used)
+            scores(more ? t + 1 : t, x);
+            const uint32_t vk = key_of(l16 >> 3, g) + ((l16 >> 1) & 3u);
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const uint8_t* vrow = sh.ring + ring_of(t) * kTileBytes + (half * 32 + vk) * kRow + (l16 & 1u) * 8u + j * 128;
+                bf16x8 w[2];
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const f32x4 a = quads(sh.scales[ring_of(t)][j][half * 32 + key_of(u, g) + (l16 & 3)]);
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const f32x4 e = sh.weights[t & 1u][rp * 2 + r][half][u][lane];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) w[r][u * 4 + i] = (__bf16)(a[i] * e[i]);
+                    }
+                }
+#pragma unroll
+                for (int d = 0; d < 8; ++d) {
+                    const i32x2 c = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lptr<i32x2>)(vrow + d * 16));
+                    const bf16x8 v = widen(c.x, c.y);
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) o[r][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, w[r], o[r][d], 0, 0, 0);
+                }
+            }
+            if (!more) break;
+            src.turn(t + 1, t_end, pg);
+            offer(t + 1);
+        }
+        // the rows' sums, from both key halves
+        sum += __shfl_xor(sum, 16);
+        sum += __shfl_xor(sum, 32);
+        barrier();
+        RowStats sums = (RowStats)sh.weights[0];
+        if (g == 0) sums[rw][kh][l16] = sum;
+        barrier();
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const uint32_t at = (rp * 2 + r) * 16u + l16;
+            const float total = sums[rp * 2 + r][0][l16] + sums[rp * 2 + r][1][l16];
+            if (row0 + at < rows) write_row<M, 8>(p, seg, at, j * 128, o[r], mo[r], total, g);
+        }
+        barrier();    // before the ring and the sums serve the next unit
     }
 }
 
@@ -884,14 +1143,14 @@ __global__ __launch_bounds__(kThreads) void weights_kernel(const AttendParams p,
     };
     auto fetch = [&](uint32_t t, int64_t pg) {
         const uint8_t* page = p.main_base + (uint64_t)(pg < 0 ? 0 : pg) * p.main_page_stride;
-        const uint32_t to = ring + (t % kRing) * kTileBytes + wave * 1024u;
+        const uint32_t to = ring + ring_of(t) * kTileBytes + wave * 1024u;
 #pragma unroll
         for (int i = 0; i < 6; ++i) {
             if (i == 5 && wave != 0) break;
             copy16_to_lds(page + wave * 1024u + lane * 16u + i * (kWaves * 1024), to + i * (kWaves * 1024));
         }
         if (wave >= 1 && wave <= 4)
-            copy4_to_lds(page + lane * kRow + 508u + wave * 4u, lds_offset(&sh.scales[t % kRing][0][0]) + (wave - 1) * 256u);
+            copy4_to_lds(page + lane * kRow + 508u + wave * 4u, lds_offset(&sh.scales[ring_of(t)][0][0]) + (wave - 1) * 256u);
     };
 
     for (uint32_t row0 = 0; row0 < rows && t0 < t1; row0 += 128) {
@@ -923,11 +1182,11 @@ __global__ __launch_bounds__(kThreads) void weights_kernel(const AttendParams p,
                 if (row0 == 0 && threadIdx.x == 0) atomicAdd(p.invalid_count, 1ull);
                 continue;
             }
-            uint8_t* tile = sh.ring + (x % kRing) * kTileBytes;
+            uint8_t* tile = sh.ring + ring_of(x) * kTileBytes;
             const uint32_t left = s.kv - x * 64u;
             const uint64_t live = left < 64 ? (1ull << left) - 1 : ~0ull;
             const bool masked = x * 64u + 64u > clear;
-            float* scales = &sh.scales[x % kRing][0][0];
+            float* scales = &sh.scales[ring_of(x)][0][0];
             uint64_t on = ~0ull;
             if (masked) {
                 on = live & sees<false>(p, s, i).bits(x * 64u);
@@ -970,19 +1229,11 @@ __global__ __launch_bounds__(kThreads) void weights_kernel(const AttendParams p,
     }
 }
 
-template <int R16, int RW, int TW, int KW>
-hipError_t launch_shape(const AttendParams& p, uint32_t blocks, hipStream_t stream) {
-    constexpr uint32_t M = 16 * R16 * RW;
+hipError_t launch_combine(const AttendParams& p, uint32_t M, hipStream_t stream) {
     const uint64_t rows = (uint64_t)p.max_q * p.heads * p.num_seqs;
     const uint32_t joins = (uint32_t)(rows / 2 + 1 < 4096 ? rows / 2 + 1 : 4096);
-    (void)hipGetLastError();
-    if (p.by_slots) {
-        attend_kernel<R16, RW, TW, KW, true><<<dim3(blocks), dim3(kThreads), 0, stream>>>(p);
-        combine_kernel<true><<<dim3(joins), dim3(256), 0, stream>>>(p, M);
-    } else {
-        attend_kernel<R16, RW, TW, KW, false><<<dim3(blocks), dim3(kThreads), 0, stream>>>(p);
-        combine_kernel<false><<<dim3(joins), dim3(256), 0, stream>>>(p, M);
-    }
+    if (p.by_slots) combine_kernel<true><<<dim3(joins), dim3(256), 0, stream>>>(p, M);
+    else combine_kernel<false><<<dim3(joins), dim3(256), 0, stream>>>(p, M);
     return hipGetLastError();
 }
 
@@ -1015,11 +1266,20 @@ hipError_t launch_attend(const AttendParams& given, void* workspace, hipStream_t
     p.line = reinterpret_cast<uint32_t*>(ws);
     p.part_lse = reinterpret_cast<float*>(ws + a.line_bytes);
     p.part = reinterpret_cast<float*>(ws + a.line_bytes + a.lse_bytes);
-    switch (a.rows) {
-        case 16: return launch_shape<1, 1, 4, 2>(p, a.blocks, stream);
-        case 32: return launch_shape<1, 2, 2, 2>(p, a.blocks, stream);
-        default: return launch_shape<1, 4, 2, 1>(p, a.blocks, stream);
+    (void)hipGetLastError();
+    const dim3 grid(a.blocks), block(kThreads);
+    if (a.rows == 16) {
+        if (p.by_slots) attend_kernel<1, 1, 4, 2, true><<<grid, block, 0, stream>>>(p);
+        else attend_kernel<1, 1, 4, 2, false><<<grid, block, 0, stream>>>(p);
+    } else if (a.rows == 32) {
+        if (p.by_slots) attend_kernel<1, 2, 2, 2, true><<<grid, block, 0, stream>>>(p);
+        else attend_kernel<1, 2, 2, 2, false><<<grid, block, 0, stream>>>(p);
+    } else {
+        if (p.by_slots) attend_wide_kernel<true><<<grid, block, 0, stream>>>(p);
+        else attend_wide_kernel<false><<<grid, block, 0, stream>>>(p);
     }
+    const hipError_t e = hipGetLastError();
+    return e != hipSuccess ? e : launch_combine(p, a.rows, stream);
 }
 
 hipError_t launch_attend_weights(const AttendParams& p, hipStream_t stream) {
