@@ -668,8 +668,6 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(const AttendParams p) 
                       p.q_rope + t * p.q_rope_token + h * p.q_rope_head + (TW == 1 ? 0 : (tw & 1) * 32), g);
             token[r] = i;
         }
-#pragma unroll
-        for (int r = 0; r < R16; ++r) q[r].landed();
         const View view = view_of<Slots>(p, seg, M, rows, row0);
         const uint32_t t_end = view.t_end;
 
@@ -688,6 +686,9 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(const AttendParams p) 
                                 Slots ? p.slots + (uint64_t)b * p.slots_stride : nullptr, s.kv, capacity, sh.ring, sh.scales, sh.slots, wave, lane};
         int64_t pg[3];                                   // pages of tiles t, t + 1, t + 2
         src.start(t0, t_end, pg);
+#pragma unroll
+        for (int r = 0; r < R16; ++r) q[r].landed();
+        __builtin_amdgcn_sched_barrier(0);
         auto first_key = [&](uint32_t half) { return (KW == 2 ? kw : half) * 32u; };
         // this wave's part of the scores of a step
         auto part_of = [&](uint32_t t, uint32_t half, f32x4 (*x)[R16]) {
@@ -910,7 +911,6 @@ __global__ __launch_bounds__(kThreads) void attend_wide_kernel(const AttendParam
             const uint64_t t = (uint64_t)s.q0 + token;
             q[0].load(p.q_latent + t * p.q_latent_token + h * p.q_latent_head, p.q_rope + t * p.q_rope_token + h * p.q_rope_head, g);
         }
-        q[0].landed();
         const View view = view_of<Slots>(p, seg, M, rows, row0);
         const uint32_t t_end = view.t_end;
         const Source<Slots> src{p, Slots ? nullptr : p.pages + (uint64_t)seg.b * p.pages_stride,
@@ -918,6 +918,7 @@ __global__ __launch_bounds__(kThreads) void attend_wide_kernel(const AttendParam
                                 sh.slots, wave, lane};
         int64_t pg[3];
         src.start(t0, t_end, pg);
+        q[0].landed();
 
         f32x4 o[2][8];
 #pragma unroll
@@ -1102,129 +1103,119 @@ __global__ __launch_bounds__(256) void combine_kernel(const AttendParams p, uint
 // ---- accumulated weights ------------------------------------------------------------
 
 // A block takes up to kWeightTiles tiles of one sequence and passes over its
-// query rows, 128 at a time (16 a wave, the operands in registers).  A position
-// belongs to one block: its sum over rows runs lane by lane (DPP over the 16
-// rows of a lane group), pass by pass and wave by wave, always in that order.
-// Bound by reading the rows, once per 128 query rows.
+// query rows, 128 at a time: 4 waves of 32 rows for either half of a tile's keys,
+// the operands in registers.  A position belongs to one block: its sum over rows
+// runs within a wave (DPP over the 16 rows of a lane group), pass by pass and wave
+// by wave, always in that order.  Bound by the vector unit: 4 instructions widen 8
+// codes for 32 rows.
 constexpr uint32_t kWeightTiles = 16;
 
 struct WeightShared {
     alignas(16) uint8_t ring[kRing * kTileBytes];
     alignas(16) float scales[kRing][4][64];
-    float sums[kWaves][kWeightTiles * 64];
+    float sums[4][kWeightTiles * 64];                // [rows][position]
 };
 
 // Sum over the 16 lanes of a row: every lane gets it.
-__device__ __forceinline__ float sum16(float v) {
-    v += __shfl_xor(v, 1);
-    v += __shfl_xor(v, 2);
-    v += __shfl_xor(v, 4);
-    return v + __shfl_xor(v, 8);
+template <int R>
+__device__ __forceinline__ float rotate_add(float v) {      // row_ror:R
+    return v + __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x120 + R, 15, 15, true));
 }
+__device__ __forceinline__ float sum16(float v) { return rotate_add<1>(rotate_add<2>(rotate_add<4>(rotate_add<8>(v)))); }
 
 __global__ __launch_bounds__(kThreads) void weights_kernel(const AttendParams p, uint32_t run) {
     __shared__ WeightShared sh;
     const uint32_t lane = threadIdx.x & 63u, l16 = lane & 15u, g = lane >> 4;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const uint32_t b = p.first_seq + blockIdx.y, t0 = blockIdx.x * run;
+    const uint32_t rw = wave & 3u, kh = wave >> 2;       // rows 32 rw of a pass, keys 32 kh of a tile
     const int64_t capacity = p.head->capacity;
-    const Seq s = sequence<false, true>(p, b, 128, capacity <= 0);
-    const uint32_t tiles = s.kv ? s.tiles : 0u;
+    Segment seg;
+    seg.b = p.first_seq + blockIdx.y;
+    seg.s = sequence<false, true>(p, seg.b, 128, capacity <= 0);
+    const Seq& s = seg.s;
+    const uint32_t t0 = blockIdx.x * run, tiles = s.kv ? s.tiles : 0u;
     const uint32_t t1 = t0 + run < tiles ? t0 + run : tiles;
     const uint32_t m = s.n > p.max_q ? p.max_q : s.n, rows = m * p.heads;
-    for (uint32_t i = threadIdx.x; i < kWaves * kWeightTiles * 64; i += kThreads) (&sh.sums[0][0])[i] = 0.f;
-    const int32_t* table = p.pages + (uint64_t)b * p.pages_stride;
+    for (uint32_t i = threadIdx.x; i < 4 * kWeightTiles * 64; i += kThreads) (&sh.sums[0][0])[i] = 0.f;
     const int64_t base = (int64_t)s.kv - s.n;
-    const uint32_t clear = base < 0 ? 0u : (uint32_t)(p.tree ? base : base + 1);   // every token sees those
-    const uint32_t ring = lds_offset(sh.ring);
-    auto page = [&](uint32_t t) -> int64_t {
-        const int64_t v = t < t1 ? uniform_load(table, t) : -1;
-        return v >= 0 && v < capacity / 64 ? v : -1;
-    };
-    auto fetch = [&](uint32_t t, int64_t pg) {
-        const uint8_t* page = p.main_base + (uint64_t)(pg < 0 ? 0 : pg) * p.main_page_stride;
-        const uint32_t to = ring + ring_of(t) * kTileBytes + wave * 1024u;
-#pragma unroll
-        for (int i = 0; i < 6; ++i) {
-            if (i == 5 && wave != 0) break;
-            copy16_to_lds(page + wave * 1024u + lane * 16u + i * (kWaves * 1024), to + i * (kWaves * 1024));
-        }
-        if (wave >= 1 && wave <= 4)
-            copy4_to_lds(page + lane * kRow + 508u + wave * 4u, lds_offset(&sh.scales[ring_of(t)][0][0]) + (wave - 1) * 256u);
-    };
+    View view;                                           // every token sees the positions below `clear`
+    view.clear = base < 0 ? 0u : (uint32_t)(p.tree ? base : base + 1);
+    view.t_end = t1;
+    const Source<false> src{p, p.pages + (uint64_t)seg.b * p.pages_stride, nullptr, s.kv, capacity, sh.ring, sh.scales, nullptr, wave, lane};
 
     for (uint32_t row0 = 0; row0 < rows && t0 < t1; row0 += 128) {
-        const uint32_t at = row0 + wave * 16u + l16, row = at < rows ? at : rows - 1;
-        const uint32_t i = row / p.heads, h = row - i * p.heads;
-        const uint64_t t = (uint64_t)s.q0 + i;
-        QFrag<4, 2> q[1];
-        q[0].load(p.q_latent + t * p.q_latent_token + h * p.q_latent_head,
-                  p.q_rope + t * p.q_rope_token + h * p.q_rope_head, g);
-        q[0].landed();
-        const float lse = p.lse[t * p.lse_token + h];
-        // a row of -inf saw nothing; rows behind the last one add nothing
-        const bool adds = at < rows && lse != -INFINITY;
-        float lse2 = adds ? lse * 1.44269504088896341f : INFINITY;
-        asm volatile("" : "+v"(lse2));
-        barrier();                        // the ring is free
-        int64_t pg[3] = {page(t0), page(t0 + 1), page(t0 + 2)};
-        fetch(t0, pg[0]);
-        if (t0 + 1 < t1) fetch(t0 + 1, pg[1]);
-        for (uint32_t x = t0; x < t1; ++x) {
-            wait_own(wave, x + 1 < t1);
+        seg.unit = row0;                                 // bad pages are counted in the first pass
+        QFrag<4, 2> q[2];
+        uint32_t token[2];
+        float lse2[2];
+        bool adds[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const uint32_t at = row0 + rw * 32u + r * 16u + l16, row = at < rows ? at : rows - 1;
+            token[r] = row / p.heads;
+            const uint32_t h = row - token[r] * p.heads;
+            const uint64_t t = (uint64_t)s.q0 + token[r];
+            q[r].load(p.q_latent + t * p.q_latent_token + h * p.q_latent_head, p.q_rope + t * p.q_rope_token + h * p.q_rope_head, g);
+            // a row of -inf saw nothing; rows behind the last one add nothing
+            const float lse = p.lse[t * p.lse_token + h];
+            adds[r] = at < rows && lse != -INFINITY;
+            lse2[r] = lse * 1.44269504088896341f;
+        }
+        barrier();                                       // the ring is free
+        int64_t pg[3];
+        src.start(t0, t1, pg);
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            q[r].landed();
+            asm volatile("" : "+v"(lse2[r]));
+        }
+        for (uint32_t t = t0; t < t1; ++t) {
+            wait_own(wave, t + 1 < t1);
             barrier();
-            if (x + 2 < t1) fetch(x + 2, pg[2]);
-            const int64_t now = pg[0];
-            pg[0] = pg[1];
-            pg[1] = pg[2];
-            pg[2] = page(x + 3);
-            if (now < 0) {
-                if (row0 == 0 && threadIdx.x == 0) atomicAdd(p.invalid_count, 1ull);
-                continue;
-            }
-            uint8_t* tile = sh.ring + ring_of(x) * kTileBytes;
-            const uint32_t left = s.kv - x * 64u;
-            const uint64_t live = left < 64 ? (1ull << left) - 1 : ~0ull;
-            const bool masked = x * 64u + 64u > clear;
-            float* scales = &sh.scales[ring_of(x)][0][0];
-            uint64_t on = ~0ull;
+            src.ahead(t, t1, pg);
+            uint8_t* tile = sh.ring + ring_of(t) * kTileBytes;
+            float* scales = &sh.scales[ring_of(t)][0][0];
+            uint64_t live;
+            bool masked;
+            inspect<false>(p, src, seg, view, t, pg[0], tile, scales, live, masked);
+            src.turn(t + 1, t1, pg);
+            f32x4 x[2][2];
+            const uint8_t* rows32 = tile + kh * 32 * kRow;
+            scores32<2, 4, 2>(x, rows32, rows32 + 528, scales + kh * 32, q, p.scale_log2, true, l16, g);
             if (masked) {
-                on = live & sees<false>(p, s, i).bits(x * 64u);
-                clean_tile(tile, scales, live);
-            }
-#pragma unroll 1
-            for (uint32_t half = 0; half < 2; ++half) {
-                f32x4 v[2][1];
-                const uint8_t* rows32 = tile + half * 32 * kRow;
-                scores32<1, 4, 2>(v, rows32, rows32 + 528, scales + half * 32, q, p.scale_log2, true, l16, g);
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    if (masked) {
+                for (int r = 0; r < 2; ++r) {
+                    const uint64_t on = (live & sees<false>(p, s, token[r]).bits(t * 64u)) >> (kh * 32);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            v[u][0][k] = (on >> (half * 32 + key_of(u, g) + k)) & 1u ? v[u][0][k] : -INFINITY;
-                    }
-                    float keep = 0.f;
+                    for (int u = 0; u < 2; ++u)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float w = adds ? __builtin_amdgcn_exp2f(v[u][0][k] - lse2) : 0.f;
-                        const float total = sum16(w);
-                        keep = (int)l16 == k ? total : keep;
-                    }
-                    if (l16 < 4) sh.sums[wave][(x - t0) * 64 + half * 32 + key_of(u, g) + l16] += keep;
+                        for (int i = 0; i < 4; ++i) x[u][r][i] = (on >> (key_of(u, g) + i)) & 1u ? x[u][r][i] : -INFINITY;
                 }
+            }
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                float keep = 0.f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float w = 0.f;
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const float e = __builtin_amdgcn_exp2f(x[u][r][i] - lse2[r]);
+                        w += adds[r] ? e : 0.f;
+                    }
+                    const float total = sum16(w);
+                    keep = (int)l16 == i ? total : keep;
+                }
+                if (l16 < 4) sh.sums[rw][(t - t0) * 64 + kh * 32 + key_of(u, g) + l16] += keep;
             }
         }
     }
-    barrier();
     __syncthreads();
-    const uint32_t end = t0 + run;
-    for (uint32_t k = threadIdx.x; k < (end - t0) * 64u; k += kThreads) {
+    for (uint32_t k = threadIdx.x; k < run * 64u; k += kThreads) {
         const uint32_t pos = t0 * 64u + k;
         if (pos >= p.max_kv) break;
-        const uint64_t at = (uint64_t)b * p.weights_stride + pos;
-        float v = 0.f;
-        for (uint32_t w = 0; w < kWaves; ++w) v += sh.sums[w][k];
+        const uint64_t at = (uint64_t)seg.b * p.weights_stride + pos;
+        const float v = (sh.sums[0][k] + sh.sums[1][k]) + (sh.sums[2][k] + sh.sums[3][k]);
         p.weights_out[at] = (p.weights_in ? p.weights_in[at] : 0.f) + v;
     }
 }
