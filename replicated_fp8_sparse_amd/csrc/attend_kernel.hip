@@ -637,15 +637,15 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(const AttendParams p) 
     static_assert(RW * KW * TW == kWaves, "every wave has its part");
     constexpr int M = 16 * R16 * RW;
     constexpr int T = 4 / TW;                       // tiles of 128 of a wave
-    constexpr int P = TW == 1 ? 2 : 1;              // RoPE halves of a wave
+    constexpr int P = 1;                            // RoPE halves of a wave
     constexpr int NB = 8 * T;                       // 16-column blocks of a wave
-    static_assert(TW == 1 || 2 * kWaves * R16 * 2048 <= kExchange, "partial scores of two steps");
+    static_assert(2 * kWaves * R16 * 2048 <= kExchange, "partial scores of two steps");
     static_assert(KW == 1 || kWaves / 2 * R16 * (NB * 1024 + 512) <= kRing * kTileBytes + kExchange, "join of key halves");
     __shared__ Shared sh;
     const uint32_t lane = threadIdx.x & 63u, l16 = lane & 15u, g = lane >> 4;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t rw = wave % RW, kw = (wave / RW) % KW, tw = wave / (RW * KW);
-    const bool ropes = TW == 1 || tw < 2;           // RoPE half tw
+    const bool ropes = tw < 2;                      // RoPE half tw
     const int64_t capacity = p.head->capacity;
     Line<Slots> line(p, M, capacity <= 0, sh.exchange);
     Segment seg;
@@ -665,7 +665,7 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(const AttendParams p) 
             const uint32_t i = row / p.heads, h = row - i * p.heads;
             const uint64_t t = (uint64_t)s.q0 + i;
             q[r].load(p.q_latent + t * p.q_latent_token + h * p.q_latent_head + tw * T * 128,
-                      p.q_rope + t * p.q_rope_token + h * p.q_rope_head + (TW == 1 ? 0 : (tw & 1) * 32), g);
+                      p.q_rope + t * p.q_rope_token + h * p.q_rope_head + (tw & 1) * 32, g);
             token[r] = i;
         }
         const View view = view_of<Slots>(p, seg, M, rows, row0);
@@ -694,12 +694,11 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(const AttendParams p) 
         auto part_of = [&](uint32_t t, uint32_t half, f32x4 (*x)[R16]) {
             const uint32_t k0 = first_key(half);
             const uint8_t* rows32 = sh.ring + ring_of(t) * kTileBytes + k0 * kRow;
-            scores32<R16, T, P>(x, rows32 + tw * T * 128, rows32 + 528 + (TW == 1 ? 0 : (tw & 1) * 64),
+            scores32<R16, T, P>(x, rows32 + tw * T * 128, rows32 + 528 + (tw & 1) * 64,
                                 &sh.scales[ring_of(t)][tw * T][k0], q, p.scale_log2, ropes, l16, g);
         };
         f32x4* const part = (f32x4*)sh.exchange + lane;  // [step & 1][wave][half u][r][lane]
         auto give = [&](uint32_t step, f32x4 (*x)[R16]) {
-            if (TW == 1) return;
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -714,7 +713,7 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(const AttendParams p) 
                     const f32x4* from = part + ((((step & 1u) * kWaves + wave) * 2 + u) * R16 + r) * 64;
                     if (TW == 2) {
                         x[u][r] += from[(int)((wave ^ (RW * KW)) - wave) * 2 * R16 * 64];
-                    } else if (TW > 2) {
+                    } else {
                         from -= tw * RW * KW * 2 * R16 * 64;
                         f32x4 total = from[0];
 #pragma unroll
@@ -938,18 +937,6 @@ __global__ __launch_bounds__(kThreads) void attend_wide_kernel(const AttendParam
             const uint8_t* rows32 = sh.ring + ring_of(t) * kTileBytes + kh * 32 * kRow;
             scores32<1, 4, 2>(to, rows32, rows32 + 528, &sh.scales[ring_of(t)][0][kh * 32], q, p.scale_log2, true, l16, g);
         };
-        // masks the scores, gives their weights; raises the flag of tile t if a row outgrew its maximum
-        auto give = [&](uint32_t t) {
-            if (masked) {
-                uint64_t on = live;
-                if (!Slots) on &= sees<Slots>(p, s, token).bits(t * 64u);
-                on >>= kh * 32;
-#pragma unroll
-                for (int u = 0; u < 2; ++u)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) x[u][0][i] = (on >> (key_of(u, g) + i)) & 1u ? x[u][0][i] : -INFINITY;
-            }
-        };
         auto top_of = [&]() {
             return fmaxf(fmaxf(fmaxf(x[0][0][0], x[0][0][1]), fmaxf(x[0][0][2], x[0][0][3])),
                          fmaxf(fmaxf(x[1][0][0], x[1][0][1]), fmaxf(x[1][0][2], x[1][0][3])));
@@ -968,8 +955,17 @@ __global__ __launch_bounds__(kThreads) void attend_wide_kernel(const AttendParam
                 sh.weights[t & 1u][rw][kh][u][lane] = e;
             }
         };
+        // masks tile t's scores and gives their weights; raises its flag if a row outgrew its maximum
         auto offer = [&](uint32_t t) {
-            give(t);
+            if (masked) {
+                uint64_t on = live;
+                if (!Slots) on &= sees<Slots>(p, s, token).bits(t * 64u);
+                on >>= kh * 32;
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[u][0][i] = (on >> (key_of(u, g) + i)) & 1u ? x[u][0][i] : -INFINITY;
+            }
             const float top = top_of();
             if (__any(top > mx + kLazy || (mx == -INFINITY && top > mx)) && lane == 0) sh.flag[t & 1u] = 1;
             publish(t);
@@ -1242,6 +1238,7 @@ AttendPlan plan_attend(uint64_t rows, uint64_t num_seqs, uint64_t num_tokens, ui
     a.least = 2;
     const uint64_t runs = units * ((tiles + a.least - 1) / a.least) + 1;
     a.blocks = (uint32_t)(units >= 256 || runs >= 256 ? 256 : runs);
+    a.wide = a.rows == 64 && units * tiles >= 16ull * a.blocks;
     a.line_bytes = ((num_seqs + 1) * 4 + 255) / 256 * 256;
     a.lse_bytes = (uint64_t)a.blocks * 2 * a.rows * 4;
     a.bytes = a.line_bytes + a.lse_bytes + (uint64_t)a.blocks * 2 * a.rows * 512 * 4;
@@ -1265,6 +1262,9 @@ hipError_t launch_attend(const AttendParams& given, void* workspace, hipStream_t
     } else if (a.rows == 32) {
         if (p.by_slots) attend_kernel<1, 2, 2, 2, true><<<grid, block, 0, stream>>>(p);
         else attend_kernel<1, 2, 2, 2, false><<<grid, block, 0, stream>>>(p);
+    } else if (!a.wide) {
+        if (p.by_slots) attend_kernel<1, 4, 2, 1, true><<<grid, block, 0, stream>>>(p);
+        else attend_kernel<1, 4, 2, 1, false><<<grid, block, 0, stream>>>(p);
     } else {
         if (p.by_slots) attend_wide_kernel<true><<<grid, block, 0, stream>>>(p);
         else attend_wide_kernel<false><<<grid, block, 0, stream>>>(p);
