@@ -64,7 +64,7 @@ static_assert(sizeof(Shared) <= 163840, "160 KB of LDS");
 // Tile t's place in the ring; opaque, so that addresses stay a base and immediate
 // offsets instead of one induction variable each.
 __device__ __forceinline__ uint32_t ring_of(uint32_t t) {
-    uint32_t r = t % kRing;
+    uint32_t r = __builtin_amdgcn_readfirstlane(t % kRing);
     asm("" : "+s"(r));
     return r;
 }
@@ -1010,28 +1010,54 @@ __global__ __launch_bounds__(kThreads) void attend_wide_kernel(const AttendParam
             if (more) look(t + 1, pg[1]);
             // this tile's values; the next one's scores (behind the last tile: this one's again, not used)
             scores(more ? t + 1 : t, x);
+            // Read in this order, each code four steps ahead of its use: left to itself
+            // the compiler waits for every read right behind it.
+            __builtin_amdgcn_sched_barrier(0);
             const uint32_t vk = key_of(l16 >> 3, g) + ((l16 >> 1) & 3u);
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const uint8_t* vrow = sh.ring + ring_of(t) * kTileBytes + (half * 32 + vk) * kRow + (l16 & 1u) * 8u + j * 128;
-                bf16x8 w[2];
+            const uint8_t* vrow = sh.ring + ring_of(t) * kTileBytes + vk * kRow + (l16 & 1u) * 8u + j * 128;
+            auto column = [&](int n) {                   // 32 keys of half n / 8 by 16 columns n % 8
+                return __builtin_amdgcn_ds_read_tr8_b64_v2i32((lptr<i32x2>)(vrow + (n >> 3) * (32 * kRow) + (n & 7) * 16));
+            };
+            f32x4 e[2][2];
+            float a[2];
+            auto read_weights = [&](int half) {
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    const f32x4 a = quads(sh.scales[ring_of(t)][j][half * 32 + key_of(u, g) + (l16 & 3)]);
+                    a[u] = sh.scales[ring_of(t)][j][half * 32 + key_of(u, g) + (l16 & 3)];
 #pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        const f32x4 e = sh.weights[t & 1u][rp * 2 + r][half][u][lane];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) w[r][u * 4 + i] = (__bf16)(a[i] * e[i]);
-                    }
+                    for (int r = 0; r < 2; ++r) e[u][r] = sh.weights[t & 1u][rp * 2 + r][half][u][lane];
                 }
+            };
+            bf16x8 w[2];
+            auto scale_weights = [&]() {
 #pragma unroll
-                for (int d = 0; d < 8; ++d) {
-                    const i32x2 c = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lptr<i32x2>)(vrow + d * 16));
-                    const bf16x8 v = widen(c.x, c.y);
+                for (int u = 0; u < 2; ++u) {
+                    const f32x4 s4 = quads(a[u]);
 #pragma unroll
-                    for (int r = 0; r < 2; ++r) o[r][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, w[r], o[r][d], 0, 0, 0);
+                    for (int r = 0; r < 2; ++r)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) w[r][u * 4 + i] = (__bf16)(s4[i] * e[u][r][i]);
                 }
+            };
+            i32x2 c[4];
+            read_weights(0);
+#pragma unroll
+            for (int n = 0; n < 4; ++n) c[n] = column(n);
+            __builtin_amdgcn_sched_barrier(0);
+            scale_weights();
+            bf16x8 v = widen(c[0].x, c[0].y);
+#pragma unroll
+            for (int n = 0; n < 16; ++n) {
+                bf16x8 next = v;
+                if (n + 4 < 16) c[n & 3] = column(n + 4);
+                if (n == 3) read_weights(1);
+                __builtin_amdgcn_sched_barrier(0);
+                if (n < 15) next = widen(c[(n + 1) & 3].x, c[(n + 1) & 3].y);
+#pragma unroll
+                for (int r = 0; r < 2; ++r) o[r][n & 7] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, w[r], o[r][n & 7], 0, 0, 0);
+                if (n == 7) scale_weights();
+                v = next;
+                __builtin_amdgcn_sched_barrier(0);
             }
             if (!more) break;
             src.turn(t + 1, t_end, pg);
