@@ -1301,8 +1301,8 @@ hipError_t launch_attend(const AttendParams& given, void* workspace, hipStream_t
 
 hipError_t launch_attend_weights(const AttendParams& p, hipStream_t stream) {
     const uint32_t tiles = (p.max_kv + 63) / 64;
-    // runs long enough to fill the card about twice, up to what a block's sums hold
-    uint64_t run = ((uint64_t)tiles * p.num_seqs + 511) / 512;
+    // runs that fill the card once, up to what a block's sums hold
+    uint64_t run = ((uint64_t)tiles * p.num_seqs + 255) / 256;
     run = run < 1 ? 1 : run > kWeightTiles ? kWeightTiles : run;
     const uint32_t blocks = (uint32_t)((tiles + run - 1) / run);
     (void)hipGetLastError();
