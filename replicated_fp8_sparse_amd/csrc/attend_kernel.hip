@@ -283,7 +283,7 @@ struct Place {
 
 // Where this block's run begins, from prefix sums of the sequences' work: by each
 // wave alone up to 64 sequences, else by the whole block.  Block 0 leaves the
-// prefixes and the share for combine_kernel.
+// prefixes and the share for combine_kernel, where there is one.
 __device__ __forceinline__ Place place(const AttendParams& p, uint32_t M, bool empty, uint8_t* scratch) {
     const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = tid >> 6;
     const bool first_block = blockIdx.x == 0;
@@ -301,7 +301,7 @@ __device__ __forceinline__ Place place(const AttendParams& p, uint32_t M, bool e
         const uint64_t here = __ballot(w && at >= first && at < x);
         r.b = here ? (uint32_t)__builtin_ctzll(here) : 0u;
         r.off = at - __builtin_amdgcn_readlane(first, r.b);
-        if (first_block && tid < p.num_seqs) p.line[tid] = first;
+        if (p.line && first_block && tid < p.num_seqs) p.line[tid] = first;
     } else {
         uint32_t* scan = (uint32_t*)scratch;
         uint32_t carry = 0, at = 0;
@@ -324,7 +324,7 @@ __device__ __forceinline__ Place place(const AttendParams& p, uint32_t M, bool e
                     carry += scan[v];
                 }
                 const uint32_t first = before + x - w;
-                if (pass == 0 && first_block && b < p.num_seqs) p.line[b] = first;
+                if (p.line && pass == 0 && first_block && b < p.num_seqs) p.line[b] = first;
                 if (pass == 1 && w && at >= first && at < first + w) {
                     scan[kWaves] = b;
                     scan[kWaves + 1] = at - first;
@@ -374,7 +374,7 @@ struct Line {
         b = __builtin_amdgcn_readfirstlane(at.b);      // the same for the block: kept in scalar registers
         off = __builtin_amdgcn_readfirstlane(at.off);
         const uint32_t each = __builtin_amdgcn_readfirstlane(at.each), total = __builtin_amdgcn_readfirstlane(at.total);
-        if (blockIdx.x == 0 && threadIdx.x == 0) p.line[p.num_seqs] = each;
+        if (p.line && blockIdx.x == 0 && threadIdx.x == 0) p.line[p.num_seqs] = each;
         pos = begin = each * blockIdx.x;
         end = begin + each < total ? begin + each : total;
     }
@@ -1124,9 +1124,10 @@ __global__ __launch_bounds__(256) void combine_kernel(const AttendParams p, uint
 
 // ---- accumulated weights ------------------------------------------------------------
 
-// A block takes up to kWeightTiles tiles of one sequence and passes over its
-// query rows, 128 at a time: 4 waves of 32 rows for either half of a tile's keys,
-// the operands in registers.  A position belongs to one block: its sum over rows
+// A block takes its run of the line of all sequences' tiles (a unit: all rows of a
+// sequence), up to kWeightTiles of one sequence at a time, and passes over the
+// sequence's query rows, 128 at a time: 4 waves of 32 rows for either half of a
+// tile's keys, the operands in registers.  A position belongs to one block: its sum over rows
 // runs within a wave (DPP over the 16 rows of a lane group), pass by pass and wave
 // by wave, always in that order.  Bound by the vector unit: 4 instructions widen 8
 // codes for 32 rows.
@@ -1145,100 +1146,126 @@ __device__ __forceinline__ float rotate_add(float v) {      // row_ror:R
 }
 __device__ __forceinline__ float sum16(float v) { return rotate_add<1>(rotate_add<2>(rotate_add<4>(rotate_add<8>(v)))); }
 
-__global__ __launch_bounds__(kThreads) void weights_kernel(const AttendParams p, uint32_t run) {
+__device__ __forceinline__ void add_weights(const AttendParams& p, uint32_t b, uint32_t pos, float v) {
+    const uint64_t at = (uint64_t)b * p.weights_stride + pos;
+    p.weights_out[at] = (p.weights_in ? p.weights_in[at] : 0.f) + v;
+}
+
+__global__ __launch_bounds__(kThreads) void weights_kernel(const AttendParams p) {
     __shared__ WeightShared sh;
     const uint32_t lane = threadIdx.x & 63u, l16 = lane & 15u, g = lane >> 4;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t rw = wave & 3u, kh = wave >> 2;       // rows 32 rw of a pass, keys 32 kh of a tile
+    const uint32_t M = p.max_q * p.heads;                // one unit a sequence
     const int64_t capacity = p.head->capacity;
-    Segment seg;
-    seg.b = p.first_seq + blockIdx.y;
-    seg.s = sequence<false, true>(p, seg.b, 128, capacity <= 0);
-    const Seq& s = seg.s;
-    const uint32_t t0 = blockIdx.x * run, tiles = s.kv ? s.tiles : 0u;
-    const uint32_t t1 = t0 + run < tiles ? t0 + run : tiles;
-    const uint32_t m = s.n > p.max_q ? p.max_q : s.n, rows = m * p.heads;
-    for (uint32_t i = threadIdx.x; i < 4 * kWeightTiles * 64; i += kThreads) (&sh.sums[0][0])[i] = 0.f;
-    const int64_t base = (int64_t)s.kv - s.n;
-    View view;                                           // every token sees the positions below `clear`
-    view.clear = base < 0 ? 0u : (uint32_t)(p.tree ? base : base + 1);
-    view.t_end = t1;
-    const Source<false> src{p, p.pages + (uint64_t)seg.b * p.pages_stride, nullptr, s.kv, capacity, sh.ring, sh.scales, nullptr, wave, lane};
 
-    for (uint32_t row0 = 0; row0 < rows && t0 < t1; row0 += 128) {
-        seg.unit = row0;                                 // bad pages are counted in the first pass
-        QFrag<4, 2> q[2];
-        uint32_t token[2];
-        float lse2[2];
-        bool adds[2];
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const uint32_t at = row0 + rw * 32u + r * 16u + l16, row = at < rows ? at : rows - 1;
-            token[r] = row / p.heads;
-            const uint32_t h = row - token[r] * p.heads;
-            const uint64_t t = (uint64_t)s.q0 + token[r];
-            q[r].load(p.q_latent + t * p.q_latent_token + h * p.q_latent_head, p.q_rope + t * p.q_rope_token + h * p.q_rope_head, g);
-            // a row of -inf saw nothing; rows behind the last one add nothing
-            const float lse = p.lse[t * p.lse_token + h];
-            adds[r] = at < rows && lse != -INFINITY;
-            lse2[r] = lse * 1.44269504088896341f;
+    // positions that no tile of the line holds, 1024 at a time: nothing is added
+    const uint32_t spans = (p.max_kv + 1023) / 1024;
+    for (uint64_t i = blockIdx.x; i < (uint64_t)spans * p.num_seqs; i += gridDim.x) {
+        const uint32_t b = (uint32_t)(i / spans), from = (uint32_t)(i - (uint64_t)b * spans) * 1024u;
+        uint32_t held = 0;
+        if (p.num_tokens) {
+            const Seq s = sequence<false, true>(p, b, M, capacity <= 0);
+            held = s.units * s.tiles * 64u;
         }
-        barrier();                                       // the ring is free
-        int64_t pg[3];
-        src.start(t0, t1, pg);
+        const uint32_t end = from + 1024u < p.max_kv ? from + 1024u : p.max_kv;
+        for (uint32_t pos = (from < held ? held : from) + threadIdx.x; pos < end; pos += kThreads) add_weights(p, b, pos, 0.f);
+    }
+    if (!p.num_tokens) return;
+
+    Line<false> line(p, M, capacity <= 0, (uint8_t*)sh.sums);
+    Segment seg;
+    uint32_t t1 = 0;
+    bool left = line.next(seg);
+    while (left) {
+        const Seq& s = seg.s;
+        const uint32_t t0 = seg.t0;
+        t1 = seg.t1 < t0 + kWeightTiles ? seg.t1 : t0 + kWeightTiles;
+        const uint32_t end = s.kv ? t1 : t0;                 // a sequence without positions has one empty tile
+        const uint32_t m = s.n > p.max_q ? p.max_q : s.n, rows = m * p.heads;
+        for (uint32_t i = threadIdx.x; i < 4 * kWeightTiles * 64; i += kThreads) (&sh.sums[0][0])[i] = 0.f;
+        const int64_t base = (int64_t)s.kv - s.n;
+        View view;                                           // every token sees the positions below `clear`
+        view.clear = base < 0 ? 0u : (uint32_t)(p.tree ? base : base + 1);
+        view.t_end = end;
+        const Source<false> src{p, p.pages + (uint64_t)seg.b * p.pages_stride, nullptr, s.kv, capacity, sh.ring, sh.scales, nullptr, wave, lane};
+
+        for (uint32_t row0 = 0; row0 < rows && t0 < end; row0 += 128) {
+            seg.unit = row0;                                 // bad pages are counted in the first pass
+            QFrag<4, 2> q[2];
+            uint32_t token[2];
+            float lse2[2];
+            bool adds[2];
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            q[r].landed();
-            asm volatile("" : "+v"(lse2[r]));
-        }
-        for (uint32_t t = t0; t < t1; ++t) {
-            wait_own(wave, t + 1 < t1);
-            barrier();
-            src.ahead(t, t1, pg);
-            uint8_t* tile = sh.ring + ring_of(t) * kTileBytes;
-            float* scales = &sh.scales[ring_of(t)][0][0];
-            uint64_t live;
-            bool masked;
-            inspect<false>(p, src, seg, view, t, pg[0], tile, scales, live, masked);
-            src.turn(t + 1, t1, pg);
-            f32x4 x[2][2];
-            const uint8_t* rows32 = tile + kh * 32 * kRow;
-            scores32<2, 4, 2>(x, rows32, rows32 + 528, scales + kh * 32, q, p.scale_log2, true, l16, g);
-            if (masked) {
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const uint64_t on = (live & sees<false>(p, s, token[r]).bits(t * 64u)) >> (kh * 32);
-#pragma unroll
-                    for (int u = 0; u < 2; ++u)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) x[u][r][i] = (on >> (key_of(u, g) + i)) & 1u ? x[u][r][i] : -INFINITY;
-                }
+            for (int r = 0; r < 2; ++r) {
+                const uint32_t at = row0 + rw * 32u + r * 16u + l16, row = at < rows ? at : rows - 1;
+                token[r] = row / p.heads;
+                const uint32_t h = row - token[r] * p.heads;
+                const uint64_t t = (uint64_t)s.q0 + token[r];
+                q[r].load(p.q_latent + t * p.q_latent_token + h * p.q_latent_head, p.q_rope + t * p.q_rope_token + h * p.q_rope_head, g);
+                // a row of -inf saw nothing; rows behind the last one add nothing
+                const float lse = p.lse[t * p.lse_token + h];
+                adds[r] = at < rows && lse != -INFINITY;
+                lse2[r] = lse * 1.44269504088896341f;
             }
+            barrier();                                       // the ring is free
+            int64_t pg[3];
+            src.start(t0, end, pg);
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                float keep = 0.f;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float w = 0.f;
+            for (int r = 0; r < 2; ++r) {
+                q[r].landed();
+                asm volatile("" : "+v"(lse2[r]));
+            }
+            for (uint32_t t = t0; t < end; ++t) {
+                wait_own(wave, t + 1 < end);
+                barrier();
+                src.ahead(t, end, pg);
+                uint8_t* tile = sh.ring + ring_of(t) * kTileBytes;
+                float* scales = &sh.scales[ring_of(t)][0][0];
+                uint64_t live;
+                bool masked;
+                inspect<false>(p, src, seg, view, t, pg[0], tile, scales, live, masked);
+                src.turn(t + 1, end, pg);
+                f32x4 x[2][2];
+                const uint8_t* rows32 = tile + kh * 32 * kRow;
+                scores32<2, 4, 2>(x, rows32, rows32 + 528, scales + kh * 32, q, p.scale_log2, true, l16, g);
+                if (masked) {
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
-                        const float e = __builtin_amdgcn_exp2f(x[u][r][i] - lse2[r]);
-                        w += adds[r] ? e : 0.f;
+                        const uint64_t on = (live & sees<false>(p, s, token[r]).bits(t * 64u)) >> (kh * 32);
+#pragma unroll
+                        for (int u = 0; u < 2; ++u)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) x[u][r][i] = (on >> (key_of(u, g) + i)) & 1u ? x[u][r][i] : -INFINITY;
                     }
-                    const float total = sum16(w);
-                    keep = (int)l16 == i ? total : keep;
                 }
-                if (l16 < 4) sh.sums[rw][(t - t0) * 64 + kh * 32 + key_of(u, g) + l16] += keep;
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    float keep = 0.f;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float w = 0.f;
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            const float e = __builtin_amdgcn_exp2f(x[u][r][i] - lse2[r]);
+                            w += adds[r] ? e : 0.f;
+                        }
+                        const float total = sum16(w);
+                        keep = (int)l16 == i ? total : keep;
+                    }
+                    if (l16 < 4) sh.sums[rw][(t - t0) * 64 + kh * 32 + key_of(u, g) + l16] += keep;
+                }
             }
         }
-    }
-    __syncthreads();
-    for (uint32_t k = threadIdx.x; k < run * 64u; k += kThreads) {
-        const uint32_t pos = t0 * 64u + k;
-        if (pos >= p.max_kv) break;
-        const uint64_t at = (uint64_t)seg.b * p.weights_stride + pos;
-        const float v = (sh.sums[0][k] + sh.sums[1][k]) + (sh.sums[2][k] + sh.sums[3][k]);
-        p.weights_out[at] = (p.weights_in ? p.weights_in[at] : 0.f) + v;
+        __syncthreads();
+        for (uint32_t k = threadIdx.x; k < (t1 - t0) * 64u; k += kThreads) {
+            const uint32_t pos = t0 * 64u + k;
+            if (pos >= p.max_kv) break;
+            add_weights(p, seg.b, pos, (sh.sums[0][k] + sh.sums[1][k]) + (sh.sums[2][k] + sh.sums[3][k]));
+        }
+        __syncthreads();
+        if (t1 < seg.t1) seg.t0 = t1;
+        else left = line.next(seg);
     }
 }
 
@@ -1299,19 +1326,13 @@ hipError_t launch_attend(const AttendParams& given, void* workspace, hipStream_t
     return e != hipSuccess ? e : launch_combine(p, a.rows, stream);
 }
 
-hipError_t launch_attend_weights(const AttendParams& p, hipStream_t stream) {
-    const uint32_t tiles = (p.max_kv + 63) / 64;
-    // runs that fill the card once, up to what a block's sums hold
-    uint64_t run = ((uint64_t)tiles * p.num_seqs + 255) / 256;
-    run = run < 1 ? 1 : run > kWeightTiles ? kWeightTiles : run;
-    const uint32_t blocks = (uint32_t)((tiles + run - 1) / run);
+hipError_t launch_attend_weights(const AttendParams& given, hipStream_t stream) {
+    AttendParams p = given;
+    p.line = nullptr;
+    p.least = 1;
+    const uint64_t tiles = (uint64_t)((p.max_kv + 63) / 64) * p.num_seqs;
     (void)hipGetLastError();
-    for (uint32_t b = 0; b < p.num_seqs; b += 32768) {          // the grid's second dimension
-        AttendParams q = p;
-        q.num_seqs = p.num_seqs - b < 32768 ? p.num_seqs - b : 32768;
-        q.first_seq = b;
-        weights_kernel<<<dim3(blocks, q.num_seqs), dim3(kThreads), 0, stream>>>(q, (uint32_t)run);
-    }
+    weights_kernel<<<dim3((uint32_t)(tiles < 256 ? tiles : 256)), dim3(kThreads), 0, stream>>>(p);
     return hipGetLastError();
 }
 

@@ -704,10 +704,11 @@ KVPUB_API kvpub_status kvpub_attend_weights(kvpub_ctx* ctx, uint32_t replica, ui
     kvpub_status st = check_reader(ctx, replica, layer);
     if (st == KVPUB_OK) st = check_queries(q);
     if (st == KVPUB_OK) st = check_pages(q, pages);
-    if (st != KVPUB_OK || q->num_tokens == 0 || pages->num_seqs == 0 || pages->max_kv_len == 0) return st;
-    if (!lse || !good_lse(lse, lse_token_stride, q->num_heads, q->num_tokens)) return KVPUB_ERR_INVALID_ARG;
+    if (st != KVPUB_OK || pages->num_seqs == 0 || pages->max_kv_len == 0) return st;
+    if (q->num_tokens && (!lse || !good_lse(lse, lse_token_stride, q->num_heads, q->num_tokens))) return KVPUB_ERR_INVALID_ARG;
     if (!weights_out || !aligned(weights_out, 4) || !aligned(weights_in, 4)) return KVPUB_ERR_INVALID_ARG;
     if (weights_stride < (int64_t)pages->max_kv_len || weights_stride > INT32_MAX) return KVPUB_ERR_INVALID_ARG;
+    if ((((uint64_t)pages->max_kv_len + 63) / 64) * pages->num_seqs >= (1ull << 31)) return KVPUB_ERR_INVALID_ARG;
     DeviceGuard guard(ctx->cfg.device);
     if (!guard.ok) return KVPUB_ERR_HIP;
     kvpub::AttendParams a = attend_params(ctx, replica, layer, q);

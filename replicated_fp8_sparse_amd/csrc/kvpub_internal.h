@@ -117,9 +117,8 @@ struct AttendParams {
     const float* weights_in;     // weights only
     float* weights_out;
     int64_t weights_stride;
-    uint32_t first_seq;          // weights only: sequence of the grid's first row
     uint32_t least;              // fewest tiles of a block
-    uint32_t* line;              // workspace: prefix of each sequence's work, then the blocks' share
+    uint32_t* line;              // workspace: prefix of each sequence's work, then the blocks' share (weights: null)
     float* part_lse;             // workspace: [blocks * 2][rows]
     float* part;                 // workspace: [blocks * 2][rows][512]
 };
