@@ -290,8 +290,8 @@ typedef struct {
  * kv_len values are taken as at least 0 and at most max_kv_len; tokens
  * beyond the first max_q_len of a sequence, and tokens that belong to no
  * sequence, keep their output as it was.  A page number outside the context's
- * pages hides its 64 positions and is counted once a call
- * (kvpub_error_read's invalid count). */
+ * pages hides its 64 positions, and is counted once a call if some token would
+ * have seen one of its tile's positions (kvpub_error_read's invalid count). */
 typedef struct {
     const int32_t *kv_len;            /* [num_seqs] */
     const int32_t *q_start;           /* [num_seqs + 1], ascending; NULL: one token a sequence */
@@ -321,6 +321,9 @@ KVPUB_API uint64_t kvpub_attend_slots_workspace(const kvpub_queries *q, uint32_t
  *        512 values a row; alignment and stride rules as for the queries
  *   lse: binary32 (t,h) at t*lse_token_stride + h, or NULL; 4-byte aligned
  *   workspace: 16-byte aligned, workspace_bytes >= kvpub_attend_workspace(q, pages)
+ * out, lse and the workspace overlap neither each other nor what the call reads.
+ * num_seqs * ceil(max_q_len*num_heads / 64) * ceil(max_kv_len / 64) stays below
+ * 2^31 (KVPUB_ERR_INVALID_ARG, as for every argument out of its range).
  * T == 0 or num_seqs == 0 launches nothing. */
 KVPUB_API kvpub_status kvpub_attend(kvpub_ctx *ctx, uint32_t replica, uint32_t layer, const kvpub_queries *q,
                                     const kvpub_pages *pages, void *out, int64_t out_token_stride,
@@ -345,8 +348,9 @@ KVPUB_API kvpub_status kvpub_attend_slots(kvpub_ctx *ctx, uint32_t replica, uint
  * or beyond kv_len[b] and on bad pages).  weights_in NULL: zeros; weights_in ==
  * weights_out adds in place; otherwise the two do not overlap.  lse is what
  * kvpub_attend gave for the same queries and pages; a row of -inf adds nothing.
- *   weights: binary32 [num_seqs], row stride weights_stride >= max_kv_len elements
- * The sums run in one fixed order (no atomics). */
+ *   weights: binary32 [num_seqs], row stride weights_stride >= max_kv_len elements;
+ *            num_seqs * ceil(max_kv_len / 64) below 2^31
+ * Without query tokens (T == 0) nothing but the weights is read.  The sums run in one fixed order (no atomics). */
 KVPUB_API kvpub_status kvpub_attend_weights(kvpub_ctx *ctx, uint32_t replica, uint32_t layer, const kvpub_queries *q,
                                             const kvpub_pages *pages, const float *lse, int64_t lse_token_stride,
                                             const float *weights_in, float *weights_out, int64_t weights_stride,
@@ -366,7 +370,8 @@ KVPUB_API kvpub_status kvpub_attend_weights(kvpub_ctx *ctx, uint32_t replica, ui
  *   kept[b][i]        = position that moved to i, -1 for new_len <= i < budget
  *   new_len[b]        = min(len, budget)
  *   weights_out[b][i] = weights_in[b][kept[b][i]] for i < new_len, 0 up to max_kv_len
- * weights_out may be weights_in itself, otherwise the two do not overlap.
+ * weights_out may be weights_in itself, otherwise the two do not overlap;
+ * new_len is not kv_len, and no other array of the call overlaps another.
  * A kept position whose source or destination page is outside the context's
  * pages is not copied, and counted.  The rows behind new_len keep their bytes. */
 typedef struct {

@@ -576,7 +576,7 @@ __device__ __forceinline__ View view_of(const AttendParams& p, const Segment& g,
 
 // The rows of tile t that exist (bits of live) and whether some row of the unit may
 // not see it whole; such a tile is cleaned.  Bad pages and slots are counted by the
-// unit that has the sequence's first rows.
+// unit that has the sequence's last rows: no other sees more of its tiles.
 template <bool Slots, class Src>
 __device__ __forceinline__ void inspect(const AttendParams& p, const Src& src, const Segment& g, const View& view, uint32_t t,
                                         int64_t page, uint8_t* tile, float* scales, uint64_t& live, bool& masked) {
@@ -586,13 +586,13 @@ __device__ __forceinline__ void inspect(const AttendParams& p, const Src& src, c
         const bool in = src.lane < left;
         live = __ballot(in && src.good(v));
         const uint64_t wrong = __ballot(in && v != -1 && !src.good(v));
-        if (wrong && g.unit == 0 && threadIdx.x == 0) atomicAdd(p.invalid_count, (unsigned long long)__popcll(wrong));
+        if (wrong && g.unit + 1 == g.s.units && threadIdx.x == 0) atomicAdd(p.invalid_count, (unsigned long long)__popcll(wrong));
         masked = live != ~0ull;
     } else {
         live = left < 64 ? (1ull << left) - 1 : ~0ull;
         masked = t * 64u + 64u > view.clear;
         if (page < 0) {                              // page 0 was copied in its place
-            if (g.unit == 0 && threadIdx.x == 0) atomicAdd(p.invalid_count, 1ull);
+            if (g.unit + 1 == g.s.units && threadIdx.x == 0) atomicAdd(p.invalid_count, 1ull);
             live = 0;
             masked = true;
         }

@@ -748,7 +748,7 @@ KVPUB_API kvpub_status kvpub_evict(kvpub_ctx* ctx, uint32_t layer, const kvpub_e
     if (io->dst_table_stride < ((int64_t)most + 63) / 64 || io->dst_table_stride > INT32_MAX) return KVPUB_ERR_INVALID_ARG;
     const bool in_place = io->dst_table == io->page_table;
     if (in_place && io->dst_table_stride != io->page_table_stride) return KVPUB_ERR_INVALID_ARG;
-    if (io->new_len == io->kv_len) return KVPUB_ERR_INVALID_ARG;      // kv_len is read again by later launches of the call
+    if (io->new_len == io->kv_len) return KVPUB_ERR_INVALID_ARG;      // one thread writes new_len while others may still read kv_len
     if (!workspace || !aligned(workspace, 16) || workspace_bytes < kvpub_evict_workspace(io)) return KVPUB_ERR_INVALID_ARG;
     DeviceGuard guard(ctx->cfg.device);
     if (!guard.ok) return KVPUB_ERR_HIP;
