@@ -30,7 +30,17 @@ class Context:
         self.ptr = ctypes.addressof(self.buf)
 
 
-CTX = Context()
+class Lazy:
+    """Built by the first call: collecting these tests loads no library."""
+    made = None
+
+    @property
+    def ptr(self):
+        self.made = self.made or Context()
+        return self.made.ptr
+
+
+CTX = Lazy()
 LIMIT = 2 ** 31
 
 
