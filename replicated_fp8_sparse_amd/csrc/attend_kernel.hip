@@ -1281,16 +1281,21 @@ hipError_t launch_combine(const AttendParams& p, uint32_t M, hipStream_t stream)
 
 AttendPlan plan_attend(uint64_t rows, uint64_t num_seqs, uint64_t num_tokens, uint64_t heads, uint64_t max_kv) {
     AttendPlan a;
-    a.rows = rows <= 16 ? 16u : rows <= 32 ? 32u : 64u;
-    uint64_t units = num_seqs * ((rows + a.rows - 1) / a.rows);
-    const uint64_t by_tokens = num_tokens * heads / a.rows + num_seqs;      // ragged: no more units than that
-    units = units < by_tokens ? units : by_tokens;
+    a.least = 2;
     const uint64_t tiles = max_kv ? (max_kv + 63) / 64 : 1;
+    // Units of 16 or 32 rows where that holds all rows, or where the line has so few
+    // runs that a block each still leaves CUs idle: more, shorter blocks then.
+    uint64_t units = 0, runs = 0;
+    for (a.rows = 16; ; a.rows *= 2) {
+        units = num_seqs * ((rows + a.rows - 1) / a.rows);
+        const uint64_t by_tokens = num_tokens * heads / a.rows + num_seqs;  // ragged: no more units than that
+        units = units < by_tokens ? units : by_tokens;
+        runs = units * ((tiles + a.least - 1) / a.least) + 1;
+        if (a.rows == 64 || rows <= a.rows || runs <= 256) break;
+    }
     a.fits = units * tiles < (1ull << 31);
     // one block a CU; never more than the line has runs
-    a.least = 2;
-    const uint64_t runs = units * ((tiles + a.least - 1) / a.least) + 1;
-    a.blocks = (uint32_t)(units >= 256 || runs >= 256 ? 256 : runs);
+    a.blocks = (uint32_t)(runs >= 256 ? 256 : runs);
     a.wide = a.rows == 64 && units * tiles >= 16ull * a.blocks;
     a.line_bytes = ((num_seqs + 1) * 4 + 255) / 256 * 256;
     a.lse_bytes = (uint64_t)a.blocks * 2 * a.rows * 4;
