@@ -1283,20 +1283,31 @@ AttendPlan plan_attend(uint64_t rows, uint64_t num_seqs, uint64_t num_tokens, ui
     AttendPlan a;
     a.least = 2;
     const uint64_t tiles = max_kv ? (max_kv + 63) / 64 : 1;
-    // Units of 16 or 32 rows where that holds all rows, or where the line has so few
-    // runs that a block each still leaves CUs idle: more, shorter blocks then.
-    uint64_t units = 0, runs = 0;
-    for (a.rows = 16; ; a.rows *= 2) {
-        units = num_seqs * ((rows + a.rows - 1) / a.rows);
-        const uint64_t by_tokens = num_tokens * heads / a.rows + num_seqs;  // ragged: no more units than that
+    uint64_t units = 0;
+    const auto runs_of = [&](uint32_t M) {
+        units = num_seqs * ((rows + M - 1) / M);
+        const uint64_t by_tokens = num_tokens * heads / M + num_seqs;       // ragged: no more units than that
         units = units < by_tokens ? units : by_tokens;
-        runs = units * ((tiles + a.least - 1) / a.least) + 1;
-        if (a.rows == 64 || rows <= a.rows || runs <= 256) break;
+        return units * ((tiles + a.least - 1) / a.least) + 1;
+    };
+    // Rows of a unit.  64 (attend_wide_kernel) from ten tiles a block on: its tile of 64
+    // rows takes 3.1 us, two of 32 rows 4.2 us, but it starts 8 us later (16 sequences
+    // of 128 heads, 4096 positions: 56.4 us against 54.9; 8192: 81.3 against 88.6).
+    // 16 where that holds all rows, or where the line has so few runs that a block each
+    // still leaves CUs idle (4 tokens of 64 heads, 256 slots: 15.4 us against 23).
+    uint64_t runs = runs_of(64);
+    a.rows = 64;
+    if (rows <= 32 || units * tiles < 10 * 256) {
+        runs = runs_of(16);
+        a.rows = 16;
+        if (rows > 16 && runs > 256) {
+            runs = runs_of(32);
+            a.rows = 32;
+        }
     }
     a.fits = units * tiles < (1ull << 31);
     // one block a CU; never more than the line has runs
     a.blocks = (uint32_t)(runs >= 256 ? 256 : runs);
-    a.wide = a.rows == 64 && units * tiles >= 16ull * a.blocks;
     a.line_bytes = ((num_seqs + 1) * 4 + 255) / 256 * 256;
     a.lse_bytes = (uint64_t)a.blocks * 2 * a.rows * 4;
     a.bytes = a.line_bytes + a.lse_bytes + (uint64_t)a.blocks * 2 * a.rows * 512 * 4;
@@ -1320,9 +1331,6 @@ hipError_t launch_attend(const AttendParams& given, void* workspace, hipStream_t
     } else if (a.rows == 32) {
         if (p.by_slots) attend_kernel<1, 2, 2, 2, true><<<grid, block, 0, stream>>>(p);
         else attend_kernel<1, 2, 2, 2, false><<<grid, block, 0, stream>>>(p);
-    } else if (!a.wide) {
-        if (p.by_slots) attend_kernel<1, 4, 2, 1, true><<<grid, block, 0, stream>>>(p);
-        else attend_kernel<1, 4, 2, 1, false><<<grid, block, 0, stream>>>(p);
     } else {
         if (p.by_slots) attend_wide_kernel<true><<<grid, block, 0, stream>>>(p);
         else attend_wide_kernel<false><<<grid, block, 0, stream>>>(p);

@@ -128,7 +128,6 @@ struct AttendPlan {
     uint32_t rows;
     uint32_t blocks;
     uint32_t least;
-    bool wide;                   // runs long enough for attend_wide_kernel
     bool fits;                   // fewer than 2^31 tiles in all
     uint64_t line_bytes;
     uint64_t lse_bytes;
