@@ -15,14 +15,23 @@
 //
 // Mapping.  A block of 8 waves takes a unit (sequence, M rows = (token, head)
 // pairs) over a run of 64-row tiles (a page), a tile being one copy of 41984
-// contiguous bytes into LDS.  A row's stride of 656 bytes (164 banks, 36 modulo
-// 64) puts 16 rows on distinct banks, so the page's own layout is read free of
-// conflicts.  Scores come out transposed (keys down, query rows across): a lane
-// holds 4 keys of one query row, row maxima and sums need two shuffles, and the
-// weights are already laid out as an operand of the second product if its key
-// order follows; ds_read_b64_tr_b8 picks the values' columns in that order.
-// One pass: running maximum and sum, the accumulator rescaled only when the
-// maximum grew by more than 2^8.
+// contiguous bytes straight into LDS, two tiles ahead of its use.  Scores come
+// out transposed (keys down, query rows across): a lane holds 4 keys of one query
+// row, row maxima and sums need two shuffles, and the weights are already laid
+// out as an operand of the second product if its key order follows;
+// ds_read_b64_tr_b8 picks the values' columns in that order.  The page's own row
+// stride (656 bytes: 164 banks, 36 modulo 64) is read as it is: 16-byte reads of
+// 16 rows take 8.0 cycles (two rows share banks), a column read 2.3 with half of
+// the rows rotated by 8 (4.1 without).  One pass: running maximum and sum, the
+// accumulator rescaled only when the maximum grew by more than 2^8.
+// M = 16 and 32: attend_kernel, the row's 512 values split between waves; M = 64:
+// attend_wide_kernel.  plan_attend() says which and what either costs.
+//
+// Bound.  The matrix units need 2200 cycles for a tile of 64 rows, its widening to
+// bf16 (4 instructions for 8 codes) and softmax about 2000 on the vector unit, LDS
+// 2500; with one barrier a tile and two waves a SIMD they overlap by half: 6300
+// cycles a tile.  64 sequences of up to 8192 positions, 128 heads: 170 us in all
+// (61 at the rate of a large bf16 matrix product, 430 TFLOP/s reached).
 //
 // Work split.  All units' tiles form one line that the blocks cut into equal
 // runs, whatever the lengths of the sequences; a unit cut between blocks leaves
@@ -628,10 +637,13 @@ __device__ __forceinline__ void write_row(const AttendParams& p, const Segment& 
 }
 
 // R16: 16-row groups of a wave.  RW waves split the rows, KW the keys of a tile, TW
-// the row's 512 values: such a wave forms its tiles' part of the scores, adds up
+// (2 or 4) the row's 512 values: such a wave forms its tiles' part of the scores, adds up
 // the others' through LDS, and takes its tiles' columns of the output.  Each code
 // is widened once a wave for 16 * R16 rows in either product; the widening (4
 // instructions for 8 codes) is what the vector unit spends most of its time on.
+// Splitting the values keeps a wave's share of the queries small: a first tile is
+// under way 2 us earlier than with whole rows (one sequence of 700 positions, 16
+// heads: 17 us, of which 6 join; whole rows 21 us).
 template <int R16, int RW, int TW, int KW, bool Slots>
 __global__ __launch_bounds__(kThreads) void attend_kernel(const AttendParams p) {
     static_assert(RW * KW * TW == kWaves, "every wave has its part");
@@ -872,6 +884,9 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(const AttendParams p) 
 // tile, gives their weights to LDS, and takes 32 rows' weights for one tile of 128
 // values: no score is formed twice, and a value's code is widened once for 32 rows.
 // The next tile's scores are formed beside this tile's values; one barrier a tile.
+// Against 4 waves of twice the rows (200 us), tiles widened once into LDS (217 us) and
+// two barriers a tile (214 us) at 64 sequences of up to 8192 positions and 128 heads:
+// 170 us; 16 drafted trees of 64 tokens, 32 heads, 8192 positions: 270 us (620 TFLOP/s).
 // The maximum the weights refer to is held by all waves alike: a row that outgrows
 // it raises a flag, and all waves then agree on new ones before the weights are used.
 struct WideShared {
@@ -1082,7 +1097,8 @@ __global__ __launch_bounds__(kThreads) void attend_wide_kernel(const AttendParam
 
 // Joins the partial results of units that were cut between blocks: a group of
 // 128 threads takes one (token, head) row, 4 columns a thread, and adds the
-// blocks' parts in order.
+// blocks' parts in order.  4 us for 256 rows of 2 parts (a chain of four reads from
+// memory), 14 us for 8192 rows of 1 to 3 parts.
 template <bool Slots>
 __global__ __launch_bounds__(256) void combine_kernel(const AttendParams p, uint32_t M) {
     const uint32_t each = p.line[p.num_seqs];
@@ -1129,8 +1145,11 @@ __global__ __launch_bounds__(256) void combine_kernel(const AttendParams p, uint
 // sequence's query rows, 128 at a time: 4 waves of 32 rows for either half of a
 // tile's keys, the operands in registers.  A position belongs to one block: its sum over rows
 // runs within a wave (DPP over the 16 rows of a lane group), pass by pass and wave
-// by wave, always in that order.  Bound by the vector unit: 4 instructions widen 8
-// codes for 32 rows.
+// by wave, always in that order.  A wave has 32 rows, so that a widened operand (4
+// vector instructions) serves two matrix instructions: with 16 rows 87 us, with 32
+// 69 us for 16 sequences of up to 16384 positions and 128 heads; one line instead of
+// equal runs of each sequence's bound 51 us (92 MB: 18 us at a copy's rate).  Bound
+// by the vector unit and, for runs of some ten tiles, by the first tile's way (8 us).
 constexpr uint32_t kWeightTiles = 16;
 
 struct WeightShared {
