@@ -12,8 +12,8 @@
 // ascending order.
 //
 // move_kernel, one block for 64 destination positions: their rows are loaded
-// into registers, then written to all replicas.  In place, a row may be another
-// block's source.  Positions only move down (kept[i] >= i), so the rows of
+// into registers, then written to all replicas.  In place (rows or weights), a row
+// may be another block's source.  Positions only move down (kept[i] >= i), so the rows of
 // destination chunk c are sources of chunks <= c alone, and as ranks are
 // consecutive of at most two of them, which select_kernel's ranks name.  A block
 // takes its chunk by a ticket of its sequence's counter, loads, raises its
@@ -33,6 +33,7 @@ constexpr int kSelThreads = 1024;
 constexpr int kSelWaves = kSelThreads / 64;
 constexpr uint32_t kLdsKeys = 32768;
 constexpr int kMoveThreads = 256;
+constexpr uint32_t kMoveBlocks = 1u << 22;         // chunks of a launch
 
 __device__ __forceinline__ bool poisoned(const CtxHead* head) { return (head->status & kStatusPoisoned) != 0; }
 
@@ -172,8 +173,9 @@ __global__ __launch_bounds__(kSelThreads) void select_kernel(const EvictParams p
     for (uint32_t c = chunks + tid; c <= p.chunks; c += kSelThreads) ranks[c] = keep;
 }
 
-template <bool InPlace>
-__global__ __launch_bounds__(kMoveThreads) void move_kernel(const EvictParams p, uint32_t seq0) {
+// Ordered: rows or weights are written over others' sources.
+template <bool Ordered>
+__global__ __launch_bounds__(kMoveThreads) void move_kernel(const EvictParams p, uint32_t seq0, uint32_t chunk0) {
     __shared__ uint64_t src[64], dst[64], isrc[64], idst[64];    // ~0: not copied
     __shared__ uint32_t ticket;
     if (poisoned(p.head)) return;
@@ -181,8 +183,8 @@ __global__ __launch_bounds__(kMoveThreads) void move_kernel(const EvictParams p,
     uint32_t* mine = p.state + (uint64_t)b * (2 * p.chunks + 2);
     uint32_t* flags = mine + 1;
     const uint32_t* ranks = mine + 1 + p.chunks;
-    uint32_t c = blockIdx.x;
-    if (InPlace) {
+    uint32_t c = chunk0 + blockIdx.x;
+    if (Ordered) {
         if (tid == 0) ticket = atomicAdd(mine, 1u);
         __syncthreads();
         c = ticket;
@@ -198,7 +200,7 @@ __global__ __launch_bounds__(kMoveThreads) void move_kernel(const EvictParams p,
         if (i < keep) {
             const uint32_t at = (uint32_t)p.kept[(uint64_t)b * p.kept_stride + i];
             weight = p.weights_in[(uint64_t)b * p.weights_stride + at];
-            if (!InPlace || at != i) {
+            if (!p.same_pages || at != i) {
                 const int64_t ps = p.pages[(uint64_t)b * p.pages_stride + (at >> 6)];
                 const int64_t pd = p.dst[(uint64_t)b * p.dst_stride + (i >> 6)];
                 if (ps >= 0 && ps < pages && pd >= 0 && pd < pages) {
@@ -237,7 +239,7 @@ __global__ __launch_bounds__(kMoveThreads) void move_kernel(const EvictParams p,
         return page * p.idx_page_stride + 8192u + in / 32u;
     };
     if (my_isrc != ~0ull) scale = *(const uint32_t*)(p.idx_base[0] + scale_at(my_isrc));
-    if (InPlace) {
+    if (Ordered) {
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");     // this thread's rows are in its registers
         __syncthreads();
         if (tid == 0) {
@@ -274,9 +276,12 @@ hipError_t launch_evict(const EvictParams& given, hipStream_t stream) {
     (void)hipGetLastError();
     select_kernel<<<dim3(p.num_seqs), dim3(kSelThreads), 0, stream>>>(p);
     for (uint32_t b = 0; b < p.num_seqs; b += 32768) {       // the grid's second dimension
-        const dim3 grid(p.chunks, p.num_seqs - b < 32768 ? p.num_seqs - b : 32768);
-        if (p.in_place) move_kernel<true><<<grid, dim3(kMoveThreads), 0, stream>>>(p, b);
-        else move_kernel<false><<<grid, dim3(kMoveThreads), 0, stream>>>(p, b);
+        const uint32_t seqs = p.num_seqs - b < 32768 ? p.num_seqs - b : 32768;
+        for (uint32_t c = 0; c < p.chunks; c += kMoveBlocks) {       // a dimension's threads stay below 2^32
+            const dim3 grid(p.chunks - c < kMoveBlocks ? p.chunks - c : kMoveBlocks, seqs);
+            if (p.same_pages || p.weights_out == p.weights_in) move_kernel<true><<<grid, dim3(kMoveThreads), 0, stream>>>(p, b, c);
+            else move_kernel<false><<<grid, dim3(kMoveThreads), 0, stream>>>(p, b, c);
+        }
     }
     return hipGetLastError();
 }

@@ -59,7 +59,7 @@ __global__ __launch_bounds__(kThreads, 2) void expanded_kernel(const ExpandedPar
     const uint32_t pair = (in / q_tiles) * 8u + xcd;
     if (pair >= pairs) return;
     const uint32_t b = p.first_seq + pair / p.heads, h = pair % p.heads;
-    const uint32_t tile_q = q_tiles - 1u - in % q_tiles;
+    const uint32_t tile_q = p.first_tile + q_tiles - 1u - in % q_tiles;
 
     int64_t q0 = p.q_start[b], q1 = p.q_start[b + 1], k0 = p.k_start[b], k1 = p.k_start[b + 1];
     q0 = q0 < 0 ? 0 : q0;
@@ -264,19 +264,22 @@ __global__ __launch_bounds__(kThreads, 2) void expanded_kernel(const ExpandedPar
 }  // namespace
 
 hipError_t launch_expanded(const ExpandedParams& given, hipStream_t stream) {
-    const uint32_t q_tiles = (given.max_q + kQueries - 1) / kQueries;
-    // at most 2^30 blocks a launch
-    const uint64_t each = (uint64_t)q_tiles * given.heads;
-    const uint32_t seqs = (uint32_t)(((1ull << 30) / each) > given.num_seqs ? given.num_seqs : (1ull << 30) / each);
+    // a grid's threads stay below 2^32: at most 2^23 blocks a launch
+    const uint32_t all = (given.max_q + kQueries - 1) / kQueries, most = (1u << 23) / 128;
+    const uint32_t q_tiles = all < most ? all : most;
+    const uint32_t seqs = (1u << 23) / (q_tiles * given.heads);          // 1 and more: 128 heads at most
     (void)hipGetLastError();
-    for (uint32_t b = 0; b < given.num_seqs; b += seqs) {
-        ExpandedParams p = given;
-        p.first_seq = b;
-        p.num_seqs = given.num_seqs - b < seqs ? given.num_seqs - b : seqs;
-        const uint32_t groups = (p.num_seqs * p.heads + 7) / 8;
-        expanded_kernel<<<dim3(groups * 8 * q_tiles), dim3(kThreads), 0, stream>>>(p, q_tiles);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
+    for (uint32_t q = 0; q < all; q += q_tiles) {
+        for (uint32_t b = 0; b < given.num_seqs; b += seqs) {
+            ExpandedParams p = given;
+            p.first_seq = b;
+            p.first_tile = q;
+            p.num_seqs = given.num_seqs - b < seqs ? given.num_seqs - b : seqs;
+            const uint32_t groups = (p.num_seqs * p.heads + 7) / 8;
+            expanded_kernel<<<dim3(groups * 8 * q_tiles), dim3(kThreads), 0, stream>>>(p, q_tiles);
+            const hipError_t e = hipGetLastError();
+            if (e != hipSuccess) return e;
+        }
     }
     return hipSuccess;
 }

@@ -779,7 +779,7 @@ KVPUB_API kvpub_status kvpub_evict(kvpub_ctx* ctx, uint32_t layer, const kvpub_e
     e.budget = io->budget;
     e.first = io->first;
     e.last = io->last;
-    e.in_place = in_place ? 1u : 0u;
+    e.same_pages = in_place ? 1u : 0u;
     e.state = static_cast<uint32_t*>(workspace);
     return map_hip(kvpub::launch_evict(e, static_cast<hipStream_t>(stream)));
 }

@@ -164,7 +164,7 @@ struct EvictParams {
     uint32_t budget;
     uint32_t first;
     uint32_t last;
-    uint32_t in_place;
+    uint32_t same_pages;         // dst is pages: rows are moved within the table
     uint32_t chunks;             // set by launch_evict: ceil(max_kv / 64)
     uint32_t* state;             // workspace: each sequence's ticket, flags[chunks], ranks[chunks + 1]
 };
@@ -192,6 +192,7 @@ struct ExpandedParams {
     uint32_t causal;
     float scale_log2;
     uint32_t first_seq;          // set by launch_expanded
+    uint32_t first_tile;
 };
 hipError_t launch_expanded(const ExpandedParams& p, hipStream_t stream);
 

@@ -154,6 +154,16 @@ def test_weights_in_place_with_other_pages():
     run_case(48, [1000, 300], 256, 4, 64, False, seed=8, weights_in_place=True)
 
 
+@pytest.mark.parametrize("lens,budget", [([20000, 6000], 15000), ([8000] * 6, 64)])
+def test_weights_in_place_of_long_sequences_with_other_pages(lens, budget):
+    """Weights that move down within their array while the rows go elsewhere: many blocks read what others overwrite."""
+    most = max(lens)
+    rising = np.linspace(0, 1, most + 5, dtype=np.float32)                    # the last ones stay: every weight moves far
+    weights = np.stack([np.random.default_rng(b).permutation(rising) if b % 2 else rising for b in range(len(lens))])
+    width = -(-most // 64) + -(-min(budget, most) // 64)
+    run_case(width * len(lens), lens, budget, 0, 1, False, weights=weights, seed=4, replicas=1, weights_in_place=True)
+
+
 def test_bad_pages_are_skipped_and_counted():
     c = A.Cache(32, seed=1, replicas=1)
     try:

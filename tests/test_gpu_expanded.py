@@ -190,3 +190,13 @@ def test_the_two_forms_agree():
             assert ((a - b).norm() / b.norm()).item() < 0.03
     finally:
         c.free()
+
+
+def test_bounds_far_beyond_the_lengths(ctx):
+    """2^17 tokens of which the sequences hold few, any of them by its bound in one of 1024 sequences: 2^24 blocks."""
+    n, m = [3, 0, 130, 1] + [1] * 20 + [0] * 1000, [70, 5, 200, 1] + [2] * 1020
+    c = Case(n, m, 16, seed=6)
+    c.io.num_tokens = c.io.max_q_len = 1 << 17       # no row behind the sequences' is touched
+    c.run(ctx)
+    c.check()
+    c.o.untouched(range(sum(n)))
