@@ -38,6 +38,8 @@
 // partial results that combine_kernel joins in block order.
 #include "kvpub_internal.h"
 
+#include <type_traits>
+
 namespace kvpub {
 namespace {
 
@@ -402,6 +404,51 @@ struct Line {
             return true;
         }
         return false;
+    }
+};
+
+// Runs that keep to one sequence, for up to 64 sequences: the shortest length with
+// which they are no more than the blocks.  A block that would take the end of one
+// sequence and the start of another pays a start twice, and all wait for it.
+struct Runs {
+    const AttendParams& p;
+    uint32_t b, t0, t1;
+    bool left;
+
+    __device__ __forceinline__ Runs(const AttendParams& p_, uint32_t M, bool empty) : p(p_) {
+        const uint32_t lane = threadIdx.x & 63u;
+        uint32_t w = 0;
+        if (lane < p.num_seqs) {
+            const Seq s = sequence<false, false>(p, lane, M, empty);
+            w = s.units * s.tiles;
+        }
+        const uint32_t total = __builtin_amdgcn_readlane(scan64(w, lane), 63);
+        uint32_t each = (total + gridDim.x - 1) / gridDim.x, x = 0;
+        each = each < 1 ? 1 : each;
+        while (true) {
+            x = scan64((w + each - 1) / each, lane);
+            // ends: with `each` as long as the longest sequence they are 64 at most, and with a
+            // grid of fewer blocks than 256 there is a block for every tile
+            if ((uint32_t)__builtin_amdgcn_readlane(x, 63) <= gridDim.x) break;
+            each += 1 + each / 16;
+        }
+        const uint32_t first = x - (w + each - 1) / each, at = blockIdx.x;
+        const uint64_t here = __ballot(at >= first && at < x);
+        left = here != 0;
+        b = here ? (uint32_t)__builtin_ctzll(here) : 0u;
+        t0 = (at - __builtin_amdgcn_readlane(first, b)) * each;
+        const uint32_t tiles = __builtin_amdgcn_readlane(w, b);
+        t1 = tiles - t0 < each ? tiles : t0 + each;
+    }
+    __device__ __forceinline__ bool next(Segment& g) {
+        if (!left) return false;
+        left = false;
+        g.s = sequence<false, true>(p, b, p.max_q * p.heads, p.head->capacity <= 0);
+        g.b = b;
+        g.unit = 0;
+        g.t0 = t0;
+        g.t1 = t1;
+        return true;
     }
 };
 
@@ -1170,6 +1217,7 @@ __device__ __forceinline__ void add_weights(const AttendParams& p, uint32_t b, u
     p.weights_out[at] = (p.weights_in ? p.weights_in[at] : 0.f) + v;
 }
 
+template <bool Few>
 __global__ __launch_bounds__(kThreads) void weights_kernel(const AttendParams p) {
     __shared__ WeightShared sh;
     const uint32_t lane = threadIdx.x & 63u, l16 = lane & 15u, g = lane >> 4;
@@ -1192,7 +1240,10 @@ __global__ __launch_bounds__(kThreads) void weights_kernel(const AttendParams p)
     }
     if (!p.num_tokens) return;
 
-    Line<false> line(p, M, capacity <= 0, (uint8_t*)sh.sums);
+    std::conditional_t<Few, Runs, Line<false>> line = [&] {
+        if constexpr (Few) return Runs(p, M, capacity <= 0);
+        else return Line<false>(p, M, capacity <= 0, (uint8_t*)sh.sums);
+    }();
     Segment seg;
     uint32_t t1 = 0;
     bool left = line.next(seg);
@@ -1364,7 +1415,9 @@ hipError_t launch_attend_weights(const AttendParams& given, hipStream_t stream) 
     p.least = 1;
     const uint64_t tiles = (uint64_t)((p.max_kv + 63) / 64) * p.num_seqs;
     (void)hipGetLastError();
-    weights_kernel<<<dim3((uint32_t)(tiles < 256 ? tiles : 256)), dim3(kThreads), 0, stream>>>(p);
+    const dim3 grid((uint32_t)(tiles < 256 ? tiles : 256));
+    if (p.num_seqs <= 64) weights_kernel<true><<<grid, dim3(kThreads), 0, stream>>>(p);
+    else weights_kernel<false><<<grid, dim3(kThreads), 0, stream>>>(p);
     return hipGetLastError();
 }
 

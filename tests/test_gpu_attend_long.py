@@ -238,6 +238,14 @@ def test_weights_of_ragged_sequences(cache):
     weigh(cache, A.Queries(pg.T, heads), pg, A.Outputs(pg.T, heads))
 
 
+@pytest.mark.parametrize("seqs", [64, 65, 80])
+def test_weights_of_many_sequences(cache, seqs):
+    rng = np.random.default_rng(seqs)
+    lens, n = rng.integers(0, 129, seqs), rng.integers(0, 3, seqs)
+    pg = A.Paged(cache, lens, n, max_kv=128)
+    weigh(cache, A.Queries(pg.T, 16), pg, A.Outputs(pg.T, 16))
+
+
 def test_weights_of_a_very_long_sequence(cache):
     """More tiles a block than it sums at once (pages stand in the table many times)."""
     lens, heads = [270037, 5000], 4
