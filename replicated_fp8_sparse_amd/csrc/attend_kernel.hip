@@ -1187,16 +1187,17 @@ __global__ __launch_bounds__(256) void combine_kernel(const AttendParams p, uint
 
 // ---- accumulated weights ------------------------------------------------------------
 
-// A block takes its run of the line of all sequences' tiles (a unit: all rows of a
-// sequence), up to kWeightTiles of one sequence at a time, and passes over the
+// A block takes a run of a sequence's tiles (with many sequences its run of the line,
+// a unit being all rows of a sequence), up to kWeightTiles of them at a time, and passes over the
 // sequence's query rows, 128 at a time: 4 waves of 32 rows for either half of a
 // tile's keys, the operands in registers.  A position belongs to one block: its sum over rows
 // runs within a wave (DPP over the 16 rows of a lane group), pass by pass and wave
 // by wave, always in that order.  A wave has 32 rows, so that a widened operand (4
 // vector instructions) serves two matrix instructions: with 16 rows 87 us, with 32
 // 69 us for 16 sequences of up to 16384 positions and 128 heads; one line instead of
-// equal runs of each sequence's bound 51 us (92 MB: 18 us at a copy's rate).  Bound
-// by the vector unit and, for runs of some ten tiles, by the first tile's way (8 us).
+// equal runs of each sequence's bound 53 us, runs that keep to one sequence 39-47 us
+// (92 MB: 18 us at a copy's rate; 28 us with the scores left out).  Bound by the vector
+// unit: 6000 cycles a tile of 128 rows, of which the matrix units need 2300.
 constexpr uint32_t kWeightTiles = 16;
 
 struct WeightShared {
