@@ -59,8 +59,8 @@ constexpr int kThreads = kWaves * 64;
 constexpr float kLn2 = 0.693147180559945309f;
 constexpr float kLazy = 8.0f;                    // rescale when a maximum grows past 2^8
 
-// LDS: the tile ring and the waves' exchange of partial scores (after the last
-// tile both hold the join of key halves), the tiles' scales by tile of 128, slot
+// LDS: the tile ring (after the last tile it holds the join of key halves), the
+// waves' exchange of partial scores, the tiles' scales by tile of 128, slot
 // lists 3 tiles deep.  160 KB in all.
 constexpr int kSlotRing = 3;
 constexpr int kExchange = 32768;
@@ -192,7 +192,7 @@ __device__ __forceinline__ void scores32(f32x4 (*x)[R16], const uint8_t* rows, c
         for (int u = 0; u < 2; ++u) a[u] = sc[u][j * 64];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-                i32x4 next[2];
+            i32x4 next[2];
 #pragma unroll
             for (int u = 0; u < 2; ++u) next[u] = j * 2 + h + 1 < 2 * T ? *(const i32x4*)(rows + at[u] + (j * 2 + h + 1) * 64) : raw[u];
 #pragma unroll
@@ -683,27 +683,28 @@ __device__ __forceinline__ void write_row(const AttendParams& p, const Segment& 
     }
 }
 
-// R16: 16-row groups of a wave.  RW waves split the rows, KW the keys of a tile, TW
-// (2 or 4) the row's 512 values: such a wave forms its tiles' part of the scores, adds up
-// the others' through LDS, and takes its tiles' columns of the output.  Each code
-// is widened once a wave for 16 * R16 rows in either product; the widening (4
-// instructions for 8 codes) is what the vector unit spends most of its time on.
-// Splitting the values keeps a wave's share of the queries small: a first tile is
-// under way 2 us earlier than with whole rows (one sequence of 700 positions, 16
-// heads: 17 us, of which 6 join; whole rows 21 us).
-template <int R16, int RW, int TW, int KW, bool Slots>
+// 16 * RW rows.  RW waves split the rows, 2 a tile's keys, TW = 4 / RW the row's 512
+// values: a wave forms its tiles' part of the scores, adds up the others' through LDS,
+// and takes its tiles' columns of the output.  The widening (4 instructions for 8
+// codes) is what the vector unit spends most of its time on.  Splitting the values
+// keeps a wave's share of the queries small: a first tile is under way 2 us earlier
+// than with whole rows (one sequence of 700 positions, 16 heads: 17 us, of which 6
+// join; whole rows 21 us).
+template <int RW, bool Slots>
 __global__ __launch_bounds__(kThreads) void attend_kernel(const AttendParams p) {
-    static_assert(RW * KW * TW == kWaves, "every wave has its part");
-    constexpr int M = 16 * R16 * RW;
+    constexpr int M = 16 * RW;
+    constexpr int TW = 4 / RW;
     constexpr int T = 4 / TW;                       // tiles of 128 of a wave
-    constexpr int P = 1;                            // RoPE halves of a wave
     constexpr int NB = 8 * T;                       // 16-column blocks of a wave
-    static_assert(2 * kWaves * R16 * 2048 <= kExchange, "partial scores of two steps");
-    static_assert(KW == 1 || kWaves / 2 * R16 * (NB * 1024 + 512) <= kRing * kTileBytes + kExchange, "join of key halves");
+    constexpr int kOthers = RW * 2;                 // waves between two that share rows and keys
+    static_assert(RW * 2 * TW == kWaves, "every wave has its part");
+    static_assert(2 * kWaves * 2048 <= kExchange, "partial scores of two tiles");
+    static_assert(kWaves / 2 * (NB * 1024 + 512) <= kRing * kTileBytes, "join of key halves");
     __shared__ Shared sh;
     const uint32_t lane = threadIdx.x & 63u, l16 = lane & 15u, g = lane >> 4;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const uint32_t rw = wave % RW, kw = (wave / RW) % KW, tw = wave / (RW * KW);
+    const uint32_t rw = wave % RW, kw = (wave / RW) % 2, tw = wave / kOthers;
+    const uint32_t k0 = kw * 32u;                   // its keys of a tile
     const bool ropes = tw < 2;                      // RoPE half tw
     const int64_t capacity = p.head->capacity;
     Line<Slots> line(p, M, capacity <= 0, sh.exchange);
@@ -714,143 +715,118 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(const AttendParams p) 
 
         // this wave's query rows
         const uint32_t m = s.n > p.max_q ? p.max_q : s.n;
-        const uint32_t rows = m * p.heads, row0 = unit * M;
-        QFrag<T, P> q[R16];
-        uint32_t token[R16];
-#pragma unroll
-        for (int r = 0; r < R16; ++r) {
+        const uint32_t rows = m * p.heads, row0 = unit * M, mine = row0 + rw * 16u + l16;
+        QFrag<T, 1> q[1];
+        uint32_t token;
+        {
             // rows behind the last one repeat it and are not written
-            const uint32_t at = row0 + (rw * R16 + r) * 16u + l16, row = at < rows ? at : rows - 1;
-            const uint32_t i = row / p.heads, h = row - i * p.heads;
-            const uint64_t t = (uint64_t)s.q0 + i;
-            q[r].load(p.q_latent + t * p.q_latent_token + h * p.q_latent_head + tw * T * 128,
+            const uint32_t row = mine < rows ? mine : rows - 1;
+            token = row / p.heads;
+            const uint32_t h = row - token * p.heads;
+            const uint64_t t = (uint64_t)s.q0 + token;
+            q[0].load(p.q_latent + t * p.q_latent_token + h * p.q_latent_head + tw * T * 128,
                       p.q_rope + t * p.q_rope_token + h * p.q_rope_head + (tw & 1) * 32, g);
-            token[r] = i;
         }
         const View view = view_of<Slots>(p, seg, M, rows, row0);
         const uint32_t t_end = view.t_end;
 
         __builtin_amdgcn_sched_barrier(0);
-        f32x4 o[R16][NB];
-        float mx[R16], sum[R16];
+        f32x4 o[NB];
+        float mx = -INFINITY, sum = 0.f;
 #pragma unroll
-        for (int r = 0; r < R16; ++r) {
-            mx[r] = -INFINITY;
-            sum[r] = 0.f;
-#pragma unroll
-            for (int d = 0; d < NB; ++d) o[r][d] = f32x4{0.f, 0.f, 0.f, 0.f};
-        }
+        for (int d = 0; d < NB; ++d) o[d] = f32x4{0.f, 0.f, 0.f, 0.f};
 
         const Source<Slots> src{p, Slots ? nullptr : p.pages + (uint64_t)b * p.pages_stride,
                                 Slots ? p.slots + (uint64_t)b * p.slots_stride : nullptr, s.kv, capacity, sh.ring, sh.scales, sh.slots, wave, lane};
         int64_t pg[3];                                   // pages of tiles t, t + 1, t + 2
         src.start(t0, t_end, pg);
-#pragma unroll
-        for (int r = 0; r < R16; ++r) q[r].landed();
+        q[0].landed();
         __builtin_amdgcn_sched_barrier(0);
-        auto first_key = [&](uint32_t half) { return (KW == 2 ? kw : half) * 32u; };
-        // this wave's part of the scores of a step
-        auto part_of = [&](uint32_t t, uint32_t half, f32x4 (*x)[R16]) {
-            const uint32_t k0 = first_key(half);
+        // this wave's part of a tile's scores
+        auto part_of = [&](uint32_t t, f32x4 (*x)[1]) {
             const uint8_t* rows32 = sh.ring + ring_of(t) * kTileBytes + k0 * kRow;
-            scores32<R16, T, P>(x, rows32 + tw * T * 128, rows32 + 528 + (tw & 1) * 64,
-                                &sh.scales[ring_of(t)][tw * T][k0], q, p.scale_log2, ropes, l16, g);
+            scores32<1, T, 1>(x, rows32 + tw * T * 128, rows32 + 528 + (tw & 1) * 64,
+                              &sh.scales[ring_of(t)][tw * T][k0], q, p.scale_log2, ropes, l16, g);
         };
-        f32x4* const part = (f32x4*)sh.exchange + lane;  // [step & 1][wave][half u][r][lane]
-        auto give = [&](uint32_t step, f32x4 (*x)[R16]) {
+        f32x4* const part = (f32x4*)sh.exchange + lane;  // [step & 1][wave][half u][lane]
+        auto give = [&](uint32_t step, f32x4 (*x)[1]) {
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int r = 0; r < R16; ++r) part[((((step & 1u) * kWaves + wave) * 2 + u) * R16 + r) * 64] = x[u][r];
+            for (int u = 0; u < 2; ++u) part[(((step & 1u) * kWaves + wave) * 2 + u) * 64] = x[u][0];
         };
         // add up the parts of the waves that share rows and keys, in one order
-        auto gather = [&](uint32_t step, f32x4 (*x)[R16]) {
+        auto gather = [&](uint32_t step, f32x4 (*x)[1]) {
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
+            for (int u = 0; u < 2; ++u) {
+                const f32x4* from = part + (((step & 1u) * kWaves + wave) * 2 + u) * 64;
+                if (TW == 2) {
+                    x[u][0] += from[(int)((wave ^ kOthers) - wave) * 2 * 64];
+                } else {
+                    from -= tw * kOthers * 2 * 64;
+                    f32x4 total = from[0];
 #pragma unroll
-                for (int r = 0; r < R16; ++r) {
-                    const f32x4* from = part + ((((step & 1u) * kWaves + wave) * 2 + u) * R16 + r) * 64;
-                    if (TW == 2) {
-                        x[u][r] += from[(int)((wave ^ (RW * KW)) - wave) * 2 * R16 * 64];
-                    } else {
-                        from -= tw * RW * KW * 2 * R16 * 64;
-                        f32x4 total = from[0];
-#pragma unroll
-                        for (int k = 1; k < TW; ++k) total += from[k * RW * KW * 2 * R16 * 64];
-                        x[u][r] = total;
-                    }
+                    for (int k = 1; k < TW; ++k) total += from[k * kOthers * 2 * 64];
+                    x[u][0] = total;
                 }
+            }
         };
 
-        // A step is 32 keys a wave.  The next step's scores are formed beside this
-        // one's weights and values, so their waits overlap; one barrier a step
-        // publishes the parts, the next tile and that the last one is done with.
-        f32x4 x[2][R16];
+        // The next tile's scores are formed beside this one's weights and values, so
+        // their waits overlap; one barrier a tile publishes the parts, the next tile
+        // and that the last one is done with.
+        f32x4 x[2][1];
         uint64_t live = ~0ull;
         bool masked = false;
         auto look = [&](uint32_t t, int64_t page) {
             inspect<Slots>(p, src, seg, view, t, page, sh.ring + ring_of(t) * kTileBytes, &sh.scales[ring_of(t)][0][0], live, masked);
         };
-        constexpr uint32_t H = 2 / KW;                   // steps of a tile
         if (t0 < t_end) {
             wait_own(wave, t0 + 1 < t_end);
             barrier();
             look(t0, pg[0]);
-            part_of(t0, 0, x);
+            part_of(t0, x);
             give(0, x);
         }
-        uint32_t t = t0, half = 0;
-        for (uint32_t step = 0; t < t_end; ++step) {
-            const bool last = half + 1 == H, more = !last || t + 1 < t_end, fresh = last && more;
-            const uint32_t tn = fresh ? t + 1 : t, hn = !more ? half : last ? 0u : half + 1;
-            if (fresh) wait_own(wave, H == 2 && t + 2 < t_end);
+        uint32_t t = t0;
+        for (uint32_t step = 0; t < t_end; ++step) {     // counted apart from t: 10 registers less
+            const bool more = t + 1 < t_end;
+            if (more) wait_own(wave, false);
             barrier();
-            if (half == 0) src.ahead(t, t_end, pg);
+            src.ahead(t, t_end, pg);
             gather(step, x);
-            const uint32_t k0 = first_key(half);
             if (masked) {
-#pragma unroll
-                for (int r = 0; r < R16; ++r) {
-                    uint64_t on = live;
-                    if (!Slots) on &= sees<Slots>(p, s, token[r]).bits(t * 64u);
-                    on >>= k0;
-#pragma unroll
-                    for (int u = 0; u < 2; ++u)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) x[u][r][i] = (on >> (key_of(u, g) + i)) & 1u ? x[u][r][i] : -INFINITY;
-                }
-            }
-            if (fresh) look(t + 1, pg[1]);
-#pragma unroll
-            for (int r = 0; r < R16; ++r) {
-                float top = fmaxf(fmaxf(fmaxf(x[0][r][0], x[0][r][1]), fmaxf(x[0][r][2], x[0][r][3])),
-                                  fmaxf(fmaxf(x[1][r][0], x[1][r][1]), fmaxf(x[1][r][2], x[1][r][3])));
-                if (__any(top > mx[r] + kLazy || (mx[r] == -INFINITY && top > mx[r]))) {
-                    top = fmaxf(top, __shfl_xor(top, 16));
-                    top = fmaxf(top, __shfl_xor(top, 32));
-                    const float next = fmaxf(mx[r], top);
-                    const float keep = mx[r] == -INFINITY ? 0.f : exp2f(mx[r] - next);
-                    mx[r] = next;
-                    sum[r] *= keep;
-#pragma unroll
-                    for (int d = 0; d < NB; ++d) o[r][d] *= keep;
-                }
-            }
-            // the next step's scores (behind the last step: this one's again, not used)
-            f32x4 xn[2][R16];
-            part_of(tn, hn, xn);
-            // weights
-#pragma unroll
-            for (int r = 0; r < R16; ++r) {
-                const float ref = mx[r] == -INFINITY ? 0.f : mx[r];
+                uint64_t on = live;
+                if (!Slots) on &= sees<Slots>(p, s, token).bits(t * 64u);
+                on >>= k0;
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        x[u][r][i] = __builtin_amdgcn_exp2f(x[u][r][i] - ref);
-                        sum[r] += x[u][r][i];
-                    }
+                    for (int i = 0; i < 4; ++i) x[u][0][i] = (on >> (key_of(u, g) + i)) & 1u ? x[u][0][i] : -INFINITY;
             }
+            if (more) look(t + 1, pg[1]);
+            float top = fmaxf(fmaxf(fmaxf(x[0][0][0], x[0][0][1]), fmaxf(x[0][0][2], x[0][0][3])),
+                              fmaxf(fmaxf(x[1][0][0], x[1][0][1]), fmaxf(x[1][0][2], x[1][0][3])));
+            if (__any(top > mx + kLazy || (mx == -INFINITY && top > mx))) {
+                top = fmaxf(top, __shfl_xor(top, 16));
+                top = fmaxf(top, __shfl_xor(top, 32));
+                const float next = fmaxf(mx, top);
+                const float keep = mx == -INFINITY ? 0.f : exp2f(mx - next);
+                mx = next;
+                sum *= keep;
+#pragma unroll
+                for (int d = 0; d < NB; ++d) o[d] *= keep;
+            }
+            // the next tile's scores (behind the last tile: this one's again, not used)
+            f32x4 xn[2][1];
+            part_of(more ? t + 1 : t, xn);
+            // weights
+            const float ref = mx == -INFINITY ? 0.f : mx;
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    x[u][0][i] = __builtin_amdgcn_exp2f(x[u][0][i] - ref);
+                    sum += x[u][0][i];
+                }
             // values: 8 keys of this lane group (4 of each half) x 16 columns
             const uint32_t vk = key_of(l16 >> 3, g) + ((l16 >> 1) & 3u);
             const uint8_t* vrow = sh.ring + ring_of(t) * kTileBytes + (k0 + vk) * kRow + (l16 & 1u) * 8u + tw * NB * 16;
@@ -859,69 +835,54 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(const AttendParams p) 
             for (int u = 0; u < 2; ++u) scale[u] = &sh.scales[ring_of(t)][tw * T][k0 + key_of(u, g) + (l16 & 3)];
 #pragma unroll
             for (int j = 0; j < T; ++j) {
-                bf16x8 w[R16];
+                bf16x8 w;
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     const f32x4 a = quads(scale[u][j * 64]);
 #pragma unroll
-                    for (int r = 0; r < R16; ++r)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) w[r][u * 4 + i] = (__bf16)(a[i] * x[u][r][i]);
+                    for (int i = 0; i < 4; ++i) w[u * 4 + i] = (__bf16)(a[i] * x[u][0][i]);
                 }
 #pragma unroll
                 for (int d = j * 8; d < j * 8 + 8; ++d) {
                     const i32x2 c = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lptr<i32x2>)(vrow + d * 16));
-                    const bf16x8 v = widen(c.x, c.y);
-#pragma unroll
-                    for (int r = 0; r < R16; ++r) o[r][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, w[r], o[r][d], 0, 0, 0);
+                    o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen(c.x, c.y), w, o[d], 0, 0, 0);
                 }
             }
             if (!more) break;
             give(step + 1, xn);
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int r = 0; r < R16; ++r) x[u][r] = xn[u][r];
-            half = hn;
-            if (fresh) {
-                t = tn;
-                src.turn(t, t_end, pg);
-            }
+            for (int u = 0; u < 2; ++u) x[u][0] = xn[u][0];
+            ++t;
+            src.turn(t, t_end, pg);
         }
         barrier();    // the ring is free
 
         // join the key halves, then write
+        sum += __shfl_xor(sum, 16);
+        sum += __shfl_xor(sum, 32);
+        f32x4* ex = (f32x4*)sh.ring + (uint32_t)(tw * RW + rw) * (NB * 64) + lane;
+        float* stat = (float*)(sh.ring + kWaves / 2 * NB * 1024) + (uint32_t)(tw * RW + rw) * 128 + lane;
+        if (kw == 1) {
 #pragma unroll
-        for (int r = 0; r < R16; ++r) {
-            sum[r] += __shfl_xor(sum[r], 16);
-            sum[r] += __shfl_xor(sum[r], 32);
-            if (KW == 2) {
-                f32x4* ex = (f32x4*)sh.ring + (uint32_t)((tw * RW + rw) * R16 + r) * (NB * 64) + lane;
-                float* stat = (float*)(sh.ring + kWaves / 2 * R16 * NB * 1024) + (uint32_t)((tw * RW + rw) * R16 + r) * 128 + lane;
-                if (kw == 1) {
+            for (int d = 0; d < NB; ++d) ex[d * 64] = o[d];
+            stat[0] = mx;
+            stat[64] = sum;
+        }
+        barrier();
+        if (kw == 0) {
+            const float m2 = stat[0], s2 = stat[64];
+            const float next = fmaxf(mx, m2);
+            const float k1 = mx == -INFINITY ? 0.f : exp2f(mx - next), k2 = m2 == -INFINITY ? 0.f : exp2f(m2 - next);
+            // a NaN sum with no maximum (every weight of a half a NaN) has to stay one
+            sum = (mx == -INFINITY ? sum : sum * k1) + (m2 == -INFINITY ? s2 : s2 * k2);
+            mx = next;
 #pragma unroll
-                    for (int d = 0; d < NB; ++d) ex[d * 64] = o[r][d];
-                    stat[0] = mx[r];
-                    stat[64] = sum[r];
-                }
-                barrier();
-                if (kw == 0) {
-                    const float m2 = stat[0], s2 = stat[64];
-                    const float next = fmaxf(mx[r], m2);
-                    const float k1 = mx[r] == -INFINITY ? 0.f : exp2f(mx[r] - next), k2 = m2 == -INFINITY ? 0.f : exp2f(m2 - next);
-                    // a NaN sum with no maximum (every weight of a half a NaN) has to stay one
-                    sum[r] = (mx[r] == -INFINITY ? sum[r] : sum[r] * k1) + (m2 == -INFINITY ? s2 : s2 * k2);
-                    mx[r] = next;
-#pragma unroll
-                    for (int d = 0; d < NB; ++d) {
-                        if (d % 4 == 0) __builtin_amdgcn_sched_barrier(0);
-                        const f32x4 other = ex[d * 64];
-                        o[r][d] = o[r][d] * (mx[r] == -INFINITY ? 1.f : k1) + other * (mx[r] == -INFINITY ? 1.f : k2);
-                    }
-                }
+            for (int d = 0; d < NB; ++d) {
+                if (d % 4 == 0) __builtin_amdgcn_sched_barrier(0);
+                const f32x4 other = ex[d * 64];
+                o[d] = o[d] * (mx == -INFINITY ? 1.f : k1) + other * (mx == -INFINITY ? 1.f : k2);
             }
-            const uint32_t at = (rw * R16 + r) * 16u + l16;
-            if (kw == 0 && row0 + at < rows) write_row<M, NB>(p, seg, at, tw * NB * 16, o[r], mx[r], sum[r], g);
+            if (mine < rows) write_row<M, NB>(p, seg, rw * 16u + l16, tw * NB * 16, o, mx, sum, g);
         }
         barrier();    // before the ring takes the next unit's tiles
     }
@@ -1397,11 +1358,11 @@ hipError_t launch_attend(const AttendParams& given, void* workspace, hipStream_t
     (void)hipGetLastError();
     const dim3 grid(a.blocks), block(kThreads);
     if (a.rows == 16) {
-        if (p.by_slots) attend_kernel<1, 1, 4, 2, true><<<grid, block, 0, stream>>>(p);
-        else attend_kernel<1, 1, 4, 2, false><<<grid, block, 0, stream>>>(p);
+        if (p.by_slots) attend_kernel<1, true><<<grid, block, 0, stream>>>(p);
+        else attend_kernel<1, false><<<grid, block, 0, stream>>>(p);
     } else if (a.rows == 32) {
-        if (p.by_slots) attend_kernel<1, 2, 2, 2, true><<<grid, block, 0, stream>>>(p);
-        else attend_kernel<1, 2, 2, 2, false><<<grid, block, 0, stream>>>(p);
+        if (p.by_slots) attend_kernel<2, true><<<grid, block, 0, stream>>>(p);
+        else attend_kernel<2, false><<<grid, block, 0, stream>>>(p);
     } else {
         if (p.by_slots) attend_wide_kernel<true><<<grid, block, 0, stream>>>(p);
         else attend_wide_kernel<false><<<grid, block, 0, stream>>>(p);
