@@ -1123,21 +1123,39 @@ __global__ __launch_bounds__(256) void combine_kernel(const AttendParams p, uint
         const uint32_t w0 = first / each, w1 = (first + s.tiles - 1) / each;
         if (w0 == w1) continue;
         const uint32_t in = row - unit * M;
-        float top = -INFINITY;
-        for (uint32_t w = w0; w <= w1; ++w) {
-            const uint64_t at = (uint64_t)(2 * w + (w == w0 && first != w0 * each ? 1 : 0)) * M + in;
-            top = fmaxf(top, p.part_lse[at]);
+        // four parts at a time, their sums and rows on the way together; behind the
+        // last part it again, with no weight
+        float top = -INFINITY, total = 0.f;
+        f32x4 o = {0.f, 0.f, 0.f, 0.f};
+        for (uint32_t w = w0; w <= w1; w += 4) {
+            float lse[4];
+            f32x4 v[4];
+#pragma unroll
+            for (uint32_t k = 0; k < 4; ++k) {
+                const uint32_t c = w + k < w1 ? w + k : w1;
+                const uint64_t at = (uint64_t)(2 * c + (c == w0 && first != w0 * each ? 1 : 0)) * M + in;
+                lse[k] = p.part_lse[at];
+                v[k] = *(const f32x4*)(p.part + at * 512 + col);
+            }
+            float next = top;
+#pragma unroll
+            for (uint32_t k = 0; k < 4; ++k) {
+                lse[k] = w + k <= w1 ? lse[k] : -INFINITY;
+                next = fmaxf(next, lse[k]);
+            }
+            const float keep = top == -INFINITY ? 1.f : exp2f(top - next);      // nothing with a weight yet, or a NaN
+            total *= keep;
+            o *= keep;
+            top = next;
+            const float ref = top == -INFINITY ? 0.f : top;
+#pragma unroll
+            for (uint32_t k = 0; k < 4; ++k) {
+                const float e = exp2f(lse[k] - ref);
+                total += e;
+                o += v[k] * e;
+            }
         }
         const float ref = top == -INFINITY ? 0.f : top;
-        float total = 0.f;
-        f32x4 o = {0.f, 0.f, 0.f, 0.f};
-        for (uint32_t w = w0; w <= w1; ++w) {
-            const uint64_t at = (uint64_t)(2 * w + (w == w0 && first != w0 * each ? 1 : 0)) * M + in;
-            const float k = exp2f(p.part_lse[at] - ref);
-            const f32x4 v = *(const f32x4*)(p.part + at * 512 + col);
-            total += k;
-            o += v * k;
-        }
         const uint32_t i = row / p.heads, h = row - i * p.heads;
         const uint64_t t = (uint64_t)s.q0 + i;
         o = o * (total == 0.f ? 0.f : 1.f / total);
