@@ -280,11 +280,10 @@ __device__ __forceinline__ uint32_t scan64(uint32_t x, uint32_t lane) {
     return x;
 }
 
-// Tiles a block takes: an equal share, at least `least` (a shorter run costs more
-// in partial results than it gains).
-__device__ __forceinline__ uint32_t share(const AttendParams& p, uint32_t total, uint32_t blocks) {
+// Tiles a block takes: an equal share.
+__device__ __forceinline__ uint32_t share(uint32_t total, uint32_t blocks) {
     const uint32_t c = (total + blocks - 1) / blocks;
-    return c < p.least ? p.least : c;
+    return c < 1 ? 1 : c;
 }
 
 struct Place {
@@ -307,7 +306,7 @@ __device__ __forceinline__ Place place(const AttendParams& p, uint32_t M, bool e
         }
         const uint32_t x = p.num_seqs == 1 ? w : scan64(w, lane), first = x - w;
         r.total = __builtin_amdgcn_readlane(x, p.num_seqs - 1);
-        r.each = share(p, r.total, gridDim.x);
+        r.each = share(r.total, gridDim.x);
         const uint32_t at = r.each * blockIdx.x;
         const uint64_t here = __ballot(w && at >= first && at < x);
         r.b = here ? (uint32_t)__builtin_ctzll(here) : 0u;
@@ -341,11 +340,11 @@ __device__ __forceinline__ Place place(const AttendParams& p, uint32_t M, bool e
                     scan[kWaves + 1] = at - first;
                 }
             }
-            if (pass == 0) at = share(p, carry, gridDim.x) * blockIdx.x;
+            if (pass == 0) at = share(carry, gridDim.x) * blockIdx.x;
         }
         __syncthreads();
         r.total = __builtin_amdgcn_readfirstlane(carry);
-        r.each = share(p, r.total, gridDim.x);
+        r.each = share(r.total, gridDim.x);
         r.b = __builtin_amdgcn_readfirstlane(scan[kWaves]);
         r.off = __builtin_amdgcn_readfirstlane(scan[kWaves + 1]);
         __syncthreads();
@@ -376,7 +375,7 @@ struct Line {
             const Seq s = sequence<true, true>(p, 0, M, empty);
             const uint32_t w = s.units * s.tiles;
             at.total = p.num_seqs * w;
-            at.each = share(p, at.total, gridDim.x);
+            at.each = share(at.total, gridDim.x);
             at.b = at.each * blockIdx.x / w;
             at.off = at.each * blockIdx.x - at.b * w;
         } else {
@@ -1331,26 +1330,26 @@ hipError_t launch_combine(const AttendParams& p, uint32_t M, hipStream_t stream)
 
 AttendPlan plan_attend(uint64_t rows, uint64_t num_seqs, uint64_t num_tokens, uint64_t heads, uint64_t max_kv) {
     AttendPlan a;
-    a.least = 2;
     const uint64_t tiles = max_kv ? (max_kv + 63) / 64 : 1;
     uint64_t units = 0;
     const auto runs_of = [&](uint32_t M) {
         units = num_seqs * ((rows + M - 1) / M);
         const uint64_t by_tokens = num_tokens * heads / M + num_seqs;       // ragged: no more units than that
         units = units < by_tokens ? units : by_tokens;
-        return units * ((tiles + a.least - 1) / a.least) + 1;
+        return units * tiles + 1;
     };
     // Rows of a unit.  64 (attend_wide_kernel) from ten tiles a block on: its tile of 64
     // rows takes 3.1 us, two of 32 rows 4.2 us, but it starts 8 us later (16 sequences
     // of 128 heads, 4096 positions: 56.4 us against 54.9; 8192: 81.3 against 88.6).
-    // 16 where that holds all rows, or where the line has so few runs that a block each
-    // still leaves CUs idle (4 tokens of 64 heads, 256 slots: 15.4 us against 23).
+    // 16 where that holds all rows, or where a line of longer units would leave CUs idle
+    // (4 tokens of 64 heads, 256 slots: 15.4 us against 23 with units of 64 rows).  A run
+    // may be one tile: 12.4 us then, against 14.7 with two at least.
     uint64_t runs = runs_of(64);
     a.rows = 64;
     if (rows <= 32 || units * tiles < 10 * 256) {
         runs = runs_of(16);
         a.rows = 16;
-        if (rows > 16 && runs > 256) {
+        if (rows > 16 && runs > 512) {
             runs = runs_of(32);
             a.rows = 32;
         }
@@ -1368,7 +1367,6 @@ hipError_t launch_attend(const AttendParams& given, void* workspace, hipStream_t
     AttendParams p = given;
     const AttendPlan a = plan_attend((uint64_t)p.max_q * p.heads, p.num_seqs, p.num_tokens, p.heads,
                                      p.by_slots ? p.num_slots : p.max_kv);
-    p.least = a.least;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     p.line = reinterpret_cast<uint32_t*>(ws);
     p.part_lse = reinterpret_cast<float*>(ws + a.line_bytes);
@@ -1392,7 +1390,6 @@ hipError_t launch_attend(const AttendParams& given, void* workspace, hipStream_t
 hipError_t launch_attend_weights(const AttendParams& given, hipStream_t stream) {
     AttendParams p = given;
     p.line = nullptr;
-    p.least = 1;
     const uint64_t tiles = (uint64_t)((p.max_kv + 63) / 64) * p.num_seqs;
     (void)hipGetLastError();
     const dim3 grid((uint32_t)(tiles < 256 ? tiles : 256));

@@ -117,7 +117,6 @@ struct AttendParams {
     const float* weights_in;     // weights only
     float* weights_out;
     int64_t weights_stride;
-    uint32_t least;              // fewest tiles of a block
     uint32_t* line;              // workspace: prefix of each sequence's work, then the blocks' share (weights: null)
     float* part_lse;             // workspace: [blocks * 2][rows]
     float* part;                 // workspace: [blocks * 2][rows][512]
@@ -127,7 +126,6 @@ struct AttendParams {
 struct AttendPlan {
     uint32_t rows;
     uint32_t blocks;
-    uint32_t least;
     bool fits;                   // fewer than 2^31 tiles in all
     uint64_t line_bytes;
     uint64_t lse_bytes;
