@@ -687,8 +687,8 @@ __device__ __forceinline__ void write_row(const AttendParams& p, const Segment& 
 // and takes its tiles' columns of the output.  The widening (4 instructions for 8
 // codes) is what the vector unit spends most of its time on.  Splitting the values
 // keeps a wave's share of the queries small: a first tile is under way 2 us earlier
-// than with whole rows (one sequence of 700 positions, 16 heads: 17 us, of which 6
-// join; whole rows 21 us).
+// than with whole rows (one sequence of 700 positions, 16 heads: 14 us, of which 4
+// join; whole rows 5 us more).
 template <int RW, bool Slots>
 __global__ __launch_bounds__(kThreads) void attend_kernel(const AttendParams p) {
     constexpr int M = 16 * RW;
@@ -1104,8 +1104,9 @@ __global__ __launch_bounds__(kThreads) void attend_wide_kernel(const AttendParam
 
 // Joins the partial results of units that were cut between blocks: a group of
 // 128 threads takes one (token, head) row, 4 columns a thread, and adds the
-// blocks' parts in order.  4 us for 256 rows of 2 parts (a chain of four reads from
-// memory), 14 us for 8192 rows of 1 to 3 parts.
+// blocks' parts in order, four on their way together (one at a time: 2.5 us more for
+// 6 parts).  4 us for 256 rows of 4 parts, a chain of three reads from memory; 12 us
+// for 8192 rows of 1 to 3 parts.
 template <bool Slots>
 __global__ __launch_bounds__(256) void combine_kernel(const AttendParams p, uint32_t M) {
     const uint32_t each = p.line[p.num_seqs];
