@@ -398,7 +398,9 @@ typedef struct {
 KVPUB_API uint64_t kvpub_evict_workspace(const kvpub_evict_io *io);
 
 /* Evict asynchronously on `stream`.  weights, tables, kept and lengths are
- * 4-byte aligned, the workspace 16-byte.  A poisoned context changes nothing. */
+ * 4-byte aligned, the workspace 16-byte.  A poisoned context changes nothing;
+ * if it is poisoned while the call runs, each sequence is evicted whole (rows,
+ * weights, kept and new_len) or left as it was. */
 KVPUB_API kvpub_status kvpub_evict(kvpub_ctx *ctx, uint32_t layer, const kvpub_evict_io *io, void *workspace,
                                    uint64_t workspace_bytes, kvpub_stream_t stream);
 

@@ -21,6 +21,12 @@
 // whose blocks already run and raise theirs before waiting for anything, so
 // every wait ends.
 //
+// A fence on another lane may poison the context at any time.  One thread of
+// select_kernel reads the status, once for its sequence, and leaves the decision
+// in the workspace; all waves of its block and of move_kernel's go by that word,
+// so a sequence is evicted whole or left as it was, and no wave leaves a block
+// that others wait in.
+//
 // Measured: 32 sequences of up to 16384 positions to 8192, two replicas, 624 MB:
 // select 27 us, move 94 us, 124 us in all, what a copy of the bytes takes (5 TB/s);
 // 4 of 1000 to 256: 8 and 5 us, 21 us in all, the passes' barriers and the launches.
@@ -40,8 +46,7 @@ constexpr int kSelWaves = kSelThreads / 64;
 constexpr uint32_t kLdsKeys = 32768;
 constexpr int kMoveThreads = 256;
 constexpr uint32_t kMoveBlocks = 1u << 22;         // chunks of a launch
-
-__device__ __forceinline__ bool poisoned(const CtxHead* head) { return (head->status & kStatusPoisoned) != 0; }
+constexpr uint32_t kSkipped = ~0u;                 // ranks[0] of a sequence that is left as it was (else 0)
 
 // Larger for larger weights; -0 as +0, a NaN below everything.
 __device__ __forceinline__ uint32_t order(float w) {
@@ -55,11 +60,11 @@ struct SelectShared {
     uint32_t hist[kSelWaves][256];
     uint32_t above[kSelWaves], equal[kSelWaves];
     uint32_t prefix, need;
+    uint32_t status;
 };
 
 __global__ __launch_bounds__(kSelThreads) void select_kernel(const EvictParams p) {
     __shared__ SelectShared sh;
-    if (poisoned(p.head)) return;
     const uint32_t b = blockIdx.x, tid = threadIdx.x, lane = tid & 63u;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int32_t given = p.kv_len[b];
@@ -69,6 +74,16 @@ __global__ __launch_bounds__(kSelThreads) void select_kernel(const EvictParams p
     uint32_t* mine = p.state + (uint64_t)b * (2 * p.chunks + 2);
     uint32_t* flags = mine + 1;
     uint32_t* ranks = mine + 1 + p.chunks;             // kept positions below 64 * c, c = 0..chunks
+    const float* w = p.weights_in + (uint64_t)b * p.weights_stride;
+    const bool cached = len <= kLdsKeys;
+    if (tid == 0) sh.status = __hip_atomic_load(&p.head->status, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (cached && len > p.budget)
+        for (uint32_t i = tid; i < len; i += kSelThreads) sh.key[i] = order(w[i]);
+    __syncthreads();
+    if (sh.status & kStatusPoisoned) {
+        if (tid == 0) ranks[0] = kSkipped;
+        return;
+    }
     if (tid == 0) {
         mine[0] = 0;
         p.new_len[b] = (int32_t)keep;
@@ -81,14 +96,8 @@ __global__ __launch_bounds__(kSelThreads) void select_kernel(const EvictParams p
         for (uint32_t c = tid; c <= p.chunks; c += kSelThreads) ranks[c] = c * 64u < len ? c * 64u : len;
         return;
     }
-    const float* w = p.weights_in + (uint64_t)b * p.weights_stride;
     const uint32_t a = p.first, z = len - p.last;     // the unprotected positions; budget < len, so a < z
     const uint32_t k = p.budget - p.first - p.last;
-    const bool cached = len <= kLdsKeys;
-    if (cached) {
-        for (uint32_t i = tid; i < len; i += kSelThreads) sh.key[i] = order(w[i]);
-        __syncthreads();
-    }
     auto key = [&](uint32_t i) { return cached ? sh.key[i] : order(w[i]); };
 
     // the k-th largest key, bits from the top: prefix is what is known of it
@@ -184,19 +193,19 @@ template <bool Ordered>
 __global__ __launch_bounds__(kMoveThreads) void move_kernel(const EvictParams p, uint32_t seq0, uint32_t chunk0) {
     __shared__ uint64_t src[64], dst[64], isrc[64], idst[64];    // ~0: not copied
     __shared__ uint32_t ticket;
-    if (poisoned(p.head)) return;
     const uint32_t b = seq0 + blockIdx.y, tid = threadIdx.x;
     uint32_t* mine = p.state + (uint64_t)b * (2 * p.chunks + 2);
     uint32_t* flags = mine + 1;
     const uint32_t* ranks = mine + 1 + p.chunks;
+    const uint32_t decision = ranks[0], keep = (uint32_t)p.new_len[b];
+    const int64_t pages = p.head->capacity / 64;
+    if (decision == kSkipped) return;                  // the same for all waves: nothing writes it meanwhile
     uint32_t c = chunk0 + blockIdx.x;
     if (Ordered) {
         if (tid == 0) ticket = atomicAdd(mine, 1u);
         __syncthreads();
         c = ticket;
     }
-    const uint32_t keep = (uint32_t)p.new_len[b];
-    const int64_t pages = p.head->capacity / 64;
     const uint32_t i0 = c * 64u;
     float weight = 0.f;
     uint64_t my_isrc = ~0ull, my_idst = ~0ull;
