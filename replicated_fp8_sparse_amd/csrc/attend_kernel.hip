@@ -35,7 +35,9 @@
 //
 // Work split.  All units' tiles form one line that the blocks cut into equal
 // runs, whatever the lengths of the sequences; a unit cut between blocks leaves
-// partial results that combine_kernel joins in block order.
+// partial results that combine_kernel joins in block order.  The block that has a
+// cut unit's first tiles names it, so the join visits those units and no others:
+// what it costs goes by the blocks, not by the call's bounds.
 #include "kvpub_internal.h"
 
 #include <type_traits>
@@ -58,6 +60,8 @@ constexpr int kWaves = 8;                        // two a SIMD: 256 registers ea
 constexpr int kThreads = kWaves * 64;
 constexpr float kLn2 = 0.693147180559945309f;
 constexpr float kLazy = 8.0f;                    // rescale when a maximum grows past 2^8
+constexpr uint32_t kMostBlocks = 256;            // of a launch: one a CU
+constexpr uint64_t kCutBytes = kMostBlocks * (sizeof(uint32_t) + sizeof(AttendCut));
 
 // LDS: the tile ring (after the last tile it holds the join of key halves), the
 // waves' exchange of partial scores, the tiles' scales by tile of 128, slot
@@ -292,11 +296,9 @@ struct Place {
 };
 
 // Where this block's run begins, from prefix sums of the sequences' work: by each
-// wave alone up to 64 sequences, else by the whole block.  Block 0 leaves the
-// prefixes and the share for combine_kernel, where there is one.
+// wave alone up to 64 sequences, else by the whole block.
 __device__ __forceinline__ Place place(const AttendParams& p, uint32_t M, bool empty, uint8_t* scratch) {
     const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = tid >> 6;
-    const bool first_block = blockIdx.x == 0;
     Place r;
     if (p.num_seqs <= 64) {
         uint32_t w = 0;
@@ -311,7 +313,6 @@ __device__ __forceinline__ Place place(const AttendParams& p, uint32_t M, bool e
         const uint64_t here = __ballot(w && at >= first && at < x);
         r.b = here ? (uint32_t)__builtin_ctzll(here) : 0u;
         r.off = at - __builtin_amdgcn_readlane(first, r.b);
-        if (p.line && first_block && tid < p.num_seqs) p.line[tid] = first;
     } else {
         uint32_t* scan = (uint32_t*)scratch;
         uint32_t carry = 0, at = 0;
@@ -334,7 +335,6 @@ __device__ __forceinline__ Place place(const AttendParams& p, uint32_t M, bool e
                     carry += scan[v];
                 }
                 const uint32_t first = before + x - w;
-                if (p.line && pass == 0 && first_block && b < p.num_seqs) p.line[b] = first;
                 if (pass == 1 && w && at >= first && at < first + w) {
                     scan[kWaves] = b;
                     scan[kWaves + 1] = at - first;
@@ -384,7 +384,6 @@ struct Line {
         b = __builtin_amdgcn_readfirstlane(at.b);      // the same for the block: kept in scalar registers
         off = __builtin_amdgcn_readfirstlane(at.off);
         const uint32_t each = __builtin_amdgcn_readfirstlane(at.each), total = __builtin_amdgcn_readfirstlane(at.total);
-        if (p.line && blockIdx.x == 0 && threadIdx.x == 0) p.line[p.num_seqs] = each;
         pos = begin = each * blockIdx.x;
         end = begin + each < total ? begin + each : total;
     }
@@ -403,6 +402,17 @@ struct Line {
             return true;
         }
         return false;
+    }
+    // Names for combine_kernel the unit that this block began and others end, if
+    // there is one: it can only be the last segment's.
+    __device__ __forceinline__ void leave_none() const {
+        if (begin >= end && threadIdx.x == 0) p.cut_last[blockIdx.x] = 0;
+    }
+    __device__ __forceinline__ void leave(const Segment& g, uint32_t rows) const {
+        if (pos < end || threadIdx.x != 0) return;
+        const uint32_t rest = g.s.tiles - g.t1, each = end - begin;     // a run that is cut is a whole share
+        p.cut_last[blockIdx.x] = g.t0 == 0 && rest ? blockIdx.x + (rest + each - 1) / each : 0u;
+        p.cuts[blockIdx.x] = AttendCut{g.slot, g.s.q0, g.unit * M, rows};
     }
 };
 
@@ -707,6 +717,7 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(const AttendParams p) 
     const bool ropes = tw < 2;                      // RoPE half tw
     const int64_t capacity = p.head->capacity;
     Line<Slots> line(p, M, capacity <= 0, sh.exchange);
+    line.leave_none();
     Segment seg;
     while (line.next(seg)) {
         const Seq& s = seg.s;
@@ -883,6 +894,7 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(const AttendParams p) 
             }
             if (mine < rows) write_row<M, NB>(p, seg, rw * 16u + l16, tw * NB * 16, o, mx, sum, g);
         }
+        line.leave(seg, rows);
         barrier();    // before the ring takes the next unit's tiles
     }
 }
@@ -916,6 +928,7 @@ __global__ __launch_bounds__(kThreads) void attend_wide_kernel(const AttendParam
     const uint32_t rp = wave & 1u, j = wave >> 1;        // values: rows 32 rp, tile j
     const int64_t capacity = p.head->capacity;
     Line<Slots> line(p, M, capacity <= 0, (uint8_t*)sh.weights);
+    line.leave_none();
     Segment seg;
     if (threadIdx.x < 2) sh.flag[threadIdx.x] = 0;       // seen by all after the first barrier of a segment
     while (line.next(seg)) {
@@ -1098,31 +1111,45 @@ __global__ __launch_bounds__(kThreads) void attend_wide_kernel(const AttendParam
             const float total = sums[rp * 2 + r][0][l16] + sums[rp * 2 + r][1][l16];
             if (row0 + at < rows) write_row<M, 8>(p, seg, at, j * 128, o[r], mo[r], total, g);
         }
+        line.leave(seg, rows);
         barrier();    // before the ring and the sums serve the next unit
     }
 }
 
-// Joins the partial results of units that were cut between blocks: a group of
-// 128 threads takes one (token, head) row, 4 columns a thread, and adds the
-// blocks' parts in order, four on their way together (one at a time: 2.5 us more for
-// 6 parts).  4 us for 256 rows of 4 parts, a chain of three reads from memory; 12 us
-// for 8192 rows of 1 to 3 parts.
-template <bool Slots>
-__global__ __launch_bounds__(256) void combine_kernel(const AttendParams p, uint32_t M) {
-    const uint32_t each = p.line[p.num_seqs];
-    const bool empty = p.head->capacity <= 0;
-    const uint32_t col = (threadIdx.x & 127u) * 4u;
-    const uint64_t per = (uint64_t)p.max_q * p.heads, all = per * p.num_seqs;
-    for (uint64_t x = (uint64_t)blockIdx.x * 2 + (threadIdx.x >> 7); x < all; x += (uint64_t)gridDim.x * 2) {
-        const uint32_t b = (uint32_t)(x / per), row = (uint32_t)(x - b * per);
-        const Seq s = sequence<Slots, false>(p, b, M, empty);
-        const uint32_t m = s.n > p.max_q ? p.max_q : s.n;
-        if (row >= m * p.heads) continue;
-        const uint32_t unit = row / M;
-        const uint32_t first = (Slots ? b * s.units * s.tiles : p.line[b]) + unit * s.tiles;
-        const uint32_t w0 = first / each, w1 = (first + s.tiles - 1) / each;
-        if (w0 == w1) continue;
-        const uint32_t in = row - unit * M;
+// Joins the partial results of the units that were cut between blocks: a group of
+// 128 threads takes one (token, head) row, 4 columns a thread, and adds the blocks'
+// parts in order, four on their way together (one at a time: 2.5 us more for 6
+// parts).  Each wave counts the cut units for itself, by ballots over the blocks'
+// notes: a grid with blocks for units that are not there costs 4 us more.
+__global__ __launch_bounds__(256) void combine_kernel(const AttendParams p, uint32_t M, uint32_t blocks) {
+    const uint32_t lane = threadIdx.x & 63u, col = (threadIdx.x & 127u) * 4u;
+    uint32_t last[4];
+    uint64_t mask[4];
+    uint32_t cut = 0;
+#pragma unroll
+    for (uint32_t j = 0; j < 4; ++j) last[j] = j * 64u + lane < blocks ? p.cut_last[j * 64u + lane] : 0u;
+#pragma unroll
+    for (uint32_t j = 0; j < 4; ++j) {
+        mask[j] = __ballot(last[j] != 0);
+        cut += (uint32_t)__popcll(mask[j]);
+    }
+    for (uint32_t x = blockIdx.x * 2u + (threadIdx.x >> 7); x < cut * M; x += gridDim.x * 2u) {
+        // the unit that block w0 began and block w1 ends, by its place among the cut ones
+        uint32_t k = __builtin_amdgcn_readfirstlane(x >> __builtin_ctz(M)), w0 = 0, w1 = 0;
+#pragma unroll
+        for (uint32_t j = 0; j < 4; ++j) {
+            const uint32_t n = (uint32_t)__popcll(mask[j]);
+            if (w1 == 0 && k < n) {
+                const bool it = ((mask[j] >> lane) & 1u) && (uint32_t)__popcll(mask[j] & ((1ull << lane) - 1)) == k;
+                const uint32_t at = (uint32_t)__builtin_ctzll(__ballot(it));
+                w0 = j * 64u + at;
+                w1 = __builtin_amdgcn_readlane(last[j], at);
+            }
+            k -= n;
+        }
+        const kptr<AttendCut> unit = (kptr<AttendCut>)(p.cuts + w0);
+        const uint32_t in = x & (M - 1), row = unit->row0 + in, slot = unit->slot, q0 = unit->q0;
+        if (row >= unit->rows) continue;
         // four parts at a time, their sums and rows on the way together; behind the
         // last part it again, with no weight
         float top = -INFINITY, total = 0.f;
@@ -1133,7 +1160,7 @@ __global__ __launch_bounds__(256) void combine_kernel(const AttendParams p, uint
 #pragma unroll
             for (uint32_t k = 0; k < 4; ++k) {
                 const uint32_t c = w + k < w1 ? w + k : w1;
-                const uint64_t at = (uint64_t)(2 * c + (c == w0 && first != w0 * each ? 1 : 0)) * M + in;
+                const uint64_t at = (uint64_t)(c == w0 ? slot : 2 * c) * M + in;
                 lse[k] = p.part_lse[at];
                 v[k] = *(const f32x4*)(p.part + at * 512 + col);
             }
@@ -1157,7 +1184,7 @@ __global__ __launch_bounds__(256) void combine_kernel(const AttendParams p, uint
         }
         const float ref = top == -INFINITY ? 0.f : top;
         const uint32_t i = row / p.heads, h = row - i * p.heads;
-        const uint64_t t = (uint64_t)s.q0 + i;
+        const uint64_t t = (uint64_t)q0 + i;
         o = o * (total == 0.f ? 0.f : 1.f / total);
         *(bf16x4*)(p.out + t * p.out_token + h * p.out_head + col) = __builtin_convertvector(o, bf16x4);
         if (p.lse && col == 0) p.lse[t * p.lse_token + h] = total == 0.f ? -INFINITY : (ref + log2f(total)) * kLn2;
@@ -1319,14 +1346,6 @@ __global__ __launch_bounds__(kThreads) void weights_kernel(const AttendParams p)
     }
 }
 
-hipError_t launch_combine(const AttendParams& p, uint32_t M, hipStream_t stream) {
-    const uint64_t rows = (uint64_t)p.max_q * p.heads * p.num_seqs;
-    const uint32_t joins = (uint32_t)(rows / 2 + 1 < 4096 ? rows / 2 + 1 : 4096);
-    if (p.by_slots) combine_kernel<true><<<dim3(joins), dim3(256), 0, stream>>>(p, M);
-    else combine_kernel<false><<<dim3(joins), dim3(256), 0, stream>>>(p, M);
-    return hipGetLastError();
-}
-
 }  // namespace
 
 AttendPlan plan_attend(uint64_t rows, uint64_t num_seqs, uint64_t num_tokens, uint64_t heads, uint64_t max_kv) {
@@ -1357,10 +1376,12 @@ AttendPlan plan_attend(uint64_t rows, uint64_t num_seqs, uint64_t num_tokens, ui
     }
     a.fits = units * tiles < (1ull << 31);
     // one block a CU; never more than the line has runs
-    a.blocks = (uint32_t)(runs >= 256 ? 256 : runs);
-    a.line_bytes = ((num_seqs + 1) * 4 + 255) / 256 * 256;
+    a.blocks = (uint32_t)(runs >= kMostBlocks ? kMostBlocks : runs);
+    // two rows a block of the join; no more units are cut than blocks end inside one
+    const uint64_t cut_rows = (units < a.blocks ? units : a.blocks) * a.rows;
+    a.joins = (uint32_t)(cut_rows / 2 < 4096 ? cut_rows / 2 : 4096);
     a.lse_bytes = (uint64_t)a.blocks * 2 * a.rows * 4;
-    a.bytes = a.line_bytes + a.lse_bytes + (uint64_t)a.blocks * 2 * a.rows * 512 * 4;
+    a.bytes = kCutBytes + a.lse_bytes + (uint64_t)a.blocks * 2 * a.rows * 512 * 4;
     return a;
 }
 
@@ -1369,9 +1390,10 @@ hipError_t launch_attend(const AttendParams& given, void* workspace, hipStream_t
     const AttendPlan a = plan_attend((uint64_t)p.max_q * p.heads, p.num_seqs, p.num_tokens, p.heads,
                                      p.by_slots ? p.num_slots : p.max_kv);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    p.line = reinterpret_cast<uint32_t*>(ws);
-    p.part_lse = reinterpret_cast<float*>(ws + a.line_bytes);
-    p.part = reinterpret_cast<float*>(ws + a.line_bytes + a.lse_bytes);
+    p.cut_last = reinterpret_cast<uint32_t*>(ws);
+    p.cuts = reinterpret_cast<AttendCut*>(ws + kMostBlocks * sizeof(uint32_t));
+    p.part_lse = reinterpret_cast<float*>(ws + kCutBytes);
+    p.part = reinterpret_cast<float*>(ws + kCutBytes + a.lse_bytes);
     (void)hipGetLastError();
     const dim3 grid(a.blocks), block(kThreads);
     if (a.rows == 16) {
@@ -1385,12 +1407,13 @@ hipError_t launch_attend(const AttendParams& given, void* workspace, hipStream_t
         else attend_wide_kernel<false><<<grid, block, 0, stream>>>(p);
     }
     const hipError_t e = hipGetLastError();
-    return e != hipSuccess ? e : launch_combine(p, a.rows, stream);
+    if (e != hipSuccess) return e;
+    combine_kernel<<<dim3(a.joins), dim3(256), 0, stream>>>(p, a.rows, a.blocks);
+    return hipGetLastError();
 }
 
 hipError_t launch_attend_weights(const AttendParams& given, hipStream_t stream) {
     AttendParams p = given;
-    p.line = nullptr;
     const uint64_t tiles = (uint64_t)((p.max_kv + 63) / 64) * p.num_seqs;
     (void)hipGetLastError();
     const dim3 grid((uint32_t)(tiles < 256 ? tiles : 256));

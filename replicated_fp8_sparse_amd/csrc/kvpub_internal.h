@@ -85,6 +85,14 @@ struct GatherParams {
     uint32_t offsets32;          // every offset within a layer fits in 32 bits (layer span < 2^32)
 };
 
+// The unit that a block began and later ones end: their parts are joined.
+struct AttendCut {
+    uint32_t slot;               // of this block's part; the others' are their first
+    uint32_t q0;                 // first token of the unit's sequence
+    uint32_t row0;               // the unit's first (token, head) row of the sequence
+    uint32_t rows;               // of the sequence
+};
+
 // Latent attention (attend_kernel.hip).  Strides in elements.
 struct AttendParams {
     const uint8_t* main_base;    // the replica, already offset to the layer
@@ -117,7 +125,8 @@ struct AttendParams {
     const float* weights_in;     // weights only
     float* weights_out;
     int64_t weights_stride;
-    uint32_t* line;              // workspace: prefix of each sequence's work, then the blocks' share (weights: null)
+    uint32_t* cut_last;          // workspace: [blocks] last block of the unit that this one began; 0: none was cut
+    AttendCut* cuts;             // workspace: [blocks] that unit, if it was cut
     float* part_lse;             // workspace: [blocks * 2][rows]
     float* part;                 // workspace: [blocks * 2][rows][512]
 };
@@ -126,8 +135,8 @@ struct AttendParams {
 struct AttendPlan {
     uint32_t rows;
     uint32_t blocks;
+    uint32_t joins;              // blocks of the join
     bool fits;                   // fewer than 2^31 tiles in all
-    uint64_t line_bytes;
     uint64_t lse_bytes;
     uint64_t bytes;
 };
