@@ -51,18 +51,32 @@ __device__ __forceinline__ void copy16_to_lds(const void* src, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(src) : "memory");
 }
 
-__global__ __launch_bounds__(kThreads, 2) void expanded_kernel(const ExpandedParams p, uint32_t q_tiles) {
-    __shared__ __align__(16) uint8_t ring[2 * kTile];
+// First token of sequence b (its end is the next one's), kept within the call's.
+__device__ __forceinline__ uint32_t token_of(const ExpandedParams& p, uint32_t b) {
+    const int32_t t = p.q_start[b];
+    return t < 0 ? 0u : ((uint32_t)t > p.num_tokens ? p.num_tokens : (uint32_t)t);
+}
+
+// The places of query tiles by tokens: sequence b's begin at place token_of(b) / 128 + b.
+// n tokens from there on are at most as many tiles as lie between that and the next
+// sequence's places, so num_tokens / 128 + num_seqs places hold all tiles, whatever
+// max_q_len allows.  The sequence of place v: 64 candidates at a time.
+__device__ __forceinline__ uint32_t sequence_at(const ExpandedParams& p, uint32_t v, uint32_t lane) {
+    uint32_t lo = 0, left = p.num_seqs;              // it is one of lo .. lo + left - 1
+    while (left > 1) {
+        const uint32_t step = (left + 63) / 64, b = lo + lane * step;
+        const bool before = lane * step < left && token_of(p, b) / kQueries + b <= v;
+        const uint32_t n = (uint32_t)__popcll(__ballot(before)), skip = (n ? n - 1 : 0u) * step;
+        lo += skip;
+        left = left - skip < step ? left - skip : step;
+    }
+    return __builtin_amdgcn_readfirstlane(lo);
+}
+
+// 128 queries of sequence b, head h from tile tile_q on.
+__device__ __forceinline__ void attend_tile(const ExpandedParams& p, uint32_t b, uint32_t h, uint32_t tile_q, uint8_t* ring) {
     const uint32_t lane = threadIdx.x & 63u, l16 = lane & 15u, g = lane >> 4;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    // block -> (sequence, head) by XCD, its query tiles in falling order
-    const uint32_t pairs = p.num_seqs * p.heads;
-    const uint32_t id = blockIdx.x, xcd = id % 8u, in = id / 8u;
-    const uint32_t pair = (in / q_tiles) * 8u + xcd;
-    if (pair >= pairs) return;
-    const uint32_t b = p.first_seq + pair / p.heads, h = pair % p.heads;
-    const uint32_t tile_q = p.first_tile + q_tiles - 1u - in % q_tiles;
-
     int64_t q0 = p.q_start[b], q1 = p.q_start[b + 1], k0 = p.k_start[b], k1 = p.k_start[b + 1];
     q0 = q0 < 0 ? 0 : q0;
     q1 = q1 > (int64_t)p.num_tokens ? (int64_t)p.num_tokens : q1;
@@ -263,14 +277,51 @@ __global__ __launch_bounds__(kThreads, 2) void expanded_kernel(const ExpandedPar
     }
 }
 
+// q_tiles tiles of each sequence and head: (sequence, head) by XCD, query tiles in falling order.
+__global__ __launch_bounds__(kThreads, 2) void expanded_kernel(const ExpandedParams p, uint32_t q_tiles) {
+    __shared__ __align__(16) uint8_t ring[2 * kTile];
+    const uint32_t pairs = p.num_seqs * p.heads;
+    const uint32_t id = blockIdx.x, xcd = id % 8u, in = id / 8u;
+    const uint32_t pair = (in / q_tiles) * 8u + xcd;
+    if (pair >= pairs) return;
+    attend_tile(p, p.first_seq + pair / p.heads, pair % p.heads, p.first_tile + q_tiles - 1u - in % q_tiles, ring);
+}
+
+// The places from first_tile on in falling order, heads across.
+__global__ __launch_bounds__(kThreads, 2) void expanded_places_kernel(const ExpandedParams p, uint32_t places) {
+    __shared__ __align__(16) uint8_t ring[2 * kTile];
+    const uint32_t v = p.first_tile + places - 1u - blockIdx.x / p.heads;
+    const uint32_t b = sequence_at(p, v, threadIdx.x & 63u), place = token_of(p, b) / kQueries + b;
+    if (v < place) return;                           // before the first sequence's
+    attend_tile(p, b, blockIdx.x % p.heads, v - place, ring);
+}
+
 }  // namespace
 
 hipError_t launch_expanded(const ExpandedParams& given, hipStream_t stream) {
     // a grid's threads stay below 2^32: at most 2^23 blocks a launch
     const uint32_t all = (given.max_q + kQueries - 1) / kQueries, most = (1u << 23) / 128;
+    (void)hipGetLastError();
+    // Blocks by tokens where max_q_len pads the sequences' tiles to more than twice the
+    // places that the tokens need: one prompt of 8192 tokens among 255 single ones, 16
+    // heads, 460 us, against 757 with blocks for every padded tile; one of 2048 among 63,
+    // 94 against 91 (the search); 65535 single tokens with no bound 12 ms, against 5e8
+    // padded blocks.
+    const uint32_t places = given.num_tokens / kQueries + given.num_seqs;
+    if ((uint64_t)given.num_seqs * all > 2ull * places) {
+        const uint32_t step = (1u << 23) / given.heads;
+        for (uint32_t v = 0; v < places; v += step) {
+            ExpandedParams p = given;
+            p.first_tile = v;
+            const uint32_t n = places - v < step ? places - v : step;
+            expanded_places_kernel<<<dim3(n * p.heads), dim3(kThreads), 0, stream>>>(p, n);
+            const hipError_t e = hipGetLastError();
+            if (e != hipSuccess) return e;
+        }
+        return hipSuccess;
+    }
     const uint32_t q_tiles = all < most ? all : most;
     const uint32_t seqs = (1u << 23) / (q_tiles * given.heads);          // 1 and more: 128 heads at most
-    (void)hipGetLastError();
     for (uint32_t q = 0; q < all; q += q_tiles) {
         for (uint32_t b = 0; b < given.num_seqs; b += seqs) {
             ExpandedParams p = given;
