@@ -215,17 +215,15 @@ __global__ __launch_bounds__(kMoveThreads) void move_kernel(const EvictParams p,
         if (i < keep) {
             const uint32_t at = (uint32_t)p.kept[(uint64_t)b * p.kept_stride + i];
             weight = p.weights_in[(uint64_t)b * p.weights_stride + at];
-            if (!p.same_pages || at != i) {
-                const int64_t ps = p.pages[(uint64_t)b * p.pages_stride + (at >> 6)];
-                const int64_t pd = p.dst[(uint64_t)b * p.dst_stride + (i >> 6)];
-                if (ps >= 0 && ps < pages && pd >= 0 && pd < pages) {
-                    s = (uint64_t)ps * p.main_page_stride + (at & 63u) * 656u;
-                    d = (uint64_t)pd * p.main_page_stride + (i & 63u) * 656u;
-                    my_isrc = (uint64_t)ps * p.idx_page_stride + (at & 63u) * 128u;
-                    my_idst = (uint64_t)pd * p.idx_page_stride + (i & 63u) * 128u;
-                } else {
-                    atomicAdd(p.invalid_count, 1ull);
-                }
+            const int64_t ps = p.pages[(uint64_t)b * p.pages_stride + (at >> 6)];
+            const int64_t pd = p.dst[(uint64_t)b * p.dst_stride + (i >> 6)];
+            if (ps < 0 || ps >= pages || pd < 0 || pd >= pages) {
+                atomicAdd(p.invalid_count, 1ull);
+            } else if (!p.same_pages || at != i) {   // in place, a row may stay where it is
+                s = (uint64_t)ps * p.main_page_stride + (at & 63u) * 656u;
+                d = (uint64_t)pd * p.main_page_stride + (i & 63u) * 656u;
+                my_isrc = (uint64_t)ps * p.idx_page_stride + (at & 63u) * 128u;
+                my_idst = (uint64_t)pd * p.idx_page_stride + (i & 63u) * 128u;
             }
         }
         src[tid] = s;
