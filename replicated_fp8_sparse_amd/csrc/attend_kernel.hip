@@ -639,10 +639,20 @@ __device__ __forceinline__ View view_of(const AttendParams& p, const Segment& g,
     return v;
 }
 
+// Whether some token of the sequence that is computed sees a position of tile t.
+__device__ __forceinline__ bool seen_by_some(const AttendParams& p, const Seq& s, uint32_t t, uint64_t live) {
+    const uint32_t m = s.n > p.max_q ? p.max_q : s.n;
+    for (uint32_t i = 0; i < m; i += 64) {
+        const uint32_t token = i + (threadIdx.x & 63u);
+        if (__ballot(token < m && (sees<false>(p, s, token).bits(t * 64u) & live) != 0)) return true;
+    }
+    return false;
+}
+
 // The rows of tile t that exist (bits of live) and whether some row of the unit may
-// not see it whole; such a tile is cleaned.  Bad pages and slots are counted by the
-// unit that has the sequence's last rows: no other sees more of its tiles.
-template <bool Slots, class Src>
+// not see it whole; such a tile is cleaned.  Count: bad pages and slots are counted by
+// the unit that has the sequence's last rows: no other sees more of its tiles.
+template <bool Slots, bool Count, class Src>
 __device__ __forceinline__ void inspect(const AttendParams& p, const Src& src, const Segment& g, const View& view, uint32_t t,
                                         int64_t page, uint8_t* tile, float* scales, uint64_t& live, bool& masked) {
     const uint32_t left = g.s.kv - t * 64u;
@@ -657,7 +667,8 @@ __device__ __forceinline__ void inspect(const AttendParams& p, const Src& src, c
         live = left < 64 ? (1ull << left) - 1 : ~0ull;
         masked = t * 64u + 64u > view.clear;
         if (page < 0) {                              // page 0 was copied in its place
-            if (g.unit + 1 == g.s.units && threadIdx.x == 0) atomicAdd(p.invalid_count, 1ull);
+            if (Count && g.unit + 1 == g.s.units && threadIdx.x < 64 && seen_by_some(p, g.s, t, live) && threadIdx.x == 0)
+                atomicAdd(p.invalid_count, 1ull);
             live = 0;
             masked = true;
         }
@@ -787,7 +798,7 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(const AttendParams p) 
         uint64_t live = ~0ull;
         bool masked = false;
         auto look = [&](uint32_t t, int64_t page) {
-            inspect<Slots>(p, src, seg, view, t, page, sh.ring + ring_of(t) * kTileBytes, &sh.scales[ring_of(t)][0][0], live, masked);
+            inspect<Slots, true>(p, src, seg, view, t, page, sh.ring + ring_of(t) * kTileBytes, &sh.scales[ring_of(t)][0][0], live, masked);
         };
         if (t0 < t_end) {
             wait_own(wave, t0 + 1 < t_end);
@@ -966,7 +977,7 @@ __global__ __launch_bounds__(kThreads) void attend_wide_kernel(const AttendParam
         bool masked = false;
 
         auto look = [&](uint32_t t, int64_t page) {
-            inspect<Slots>(p, src, seg, view, t, page, sh.ring + ring_of(t) * kTileBytes, &sh.scales[ring_of(t)][0][0], live, masked);
+            inspect<Slots, true>(p, src, seg, view, t, page, sh.ring + ring_of(t) * kTileBytes, &sh.scales[ring_of(t)][0][0], live, masked);
         };
         auto scores = [&](uint32_t t, f32x4 (*to)[1]) {
             const uint8_t* rows32 = sh.ring + ring_of(t) * kTileBytes + kh * 32 * kRow;
@@ -1268,7 +1279,6 @@ __global__ __launch_bounds__(kThreads) void weights_kernel(const AttendParams p)
         const Source<false> src{p, p.pages + (uint64_t)seg.b * p.pages_stride, nullptr, s.kv, capacity, sh.ring, sh.scales, nullptr, wave, lane};
 
         for (uint32_t row0 = 0; row0 < rows && t0 < end; row0 += 128) {
-            seg.unit = row0;                                 // bad pages are counted in the first pass
             QFrag<4, 2> q[2];
             uint32_t token[2];
             float lse2[2];
@@ -1301,7 +1311,7 @@ __global__ __launch_bounds__(kThreads) void weights_kernel(const AttendParams p)
                 float* scales = &sh.scales[ring_of(t)][0][0];
                 uint64_t live;
                 bool masked;
-                inspect<false>(p, src, seg, view, t, pg[0], tile, scales, live, masked);
+                inspect<false, false>(p, src, seg, view, t, pg[0], tile, scales, live, masked);
                 src.turn(t + 1, end, pg);
                 f32x4 x[2][2];
                 const uint8_t* rows32 = tile + kh * 32 * kRow;
@@ -1334,7 +1344,16 @@ __global__ __launch_bounds__(kThreads) void weights_kernel(const AttendParams p)
                 }
             }
         }
+        // the tiles' bad pages are counted here, where no operands are held
+        const bool mine = wave == 0 && lane < end - t0;
+        const int32_t page = mine ? src.table[t0 + lane] : 0;
         __syncthreads();
+        uint64_t bad = __ballot(mine && (page < 0 || page >= capacity / 64));
+        while (bad) {
+            const uint32_t t = t0 + (uint32_t)__builtin_ctzll(bad), left = s.kv - t * 64u;
+            bad &= bad - 1;
+            if (seen_by_some(p, s, t, left < 64 ? (1ull << left) - 1 : ~0ull) && lane == 0) atomicAdd(p.invalid_count, 1ull);
+        }
         for (uint32_t k = threadIdx.x; k < (t1 - t0) * 64u; k += kThreads) {
             const uint32_t pos = t0 * 64u + k;
             if (pos >= p.max_kv) break;
