@@ -90,13 +90,18 @@ __device__ __forceinline__ uint32_t lds_offset(const void* p) {
 
 // 64 lanes x 16 bytes from each lane's address to 1024 consecutive LDS bytes.
 // Written as asm because the compiler otherwise waits for every outstanding copy
-// before any LDS read; wait_tile() below counts them instead.
+// before any LDS read; wait_own() below counts them instead.
+// (m0 is a reserved register, which the compiler warns of: it holds no value of its own
+// there, but may set it once for several uses.)
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void copy16_to_lds(const uint8_t* src, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(src) : "memory");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(src) : "memory", "m0");
 }
 __device__ __forceinline__ void copy4_to_lds(const uint8_t* src, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(lds), "v"(src) : "memory");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(lds), "v"(src) : "memory", "m0");
 }
+#pragma clang diagnostic pop
 
 // This wave's own copies of all but the newest tile have landed.  A tile is 41
 // copies of rows, wave, wave + 8, ..., and one of each tile's scales by waves

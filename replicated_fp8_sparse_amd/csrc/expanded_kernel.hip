@@ -47,9 +47,14 @@ constexpr float kLazy = 8.0f;
 __device__ __forceinline__ uint32_t lds_offset(const void* p) {
     return (uint32_t)(uintptr_t)(lptr<const uint8_t>)(const uint8_t*)p;
 }
+// (m0 is a reserved register, which the compiler warns of: it holds no value of its own
+// there, but may set it once for several uses.)
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void copy16_to_lds(const void* src, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(src) : "memory");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(src) : "memory", "m0");
 }
+#pragma clang diagnostic pop
 
 // First token of sequence b (its end is the next one's), kept within the call's.
 __device__ __forceinline__ uint32_t token_of(const ExpandedParams& p, uint32_t b) {
