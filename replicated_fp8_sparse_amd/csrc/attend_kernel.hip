@@ -11,7 +11,9 @@
 // the accumulator.  (The scaled e4m3 instruction would take the codes as they
 // are and each query as the sum of two e4m3 numbers at the same rate; its sums
 // were found off by 2^-16 of the largest product, too much for lse.)  The
-// weights are rounded to bf16 for the second product.
+// weights are rounded to bf16 for the second product: a second operand for their
+// low part would double its matrix instructions, and outputs are off by 0.0022 of
+// their norm where their own rounding alone leaves 0.0017.
 //
 // Mapping.  A block of 8 waves takes a unit (sequence, M rows = (token, head)
 // pairs) over a run of 64-row tiles (a page), a tile being one copy of 41984
@@ -30,7 +32,7 @@
 // Bound.  The matrix units need 2200 cycles for a tile of 64 rows, its widening to
 // bf16 (4 instructions for 8 codes) and softmax about 2000 on the vector unit, LDS
 // 2500; with one barrier a tile and two waves a SIMD they overlap by half: 6300
-// cycles a tile.  64 sequences of up to 8192 positions, 128 heads: 170 us in all
+// cycles a tile.  64 sequences of up to 8192 positions, 128 heads: 160-180 us in all
 // (61 at the rate of a large bf16 matrix product, 430 TFLOP/s reached).
 //
 // Work split.  All units' tiles form one line that the blocks cut into equal
@@ -423,7 +425,8 @@ struct Line {
 
 // Runs that keep to one sequence, for up to 64 sequences: the shortest length with
 // which they are no more than the blocks.  A block that would take the end of one
-// sequence and the start of another pays a start twice, and all wait for it.
+// sequence and the start of another pays a start twice, and all wait for it.  (64 lanes:
+// 64 sequences of 4096 positions, 128 heads, 65 us; 65 of them, on one line, 80.)
 struct Runs {
     const AttendParams& p;
     uint32_t b, t0, t1;
@@ -644,22 +647,35 @@ __device__ __forceinline__ View view_of(const AttendParams& p, const Segment& g,
     return v;
 }
 
-// Whether some token of the sequence that is computed sees a position of tile t.
-__device__ __forceinline__ bool seen_by_some(const AttendParams& p, const Seq& s, uint32_t t, uint64_t live) {
-    const uint32_t m = s.n > p.max_q ? p.max_q : s.n;
-    for (uint32_t i = 0; i < m; i += 64) {
-        const uint32_t token = i + (threadIdx.x & 63u);
-        if (__ballot(token < m && (sees<false>(p, s, token).bits(t * 64u) & live) != 0)) return true;
+// Counts the bad pages among tiles t0 .. t_end - 1 of which some token of the sequence
+// that is computed sees a position.  By one wave, where inspect() met any: behind the
+// loop over the tiles (in it, its scalars cost the loop 3 %).
+__device__ __forceinline__ void count_bad_pages(const AttendParams& p, const Seq& s, const int32_t* table, int64_t capacity,
+                                                uint32_t t0, uint32_t t_end) {
+    const uint32_t lane = threadIdx.x & 63u, m = s.n > p.max_q ? p.max_q : s.n;
+    uint32_t n = 0;
+    for (uint32_t from = t0; from < t_end; from += 64) {
+        const int64_t page = from + lane < t_end ? table[from + lane] : 0;
+        uint64_t bad = __ballot(page < 0 || page >= capacity / 64);
+        while (bad) {
+            const uint32_t t = from + (uint32_t)__builtin_ctzll(bad), left = s.kv - t * 64u;
+            const uint64_t live = left < 64 ? (1ull << left) - 1 : ~0ull;
+            bad &= bad - 1;
+            bool seen = false;
+            for (uint32_t i = 0; i < m && !seen; i += 64)
+                seen = __ballot(i + lane < m && (sees<false>(p, s, i + lane).bits(t * 64u) & live) != 0) != 0;
+            n += seen;
+        }
     }
-    return false;
+    if (n && lane == 0) atomicAdd(p.invalid_count, (unsigned long long)n);
 }
 
 // The rows of tile t that exist (bits of live) and whether some row of the unit may
-// not see it whole; such a tile is cleaned.  Count: bad pages and slots are counted by
-// the unit that has the sequence's last rows: no other sees more of its tiles.
-template <bool Slots, bool Count, class Src>
+// not see it whole; such a tile is cleaned.  Bad slots are counted by the unit that has
+// the token's last rows; `bad` is raised for a bad page.
+template <bool Slots, class Src>
 __device__ __forceinline__ void inspect(const AttendParams& p, const Src& src, const Segment& g, const View& view, uint32_t t,
-                                        int64_t page, uint8_t* tile, float* scales, uint64_t& live, bool& masked) {
+                                        int64_t page, uint8_t* tile, float* scales, uint64_t& live, bool& masked, bool& bad) {
     const uint32_t left = g.s.kv - t * 64u;
     if (Slots) {
         const int64_t v = src.slots[t % kSlotRing][src.lane];
@@ -672,8 +688,7 @@ __device__ __forceinline__ void inspect(const AttendParams& p, const Src& src, c
         live = left < 64 ? (1ull << left) - 1 : ~0ull;
         masked = t * 64u + 64u > view.clear;
         if (page < 0) {                              // page 0 was copied in its place
-            if (Count && g.unit + 1 == g.s.units && threadIdx.x < 64 && seen_by_some(p, g.s, t, live) && threadIdx.x == 0)
-                atomicAdd(p.invalid_count, 1ull);
+            bad = true;
             live = 0;
             masked = true;
         }
@@ -801,9 +816,9 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(const AttendParams p) 
         // and that the last one is done with.
         f32x4 x[2][1];
         uint64_t live = ~0ull;
-        bool masked = false;
+        bool masked = false, bad = false;
         auto look = [&](uint32_t t, int64_t page) {
-            inspect<Slots, true>(p, src, seg, view, t, page, sh.ring + ring_of(t) * kTileBytes, &sh.scales[ring_of(t)][0][0], live, masked);
+            inspect<Slots>(p, src, seg, view, t, page, sh.ring + ring_of(t) * kTileBytes, &sh.scales[ring_of(t)][0][0], live, masked, bad);
         };
         if (t0 < t_end) {
             wait_own(wave, t0 + 1 < t_end);
@@ -911,6 +926,7 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(const AttendParams p) 
             if (mine < rows) write_row<M, NB>(p, seg, rw * 16u + l16, tw * NB * 16, o, mx, sum, g);
         }
         line.leave(seg, rows);
+        if (!Slots && bad && wave == 0 && seg.unit + 1 == s.units) count_bad_pages(p, s, src.table, capacity, t0, t_end);
         barrier();    // before the ring takes the next unit's tiles
     }
 }
@@ -921,7 +937,8 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(const AttendParams p) 
 // The next tile's scores are formed beside this tile's values; one barrier a tile.
 // Against 4 waves of twice the rows (200 us), tiles widened once into LDS (217 us) and
 // two barriers a tile (214 us) at 64 sequences of up to 8192 positions and 128 heads:
-// 170 us; 16 drafted trees of 64 tokens, 32 heads, 8192 positions: 270 us (620 TFLOP/s).
+// 170 us; 16 drafted trees of 64 tokens, 32 heads, 8192 positions: 237-340 us (490-700
+// TFLOP/s).  512 lists of 2048 slots, 128 heads: 521 us (units of 32 rows 738).
 // The maximum the weights refer to is held by all waves alike: a row that outgrows
 // it raises a flag, and all waves then agree on new ones before the weights are used.
 struct WideShared {
@@ -979,10 +996,10 @@ __global__ __launch_bounds__(kThreads) void attend_wide_kernel(const AttendParam
         float sum = 0.f, fresh_sum = 0.f;
         f32x4 x[2][1];                                   // scores of the tile whose weights are given
         uint64_t live = ~0ull;
-        bool masked = false;
+        bool masked = false, bad = false;
 
         auto look = [&](uint32_t t, int64_t page) {
-            inspect<Slots, true>(p, src, seg, view, t, page, sh.ring + ring_of(t) * kTileBytes, &sh.scales[ring_of(t)][0][0], live, masked);
+            inspect<Slots>(p, src, seg, view, t, page, sh.ring + ring_of(t) * kTileBytes, &sh.scales[ring_of(t)][0][0], live, masked, bad);
         };
         auto scores = [&](uint32_t t, f32x4 (*to)[1]) {
             const uint8_t* rows32 = sh.ring + ring_of(t) * kTileBytes + kh * 32 * kRow;
@@ -1128,6 +1145,7 @@ __global__ __launch_bounds__(kThreads) void attend_wide_kernel(const AttendParam
             if (row0 + at < rows) write_row<M, 8>(p, seg, at, j * 128, o[r], mo[r], total, g);
         }
         line.leave(seg, rows);
+        if (!Slots && bad && wave == 0 && seg.unit + 1 == s.units) count_bad_pages(p, s, src.table, capacity, t0, t_end);
         barrier();    // before the ring and the sums serve the next unit
     }
 }
@@ -1136,7 +1154,9 @@ __global__ __launch_bounds__(kThreads) void attend_wide_kernel(const AttendParam
 // 128 threads takes one (token, head) row, 4 columns a thread, and adds the blocks'
 // parts in order, four on their way together (one at a time: 2.5 us more for 6
 // parts).  Each wave counts the cut units for itself, by ballots over the blocks'
-// notes: a grid with blocks for units that are not there costs 4 us more.
+// notes: a grid with blocks for units that are not there costs 4 us more (slots 16 x
+// 2048).  4 us for 256 rows of 4 parts, a chain of three reads from memory; 12 us for
+// 8192 rows of 1 to 3 parts.
 __global__ __launch_bounds__(256) void combine_kernel(const AttendParams p, uint32_t M, uint32_t blocks) {
     const uint32_t lane = threadIdx.x & 63u, col = (threadIdx.x & 127u) * 4u;
     uint32_t last[4];
@@ -1217,7 +1237,7 @@ __global__ __launch_bounds__(256) void combine_kernel(const AttendParams p, uint
 // by wave, always in that order.  A wave has 32 rows, so that a widened operand (4
 // vector instructions) serves two matrix instructions: with 16 rows 87 us, with 32
 // 69 us for 16 sequences of up to 16384 positions and 128 heads; one line instead of
-// equal runs of each sequence's bound 53 us, runs that keep to one sequence 39-47 us
+// equal runs of each sequence's bound 53 us, runs that keep to one sequence 39-48 us
 // (92 MB: 18 us at a copy's rate; 28 us with the scores left out).  Bound by the vector
 // unit: 6000 cycles a tile of 128 rows, of which the matrix units need 2300.
 constexpr uint32_t kWeightTiles = 16;
@@ -1281,6 +1301,7 @@ __global__ __launch_bounds__(kThreads) void weights_kernel(const AttendParams p)
         View view;                                           // every token sees the positions below `clear`
         view.clear = base < 0 ? 0u : (uint32_t)(p.tree ? base : base + 1);
         view.t_end = end;
+        bool bad = false;
         const Source<false> src{p, p.pages + (uint64_t)seg.b * p.pages_stride, nullptr, s.kv, capacity, sh.ring, sh.scales, nullptr, wave, lane};
 
         for (uint32_t row0 = 0; row0 < rows && t0 < end; row0 += 128) {
@@ -1316,7 +1337,7 @@ __global__ __launch_bounds__(kThreads) void weights_kernel(const AttendParams p)
                 float* scales = &sh.scales[ring_of(t)][0][0];
                 uint64_t live;
                 bool masked;
-                inspect<false, false>(p, src, seg, view, t, pg[0], tile, scales, live, masked);
+                inspect<false>(p, src, seg, view, t, pg[0], tile, scales, live, masked, bad);
                 src.turn(t + 1, end, pg);
                 f32x4 x[2][2];
                 const uint8_t* rows32 = tile + kh * 32 * kRow;
@@ -1349,16 +1370,8 @@ __global__ __launch_bounds__(kThreads) void weights_kernel(const AttendParams p)
                 }
             }
         }
-        // the tiles' bad pages are counted here, where no operands are held
-        const bool mine = wave == 0 && lane < end - t0;
-        const int32_t page = mine ? src.table[t0 + lane] : 0;
         __syncthreads();
-        uint64_t bad = __ballot(mine && (page < 0 || page >= capacity / 64));
-        while (bad) {
-            const uint32_t t = t0 + (uint32_t)__builtin_ctzll(bad), left = s.kv - t * 64u;
-            bad &= bad - 1;
-            if (seen_by_some(p, s, t, left < 64 ? (1ull << left) - 1 : ~0ull) && lane == 0) atomicAdd(p.invalid_count, 1ull);
-        }
+        if (bad && wave == 0) count_bad_pages(p, s, src.table, capacity, t0, end);
         for (uint32_t k = threadIdx.x; k < (t1 - t0) * 64u; k += kThreads) {
             const uint32_t pos = t0 * 64u + k;
             if (pos >= p.max_kv) break;
@@ -1384,7 +1397,8 @@ AttendPlan plan_attend(uint64_t rows, uint64_t num_seqs, uint64_t num_tokens, ui
     };
     // Rows of a unit.  64 (attend_wide_kernel) from ten tiles a block on: its tile of 64
     // rows takes 3.1 us, two of 32 rows 4.2 us, but it starts 8 us later (16 sequences
-    // of 128 heads, 4096 positions: 56.4 us against 54.9; 8192: 81.3 against 88.6).
+    // of 128 heads, 4096 positions: 56.4 us against 54.9; 8192: 81.3 against 88.6; lists of
+    // 2048 slots for 40 tokens: 80 against 76; 64 tokens: 83 against 88; 128: 123 against 167).
     // 16 where that holds all rows, or where a line of longer units would leave CUs idle
     // (4 tokens of 64 heads, 256 slots: 15.4 us against 23 with units of 64 rows).  A run
     // may be one tile: 12.4 us then, against 14.7 with two at least.
