@@ -19,8 +19,10 @@
 // of the second product with its keys in that order.  The causal limit cuts a
 // block's tiles; blocks with the most tiles start first, and blocks of one head
 // go to one XCD (its L2 holds the head's keys).  Bound by the matrix units: 2 x 4096
-// queries over 8192 keys, 16 heads, 427 us, 830 TFLOP/s, 69 % of a large bf16 matrix
+// queries over 8192 keys, 16 heads, 427-431 us, 830 TFLOP/s, 69 % of a large bf16 matrix
 // product, with the exponentials and sums between the products; 100 queries 10 us.
+// The weights are rounded to bf16 as an operand of the second product: a second operand
+// for their low part would double it, for less than the output's rounding takes away.
 #include "kvpub_internal.h"
 
 namespace kvpub {
