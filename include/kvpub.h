@@ -447,6 +447,206 @@ typedef struct {
 
 KVPUB_API kvpub_status kvpub_attend_expanded(kvpub_ctx *ctx, const kvpub_expanded_io *io, kvpub_stream_t stream);
 
+/* ---- Rotary positions --------------------------------------------------------
+ *
+ * A rotation turns pairs of a row's values by angles that go by the token's
+ * position: pair i by a = 2 pi frac(position * turns[i] / 2^64),
+ *   y1 = magnitude * (x1 cos a - x2 sin a),  y2 = magnitude * (x1 sin a + x2 cos a).
+ * The frequencies are a table of turns a position in units of 2^-64, so that an
+ * angle is one 64-bit product whatever the position: far ones lose nothing.
+ * Angles are held to 2^-33 of a turn, sines, cosines and products in binary32.
+ * Positions are int32 and may be negative (they turn back). */
+#define KVPUB_ROTATE_PAIRS 0u   /* pair i: values start + 2i and start + 2i + 1 */
+#define KVPUB_ROTATE_HALVES 1u  /* pair i: values start + i and start + dim/2 + i */
+
+typedef struct {
+    const uint64_t *turns;            /* device, [dim / 2], 8-byte aligned */
+    uint32_t dim;                     /* rotated values of a row: a multiple of 8, at least 8 */
+    uint32_t start;                   /* the first of them: a multiple of 8; start + dim at most the row's width */
+    uint32_t layout;                  /* KVPUB_ROTATE_* */
+    float magnitude;                  /* of the rotated values; finite, 1 where a scaling asks for nothing else */
+} kvpub_rotation;
+
+/* How a model's frequencies f_i = base^(-2i/dim) (radians a position) are
+ * stretched for contexts longer than those it was trained on:
+ *   NONE    f_i
+ *   LINEAR  f_i / factor
+ *   GROWN   f_i of the base grown to base * factor^(dim / (dim - 2))
+ *   RAMP    f_i k_i + f_i / factor * (1 - k_i), k_i = 1 - clamp((i - lo) / (hi - lo), 0, 1)
+ *           with lo = max(0, floor(d(high))), hi = min(dim - 1, ceil(d(low))) (hi - lo at least 0.001),
+ *           d(t) = dim * ln(original / (2 pi t)) / (2 ln base): by the pair's index between those
+ *           that turn `high` and `low` times over the original length
+ *   BLEND   the same with k_i = clamp((original * f_i / (2 pi) - low) / (high - low), 0, 1): by the turns */
+#define KVPUB_SCALING_NONE 0u
+#define KVPUB_SCALING_LINEAR 1u
+#define KVPUB_SCALING_GROWN 2u
+#define KVPUB_SCALING_RAMP 3u
+#define KVPUB_SCALING_BLEND 4u
+
+typedef struct {
+    uint32_t dim;                     /* a multiple of 8, 8..1024 */
+    uint32_t scaling;                 /* KVPUB_SCALING_* */
+    double base;                      /* finite, > 1 */
+    double factor;                    /* finite, >= 1 (not read by NONE) */
+    double original;                  /* positions of the original context, >= 1 (RAMP, BLEND) */
+    double low;                       /* turns over it, 0 < low < high, finite (RAMP, BLEND) */
+    double high;
+} kvpub_rotation_config;
+
+/* Fill turns[0 .. dim/2 - 1], a host array, for the caller to copy to the
+ * device once.  Host arithmetic only: needs no device. */
+KVPUB_API kvpub_status kvpub_rotation_turns(const kvpub_rotation_config *config, uint64_t *turns);
+
+/* Element types of the calls below. */
+#define KVPUB_BF16 0u
+#define KVPUB_FP16 1u
+#define KVPUB_FP32 2u
+
+/* Rows of heads rotated by their tokens' positions: y = the rotation of x, the
+ * values outside [start, start + dim) copied.  y == x with equal strides rotates in
+ * place (only the rotated values are touched); otherwise the two do not overlap.
+ * transpose: by the negative angles (times the same magnitude), which takes the
+ * gradient of y to the gradient of x.  Rounded once, to the element type.
+ * Element (t, h, k) is at t*token_stride + h*head_stride + k; pointers 16-byte
+ * aligned, strides multiples of 8 elements, at most 2^31 - 1, head strides at
+ * least head_dim (any value if num_heads is 1); x's token stride may be 0.
+ * A value that is not finite reaches its own pair only. */
+typedef struct {
+    const void *x;                    /* [T, H, head_dim] */
+    void *y;                          /* [T, H, head_dim] */
+    int64_t x_token_stride, x_head_stride;
+    int64_t y_token_stride, y_head_stride;
+    const int32_t *positions;         /* [T], 4-byte aligned */
+    kvpub_rotation rotation;
+    int64_t num_tokens;               /* 0..2^24 */
+    uint32_t num_heads;               /* 1..1024 */
+    uint32_t head_dim;                /* a multiple of 8, 8..1024 */
+    uint32_t type;                    /* KVPUB_BF16, KVPUB_FP16 or KVPUB_FP32 */
+    uint32_t transpose;               /* 0 or 1 */
+} kvpub_rotate_io;
+
+/* Asynchronously on `stream`; no allocation, no synchronization, safe under
+ * stream capture.  The context gives the device only. */
+KVPUB_API kvpub_status kvpub_rotate(kvpub_ctx *ctx, const kvpub_rotate_io *io, kvpub_stream_t stream);
+
+/* kvpub_store with the rotation applied on the way: token t's RoPE row and its
+ * Indexer-K row are rotated by positions[t] before they are stored (a NULL
+ * rotation leaves that row as it is; both NULL is kvpub_store, and `positions`
+ * is not read).  The RoPE values are rounded to bf16 once; the Indexer-K values are
+ * not rounded before their scale and codes: scale = RN32(amax / 448), code =
+ * e4m3fn(RN32(x / scale)) of the rotated binary32 values.  Everything else,
+ * arguments and slots included, is as for kvpub_store. */
+KVPUB_API kvpub_status kvpub_store_rotated(kvpub_ctx *ctx, uint32_t layer, int64_t num_tokens,
+                                           const void *latent, int64_t latent_row_stride,
+                                           const void *rope, int64_t rope_row_stride,
+                                           const void *indexer, int64_t indexer_row_stride,
+                                           const int64_t *slot_mapping, const int32_t *positions,
+                                           const kvpub_rotation *rope_rotation,
+                                           const kvpub_rotation *indexer_rotation, kvpub_stream_t stream);
+
+/* ---- A cache of key and value heads ------------------------------------------
+ *
+ * For attention that keeps keys and values of several heads instead of one
+ * latent vector: a replicated paged cache of e4m3 codes with one scale for each
+ * block of 64 tokens (a page) and head, keys and values apart.
+ * A page of one layer, G heads of D values, at
+ * replica + layer*layer_stride + page*page_stride:
+ *   head g at g*128*D:  [64][D] codes of the keys, then [64][D] codes of the values
+ *   behind all heads, at G*128*D + 2*g: the scale byte of the keys, then of the values
+ * A byte b stands for 2^(b - 127), b taken as 1..245.  A stored value is code * scale.
+ * A power of two costs a floating code no precision, and lets a block that is
+ * partly filled take a larger scale later without rounding its codes again
+ * (but for those that become subnormal).
+ *
+ * The context gives the device, the fail-closed state of its fences and the
+ * counter of bad pages; the descriptor names the memory, which is the caller's. */
+#define KVPUB_HEADS_PAGE_BYTES(num_kv_heads, head_dim) \
+    (((uint64_t)(num_kv_heads) * (128u * (uint64_t)(head_dim) + 2u) + 15u) / 16u * 16u)
+
+typedef struct {
+    void *bases[KVPUB_MAX_REPLICAS];  /* device, 16-byte aligned; num_replicas of them are read */
+    uint64_t num_pages;               /* pages of a layer, 1..2^31 - 1 */
+    uint64_t page_stride;             /* bytes, >= KVPUB_HEADS_PAGE_BYTES, multiple of 16 */
+    uint64_t layer_stride;            /* bytes, >= num_pages*page_stride, multiple of 16 (one layer: not read) */
+    uint32_t num_replicas;            /* 1..8 */
+    uint32_t num_layers;              /* >= 1 */
+    uint32_t num_kv_heads;            /* G, 1..128 */
+    uint32_t head_dim;                /* D: 64, 128 or 256 */
+} kvpub_heads;
+
+/* New keys and values.  Element (t, g, k) is at t*token_stride + g*head_stride + k;
+ * alignment and strides as for kvpub_rotate_io's x. */
+typedef struct {
+    const void *k;                    /* [T, G, D] */
+    const void *v;                    /* [T, G, D] */
+    int64_t k_token_stride, k_head_stride;
+    int64_t v_token_stride, v_head_stride;
+    int64_t num_tokens;               /* T, 0..2^24 */
+    uint32_t type;                    /* KVPUB_BF16 or KVPUB_FP16 */
+    uint32_t reserved;                /* must be 0 */
+} kvpub_heads_rows;
+
+/* Append: token i of sequence b's n (q_start as in kvpub_pages) becomes its
+ * position p = kv_len[b] - n + i, in every replica; kv_len counts the new tokens.
+ * The key is rotated first, by positions[t], or by p if positions is NULL; a NULL
+ * rotation leaves keys as they are (positions is not read).  Rotated values are
+ * not rounded before their codes.
+ * A block's scale is the least 2^e, -126 <= e <= 118, with every finite |x| of its
+ * new tokens at most 448 * 2^e, and, if it holds older positions of the sequence,
+ * at least the scale it had (replica 0's): those are brought to the new scale,
+ * code = e4m3fn(old value / scale).  Magnitudes beyond 448 scales (infinities
+ * among them) become +-448, a NaN becomes a NaN code.
+ * Rows of the pages that hold neither older positions nor new ones keep their
+ * bytes, and so do the older ones if the scale stays.  A page that gets rows belongs
+ * to one sequence of the call (a shared prefix ends on a page's end).  tree_mask
+ * is not read; tokens beyond the first max_q_len of a sequence, negative
+ * positions, and tokens that belong to no sequence are not stored.  A page
+ * number outside the cache's pages drops its rows, and is counted once a call.
+ * A context poisoned by a fence timeout stores nothing.  Asynchronous on
+ * `stream`; no allocation, no synchronization, safe under stream capture. */
+KVPUB_API kvpub_status kvpub_heads_append(kvpub_ctx *ctx, const kvpub_heads *cache, uint32_t layer,
+                                          const kvpub_heads_rows *rows, const kvpub_pages *pages,
+                                          const kvpub_rotation *rotation, const int32_t *positions,
+                                          kvpub_stream_t stream);
+
+/* Queries of H heads over the cache's G: head h reads key-value head h / (H/G). */
+typedef struct {
+    const void *q;                    /* [T, H, D] */
+    void *out;                        /* [T, H, D], of q's type */
+    float *lse;                       /* [T, H] at t*lse_token_stride + h, or NULL; 4-byte aligned */
+    int64_t q_token_stride, q_head_stride;
+    int64_t out_token_stride, out_head_stride;
+    int64_t lse_token_stride;
+    int64_t num_tokens;               /* T, 0..2^24 */
+    uint32_t num_heads;               /* H: a multiple of G, at most 128 * G and 1024 */
+    uint32_t type;                    /* KVPUB_BF16 or KVPUB_FP16 */
+    float scale;                      /* finite; the softmax scale */
+    uint32_t reserved;                /* must be 0 */
+} kvpub_heads_queries;
+
+/* Bytes of workspace that kvpub_heads_attend takes for such a call (0 if a
+ * descriptor is not valid).  It depends on num_kv_heads, head_dim, num_heads,
+ * num_tokens, num_seqs, max_q_len and max_kv_len alone and grows with each; rules as
+ * for kvpub_attend_workspace. */
+KVPUB_API uint64_t kvpub_heads_attend_workspace(const kvpub_heads *cache, const kvpub_heads_queries *q,
+                                                const kvpub_pages *pages);
+
+/* Attention over the sequences' cached positions in replica `replica`, layer `layer`:
+ *   s(t,h,p) = scale * (q[t,h] . k[p,g]),  lse[t,h] = ln sum_p exp(s(t,h,p)),
+ *   out[t,h] = sum_p exp(s(t,h,p) - lse[t,h]) v[p,g],  g = h / (H/G)
+ * over the positions that t sees (kvpub_pages: causal, or a drafted tree).
+ * What is said of kvpub_attend holds here: a query that sees nothing gives 0
+ * and -inf, what it does not see has no effect whatever its bytes hold, bad pages
+ * hide their positions and are counted, tokens of no sequence keep their output,
+ * the same call gives the same bits.  Scores, maxima and sums are binary32;
+ * weights are rounded to bf16 for the second product (FP16: to the sum of two
+ * bf16), out once to its type.  A query or a seen row that is not finite leaves
+ * the rows it reaches unspecified, NaN as a rule.
+ * T == 0 or num_seqs == 0 launches nothing. */
+KVPUB_API kvpub_status kvpub_heads_attend(kvpub_ctx *ctx, const kvpub_heads *cache, uint32_t replica, uint32_t layer,
+                                          const kvpub_heads_queries *q, const kvpub_pages *pages, void *workspace,
+                                          uint64_t workspace_bytes, kvpub_stream_t stream);
+
 /* Replica storage at stable virtual addresses, on cfg->device (vLLM PR
  * #52863, Relationship to existing work: the replicated cache builds on a
  * cache kept at a stable virtual address so that it can grow in place).

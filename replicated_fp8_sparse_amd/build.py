@@ -11,7 +11,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libkvpub.so")
 SOURCES = ["kvpub_api.hip", "store_kernel.hip", "fence_kernel.hip", "gather_kernel.hip", "attend_kernel.hip",
-           "evict_kernel.hip", "expanded_kernel.hip",
+           "evict_kernel.hip", "expanded_kernel.hip", "rotate_kernel.hip", "store_rotated_kernel.hip",
+           "heads_append_kernel.hip", "heads_attend_kernel.hip",
            "vmm.hip"]
 FLOOR_LIB = os.path.join(PKG, "libkvpub_floor.so")
 FLOOR_SOURCES = ["floor_kernel.hip"]

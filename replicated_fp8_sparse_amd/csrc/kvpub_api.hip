@@ -355,6 +355,70 @@ kvpub::AttendPlan slot_plan(const kvpub_queries* q, uint32_t num_slots) {
     return kvpub::plan_attend(q->num_heads, q->num_tokens, q->num_tokens, q->num_heads, num_slots);
 }
 
+// ---- rotations and the cache of heads: argument checks ------------------------
+
+bool good_rotation(const kvpub_rotation* r, uint32_t width) {
+    return r->turns && aligned(r->turns, 8) && r->dim >= 8 && r->dim % 8 == 0 && r->start % 8 == 0 &&
+           (uint64_t)r->start + r->dim <= width && r->layout <= KVPUB_ROTATE_HALVES && std::isfinite(r->magnitude);
+}
+
+kvpub::RotationParams rotation_params(const kvpub_rotation* r) {
+    if (!r) return kvpub::RotationParams{nullptr, 0, 0, 0, 0.f};
+    return kvpub::RotationParams{r->turns, r->dim, r->start, r->layout == KVPUB_ROTATE_HALVES ? 1u : 0u, r->magnitude};
+}
+
+bool good_heads(const kvpub_heads* c) {
+    if (!c || c->num_replicas < 1 || c->num_replicas > KVPUB_MAX_REPLICAS || c->num_layers < 1) return false;
+    if (c->num_kv_heads < 1 || c->num_kv_heads > 128) return false;
+    if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return false;
+    if (c->num_pages < 1 || c->num_pages > INT32_MAX) return false;
+    if (c->page_stride < KVPUB_HEADS_PAGE_BYTES(c->num_kv_heads, c->head_dim) || c->page_stride % 16) return false;
+    if (c->num_layers > 1 && (c->layer_stride % 16 || c->layer_stride / c->page_stride < c->num_pages)) return false;
+    for (uint32_t r = 0; r < c->num_replicas; ++r)
+        if (!c->bases[r] || !aligned(c->bases[r], 16)) return false;
+    return true;
+}
+
+uint8_t* heads_layer(const kvpub_heads* c, uint32_t replica, uint32_t layer) {
+    return static_cast<uint8_t*>(c->bases[replica]) + (layer ? (uint64_t)layer * c->layer_stride : 0);
+}
+
+kvpub::HeadsParams heads_params(const kvpub_heads* c) {
+    return kvpub::HeadsParams{c->page_stride, (int64_t)c->num_pages, c->num_kv_heads, c->head_dim};
+}
+
+// The sequences of a call with these tokens.
+kvpub_status check_seqs(const kvpub_pages* g, int64_t tokens) {
+    kvpub_queries q;
+    std::memset(&q, 0, sizeof q);
+    q.num_tokens = tokens;
+    return check_pages(&q, g);
+}
+
+kvpub::SeqParams seq_params(const kvpub_pages* g, int64_t tokens) {
+    kvpub::SeqParams s;
+    s.kv_len = g->kv_len;
+    s.q_start = g->q_start;
+    s.pages = g->page_table;
+    s.pages_stride = g->page_table_stride;
+    s.num_seqs = g->num_seqs;
+    s.num_tokens = (uint32_t)tokens;
+    s.max_q = (uint32_t)std::min<int64_t>(g->q_start ? g->max_q_len : 1, tokens);
+    s.max_kv = g->max_kv_len;
+    return s;
+}
+
+bool good_heads_queries(const kvpub_heads* c, const kvpub_heads_queries* q) {
+    return q && q->num_tokens >= 0 && q->num_tokens <= kMaxQueryTokens && q->num_heads >= 1 && q->num_heads <= 1024 &&
+           q->num_heads % c->num_kv_heads == 0 && q->num_heads / c->num_kv_heads <= 128 && q->type <= KVPUB_FP16 && q->reserved == 0 &&
+           std::isfinite(q->scale) && std::isfinite(q->scale * 1.44269504f);
+}
+
+kvpub::HeadsAttendPlan heads_plan(const kvpub_heads* c, const kvpub_heads_queries* q, const kvpub_pages* g) {
+    const kvpub::SeqParams s = seq_params(g, q->num_tokens);
+    return kvpub::plan_heads_attend(heads_params(c), q->num_heads / c->num_kv_heads, s.num_seqs, s.num_tokens, s.max_q, s.max_kv);
+}
+
 }  // namespace
 
 static __device__ __align__(256) uint8_t scratch[kStaticWordsBytes];
@@ -836,6 +900,169 @@ KVPUB_API kvpub_status kvpub_attend_expanded(kvpub_ctx* ctx, const kvpub_expande
     e.causal = io->causal;
     e.scale_log2 = (float)((double)io->scale * 1.4426950408889634074);
     return map_hip(kvpub::launch_expanded(e, static_cast<hipStream_t>(stream)));
+}
+
+KVPUB_API kvpub_status kvpub_rotation_turns(const kvpub_rotation_config* c, uint64_t* turns) {
+    if (!c || !turns || c->dim < 8 || c->dim > 1024 || c->dim % 8 || c->scaling > KVPUB_SCALING_BLEND) return KVPUB_ERR_INVALID_ARG;
+    if (!std::isfinite(c->base) || c->base <= 1.0) return KVPUB_ERR_INVALID_ARG;
+    if (c->scaling != KVPUB_SCALING_NONE && (!std::isfinite(c->factor) || c->factor < 1.0)) return KVPUB_ERR_INVALID_ARG;
+    if (c->scaling >= KVPUB_SCALING_RAMP &&
+        (!std::isfinite(c->original) || c->original < 1.0 || !(c->low > 0.0) || !(c->low < c->high) || !std::isfinite(c->high)))
+        return KVPUB_ERR_INVALID_ARG;
+    // in the 64 bits of a long double's significand
+    const long double tau = 6.283185307179586476925286766559005768L, dim = c->dim, factor = c->factor;
+    long double base = c->base, lo = 0, hi = 0;
+    if (c->scaling == KVPUB_SCALING_GROWN) base *= std::pow(factor, dim / (dim - 2));
+    if (c->scaling == KVPUB_SCALING_RAMP) {
+        lo = std::max(0.0L, std::floor(dim * std::log(c->original / (tau * c->high)) / (2 * std::log(base))));
+        hi = std::min(dim - 1, std::ceil(dim * std::log(c->original / (tau * c->low)) / (2 * std::log(base))));
+    }
+    for (uint32_t i = 0; i < c->dim / 2; ++i) {
+        long double f = std::pow(base, -2.0L * i / dim), keep = 1;
+        if (c->scaling == KVPUB_SCALING_LINEAR) keep = 0;
+        if (c->scaling == KVPUB_SCALING_RAMP) keep = 1 - std::min(1.0L, std::max(0.0L, (i - lo) / std::max(hi - lo, 0.001L)));
+        if (c->scaling == KVPUB_SCALING_BLEND) keep = std::min(1.0L, std::max(0.0L, (c->original * f / tau - c->low) / ((long double)c->high - c->low)));
+        if (keep < 1) f = f * keep + f / factor * (1 - keep);
+        turns[i] = (uint64_t)std::floor(f / tau * 18446744073709551616.0L + 0.5L);      // f <= 1: below 2^62
+    }
+    return KVPUB_OK;
+}
+
+KVPUB_API kvpub_status kvpub_rotate(kvpub_ctx* ctx, const kvpub_rotate_io* io, kvpub_stream_t stream) {
+    if (!ctx || !io) return KVPUB_ERR_INVALID_ARG;
+    if (io->num_tokens < 0 || io->num_tokens > kMaxQueryTokens || io->num_heads < 1 || io->num_heads > 1024 || io->head_dim < 8 ||
+        io->head_dim > 1024 || io->head_dim % 8 || io->type > KVPUB_FP32 || io->transpose > 1 || !good_rotation(&io->rotation, io->head_dim))
+        return KVPUB_ERR_INVALID_ARG;
+    if (io->num_tokens == 0) return KVPUB_OK;
+    if (!good_rows(io->x, io->x_token_stride, io->x_head_stride, io->head_dim, io->num_heads) ||
+        !good_output(io->y, io->y_token_stride, io->y_head_stride, io->head_dim, io->num_heads, io->num_tokens) || !io->positions ||
+        !aligned(io->positions, 4))
+        return KVPUB_ERR_INVALID_ARG;
+    const bool in_place = io->x == io->y;
+    if (in_place && (io->x_token_stride != io->y_token_stride || io->x_head_stride != io->y_head_stride)) return KVPUB_ERR_INVALID_ARG;
+    DeviceGuard guard(ctx->cfg.device);
+    if (!guard.ok) return KVPUB_ERR_HIP;
+    kvpub::RotateParams p;
+    std::memset(&p, 0, sizeof p);
+    p.x = io->x;
+    p.y = io->y;
+    p.x_token = io->x_token_stride;
+    p.x_head = io->x_head_stride;
+    p.y_token = io->y_token_stride;
+    p.y_head = io->y_head_stride;
+    p.positions = io->positions;
+    p.rotation = rotation_params(&io->rotation);
+    p.num_tokens = (uint32_t)io->num_tokens;
+    p.heads = io->num_heads;
+    p.units = (in_place ? io->rotation.dim : io->head_dim) / 8;
+    p.type = io->type;
+    p.sign = io->transpose ? -io->rotation.magnitude : io->rotation.magnitude;
+    return map_hip(kvpub::launch_rotate(p, static_cast<hipStream_t>(stream)));
+}
+
+KVPUB_API kvpub_status kvpub_store_rotated(kvpub_ctx* ctx, uint32_t layer, int64_t num_tokens, const void* latent, int64_t latent_row_stride,
+                                           const void* rope, int64_t rope_row_stride, const void* indexer, int64_t indexer_row_stride,
+                                           const int64_t* slot_mapping, const int32_t* positions, const kvpub_rotation* rope_rotation,
+                                           const kvpub_rotation* indexer_rotation, kvpub_stream_t stream) {
+    if (!rope_rotation && !indexer_rotation)
+        return kvpub_store(ctx, layer, num_tokens, latent, latent_row_stride, rope, rope_row_stride, indexer, indexer_row_stride,
+                           slot_mapping, stream);
+    kvpub_status st = check_store(ctx, layer, num_tokens, latent, latent_row_stride, rope, rope_row_stride, indexer, indexer_row_stride,
+                                  slot_mapping);
+    if (st != KVPUB_OK) return st;
+    if ((rope_rotation && !good_rotation(rope_rotation, KVPUB_ROPE_DIM)) ||
+        (indexer_rotation && !good_rotation(indexer_rotation, KVPUB_INDEXER_DIM)))
+        return KVPUB_ERR_INVALID_ARG;
+    if (num_tokens == 0) return KVPUB_OK;
+    if (!positions || !aligned(positions, 4)) return KVPUB_ERR_INVALID_ARG;
+    DeviceGuard guard(ctx->cfg.device);
+    if (!guard.ok) return KVPUB_ERR_HIP;
+    kvpub::StoreRotatedParams p;
+    std::memset(&p, 0, sizeof p);
+    p.s = store_params(ctx, layer, num_tokens, latent, latent_row_stride, rope, rope_row_stride, indexer, indexer_row_stride, slot_mapping);
+    p.positions = positions;
+    p.rope = rotation_params(rope_rotation);
+    p.indexer = rotation_params(indexer_rotation);
+    p.replicas = ctx->cfg.num_replicas;
+    return map_hip(kvpub::launch_store_rotated(p, static_cast<hipStream_t>(stream)));
+}
+
+KVPUB_API kvpub_status kvpub_heads_append(kvpub_ctx* ctx, const kvpub_heads* cache, uint32_t layer, const kvpub_heads_rows* rows,
+                                          const kvpub_pages* pages, const kvpub_rotation* rotation, const int32_t* positions,
+                                          kvpub_stream_t stream) {
+    if (!ctx || !good_heads(cache) || layer >= cache->num_layers || !rows) return KVPUB_ERR_INVALID_ARG;
+    if (rows->num_tokens < 0 || rows->num_tokens > kMaxQueryTokens || rows->type > KVPUB_FP16 || rows->reserved != 0)
+        return KVPUB_ERR_INVALID_ARG;
+    if (rotation && !good_rotation(rotation, cache->head_dim)) return KVPUB_ERR_INVALID_ARG;
+    kvpub_status st = check_seqs(pages, rows->num_tokens);
+    if (st != KVPUB_OK || rows->num_tokens == 0 || pages->num_seqs == 0) return st;
+    const uint32_t G = cache->num_kv_heads, D = cache->head_dim;
+    if (!good_rows(rows->k, rows->k_token_stride, rows->k_head_stride, D, G) || !good_rows(rows->v, rows->v_token_stride, rows->v_head_stride, D, G))
+        return KVPUB_ERR_INVALID_ARG;
+    if (rotation && !aligned(positions, 4)) return KVPUB_ERR_INVALID_ARG;
+    DeviceGuard guard(ctx->cfg.device);
+    if (!guard.ok) return KVPUB_ERR_HIP;
+    kvpub::HeadsAppendParams p;
+    std::memset(&p, 0, sizeof p);
+    p.heads = heads_params(cache);
+    p.seqs = seq_params(pages, rows->num_tokens);
+    for (uint32_t r = 0; r < cache->num_replicas; ++r) p.base[r] = heads_layer(cache, r, layer);
+    p.replicas = cache->num_replicas;
+    p.type = rows->type;
+    p.k = static_cast<const uint16_t*>(rows->k);
+    p.v = static_cast<const uint16_t*>(rows->v);
+    p.k_token = rows->k_token_stride;
+    p.k_head = rows->k_head_stride;
+    p.v_token = rows->v_token_stride;
+    p.v_head = rows->v_head_stride;
+    p.positions = positions;
+    p.rotation = rotation_params(rotation);
+    p.head = reinterpret_cast<const kvpub::CtxHead*>(ctx->words + kvpub::kStatusOffset);
+    p.invalid_count = reinterpret_cast<unsigned long long*>(ctx->words + kvpub::kInvalidOffset);
+    return map_hip(kvpub::launch_heads_append(p, static_cast<hipStream_t>(stream)));
+}
+
+KVPUB_API uint64_t kvpub_heads_attend_workspace(const kvpub_heads* cache, const kvpub_heads_queries* q, const kvpub_pages* pages) {
+    if (!good_heads(cache) || !good_heads_queries(cache, q) || !good_pages(pages) || q->num_tokens == 0 || pages->num_seqs == 0) return 0;
+    return heads_plan(cache, q, pages).bytes;
+}
+
+KVPUB_API kvpub_status kvpub_heads_attend(kvpub_ctx* ctx, const kvpub_heads* cache, uint32_t replica, uint32_t layer,
+                                          const kvpub_heads_queries* q, const kvpub_pages* pages, void* workspace,
+                                          uint64_t workspace_bytes, kvpub_stream_t stream) {
+    if (!ctx || !good_heads(cache) || replica >= cache->num_replicas || layer >= cache->num_layers || !good_heads_queries(cache, q))
+        return KVPUB_ERR_INVALID_ARG;
+    kvpub_status st = check_seqs(pages, q->num_tokens);
+    if (st != KVPUB_OK || q->num_tokens == 0 || pages->num_seqs == 0) return st;
+    const uint32_t D = cache->head_dim;
+    if (!good_rows(q->q, q->q_token_stride, q->q_head_stride, D, q->num_heads) ||
+        !good_output(q->out, q->out_token_stride, q->out_head_stride, D, q->num_heads, q->num_tokens) ||
+        !good_lse(q->lse, q->lse_token_stride, q->num_heads, q->num_tokens))
+        return KVPUB_ERR_INVALID_ARG;
+    const kvpub::HeadsAttendPlan plan = heads_plan(cache, q, pages);
+    if (!workspace || !aligned(workspace, 16) || workspace_bytes < plan.bytes) return KVPUB_ERR_INVALID_ARG;
+    DeviceGuard guard(ctx->cfg.device);
+    if (!guard.ok) return KVPUB_ERR_HIP;
+    kvpub::HeadsAttendParams p;
+    std::memset(&p, 0, sizeof p);
+    p.heads = heads_params(cache);
+    p.seqs = seq_params(pages, q->num_tokens);
+    p.base = heads_layer(cache, replica, layer);
+    p.type = q->type;
+    p.group = q->num_heads / cache->num_kv_heads;
+    p.q = static_cast<const uint16_t*>(q->q);
+    p.out = static_cast<uint16_t*>(q->out);
+    p.q_token = q->q_token_stride;
+    p.q_head = q->q_head_stride;
+    p.out_token = q->out_token_stride;
+    p.out_head = q->out_head_stride;
+    p.lse = q->lse;
+    p.lse_token = q->lse_token_stride;
+    p.scale_log2 = (float)((double)q->scale * 1.4426950408889634074);
+    p.tree = pages->tree_mask;
+    p.tree_words = pages->tree_words;
+    p.invalid_count = reinterpret_cast<unsigned long long*>(ctx->words + kvpub::kInvalidOffset);
+    return map_hip(kvpub::launch_heads_attend(p, workspace, static_cast<hipStream_t>(stream)));
 }
 
 KVPUB_API kvpub_status kvpub_fence(kvpub_ctx* ctx, uint32_t lane, kvpub_stream_t stream) {

@@ -203,6 +203,113 @@ struct ExpandedParams {
 };
 hipError_t launch_expanded(const ExpandedParams& p, hipStream_t stream);
 
+// A rotation by positions (rotation.h); dim == 0: none.
+struct RotationParams {
+    const uint64_t* turns;
+    uint32_t dim;
+    uint32_t start;
+    uint32_t halves;
+    float magnitude;
+};
+
+// Rows of heads rotated (rotate_kernel.hip).  Strides in elements.
+struct RotateParams {
+    const void* x;
+    void* y;
+    int64_t x_token, x_head, y_token, y_head;
+    const int32_t* positions;
+    RotationParams rotation;
+    uint32_t num_tokens;
+    uint32_t heads;
+    uint32_t units;              // groups of 8 values of a row that the call touches: the rotated ones, then the copied ones
+    uint32_t type;               // KVPUB_BF16, KVPUB_FP16, KVPUB_FP32
+    float sign;                  // the magnitude, negative for the transpose
+};
+hipError_t launch_rotate(const RotateParams& p, hipStream_t stream);
+
+// The latent cache's store with rotations (store_rotated_kernel.hip).
+struct StoreRotatedParams {
+    StoreParams s;
+    const int32_t* positions;
+    RotationParams rope;
+    RotationParams indexer;
+    uint32_t replicas;
+};
+hipError_t launch_store_rotated(const StoreRotatedParams& p, hipStream_t stream);
+
+// The cache of key and value heads: one replica's layer.
+struct HeadsParams {
+    uint64_t page_stride;        // bytes
+    int64_t num_pages;
+    uint32_t groups;             // key-value heads
+    uint32_t dim;                // values of a head
+};
+
+// The sequences of a call on it (kvpub_pages).
+struct SeqParams {
+    const int32_t* kv_len;
+    const int32_t* q_start;      // null: one token a sequence
+    const int32_t* pages;
+    int64_t pages_stride;
+    uint32_t num_seqs;
+    uint32_t num_tokens;
+    uint32_t max_q;
+    uint32_t max_kv;
+};
+
+// Appending to it (heads_append_kernel.hip).
+struct HeadsAppendParams {
+    HeadsParams heads;
+    SeqParams seqs;
+    uint8_t* base[kMaxReplicas]; // replica r, already offset to the layer
+    uint32_t replicas;
+    uint32_t type;               // KVPUB_BF16 or KVPUB_FP16
+    const uint16_t* k;
+    const uint16_t* v;
+    int64_t k_token, k_head, v_token, v_head;
+    const int32_t* positions;    // null: the positions in the sequence
+    RotationParams rotation;
+    const CtxHead* head;         // status
+    unsigned long long* invalid_count;
+    uint32_t first;              // set by launch_heads_append: the launch's first place
+};
+hipError_t launch_heads_append(const HeadsAppendParams& p, hipStream_t stream);
+
+// Attention over it (heads_attend_kernel.hip).
+struct HeadsAttendParams {
+    HeadsParams heads;
+    SeqParams seqs;
+    const uint8_t* base;         // the replica, already offset to the layer
+    uint32_t type;
+    uint32_t group;              // query heads of a key-value head
+    const uint16_t* q;
+    uint16_t* out;
+    int64_t q_token, q_head, out_token, out_head, lse_token;
+    float* lse;                  // null: not written
+    float scale_log2;            // scale * log2(e)
+    uint32_t tree_words;
+    const uint64_t* tree;        // null: causal
+    unsigned long long* invalid_count;
+    uint32_t chunk;              // positions of a cut
+    uint32_t chunks;             // cuts of max_kv
+    uint32_t first;              // the launch's first unit
+    uint32_t units;              // places for (sequence, rows) units
+    float* part;                 // workspace: [units][groups][chunks][rows][dim]
+    float* part_ml;              // workspace: [units][groups][chunks][rows][2], maximum and sum
+};
+
+// How a call is cut: query rows of a unit, positions of a cut, workspace.
+struct HeadsAttendPlan {
+    uint32_t rows;
+    uint32_t chunk;
+    uint32_t chunks;
+    uint64_t units;
+    uint64_t bytes;
+};
+HeadsAttendPlan plan_heads_attend(const HeadsParams& h, uint32_t group, uint64_t num_seqs, uint64_t num_tokens, uint64_t max_q,
+                                  uint64_t max_kv);
+hipError_t launch_heads_attend(const HeadsAttendParams& p, void* workspace, hipStream_t stream);
+
 // Enqueue the dequantizing gather on `stream`; returns the launch status.
 hipError_t launch_gather(const GatherParams& p, hipStream_t stream);
 // True if ctx's replicas are exactly these bases with these layer and page strides.

@@ -40,6 +40,10 @@ IDX_PAGE_BYTES = 64 * 128 + 64 * 4
 IDX_SCALES_OFFSET = 64 * 128
 MAX_REPLICAS = 8
 
+BF16, FP16, FP32 = 0, 1, 2
+ROTATE_PAIRS, ROTATE_HALVES = 0, 1
+SCALING_NONE, SCALING_LINEAR, SCALING_GROWN, SCALING_RAMP, SCALING_BLEND = range(5)
+
 # Every function include/kvpub.h declares.
 EXPORTS = ("kvpub_config_init", "kvpub_create", "kvpub_create_static", "kvpub_store", "kvpub_gather", "kvpub_fence",
            "kvpub_fence_host_epoch",
@@ -48,7 +52,9 @@ EXPORTS = ("kvpub_config_init", "kvpub_create", "kvpub_create_static", "kvpub_st
            "kvpub_destroy", "kvpub_strerror", "kvpub_abi_version", "kvpub_vmm_create",
            "kvpub_vmm_grow", "kvpub_vmm_pages", "kvpub_vmm_destroy",
            "kvpub_attend_workspace", "kvpub_attend", "kvpub_attend_slots_workspace", "kvpub_attend_slots",
-           "kvpub_attend_weights", "kvpub_evict_workspace", "kvpub_evict", "kvpub_attend_expanded")
+           "kvpub_attend_weights", "kvpub_evict_workspace", "kvpub_evict", "kvpub_attend_expanded",
+           "kvpub_rotation_turns", "kvpub_rotate", "kvpub_store_rotated", "kvpub_heads_append",
+           "kvpub_heads_attend_workspace", "kvpub_heads_attend")
 
 
 class kvpub_config(ctypes.Structure):
@@ -143,6 +149,79 @@ class kvpub_expanded_io(ctypes.Structure):
                  ("reserved", ctypes.c_uint32)])
 
 
+class kvpub_rotation(ctypes.Structure):
+    _fields_ = [("turns", ctypes.c_void_p),
+                ("dim", ctypes.c_uint32),
+                ("start", ctypes.c_uint32),
+                ("layout", ctypes.c_uint32),
+                ("magnitude", ctypes.c_float)]
+
+
+class kvpub_rotation_config(ctypes.Structure):
+    _fields_ = [("dim", ctypes.c_uint32),
+                ("scaling", ctypes.c_uint32),
+                ("base", ctypes.c_double),
+                ("factor", ctypes.c_double),
+                ("original", ctypes.c_double),
+                ("low", ctypes.c_double),
+                ("high", ctypes.c_double)]
+
+
+class kvpub_rotate_io(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p),
+                ("y", ctypes.c_void_p),
+                ("x_token_stride", ctypes.c_int64),
+                ("x_head_stride", ctypes.c_int64),
+                ("y_token_stride", ctypes.c_int64),
+                ("y_head_stride", ctypes.c_int64),
+                ("positions", ctypes.c_void_p),
+                ("rotation", kvpub_rotation),
+                ("num_tokens", ctypes.c_int64),
+                ("num_heads", ctypes.c_uint32),
+                ("head_dim", ctypes.c_uint32),
+                ("type", ctypes.c_uint32),
+                ("transpose", ctypes.c_uint32)]
+
+
+class kvpub_heads(ctypes.Structure):
+    _fields_ = [("bases", ctypes.c_void_p * MAX_REPLICAS),
+                ("num_pages", ctypes.c_uint64),
+                ("page_stride", ctypes.c_uint64),
+                ("layer_stride", ctypes.c_uint64),
+                ("num_replicas", ctypes.c_uint32),
+                ("num_layers", ctypes.c_uint32),
+                ("num_kv_heads", ctypes.c_uint32),
+                ("head_dim", ctypes.c_uint32)]
+
+
+class kvpub_heads_rows(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p),
+                ("v", ctypes.c_void_p),
+                ("k_token_stride", ctypes.c_int64),
+                ("k_head_stride", ctypes.c_int64),
+                ("v_token_stride", ctypes.c_int64),
+                ("v_head_stride", ctypes.c_int64),
+                ("num_tokens", ctypes.c_int64),
+                ("type", ctypes.c_uint32),
+                ("reserved", ctypes.c_uint32)]
+
+
+class kvpub_heads_queries(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p),
+                ("out", ctypes.c_void_p),
+                ("lse", ctypes.c_void_p),
+                ("q_token_stride", ctypes.c_int64),
+                ("q_head_stride", ctypes.c_int64),
+                ("out_token_stride", ctypes.c_int64),
+                ("out_head_stride", ctypes.c_int64),
+                ("lse_token_stride", ctypes.c_int64),
+                ("num_tokens", ctypes.c_int64),
+                ("num_heads", ctypes.c_uint32),
+                ("type", ctypes.c_uint32),
+                ("scale", ctypes.c_float),
+                ("reserved", ctypes.c_uint32)]
+
+
 class KvpubError(RuntimeError):
     def __init__(self, status, what=""):
         self.status = status
@@ -164,6 +243,7 @@ def load(path=LIB_PATH):
     vp, u32, u64, i64, i32 = (ctypes.c_void_p, ctypes.c_uint32, ctypes.c_uint64,
                               ctypes.c_int64, ctypes.c_int)
     cfgp = ctypes.POINTER(kvpub_config)
+    rp, hp, hqp = ctypes.POINTER(kvpub_rotation), ctypes.POINTER(kvpub_heads), ctypes.POINTER(kvpub_heads_queries)
     qp, pp, ep = ctypes.POINTER(kvpub_queries), ctypes.POINTER(kvpub_pages), ctypes.POINTER(kvpub_evict_io)
     sig = {
         "kvpub_config_init": (None, [cfgp, u32, u32, u64]),
@@ -194,6 +274,12 @@ def load(path=LIB_PATH):
         "kvpub_evict_workspace": (u64, [ep]),
         "kvpub_evict": (i32, [vp, u32, ep, vp, u64, vp]),
         "kvpub_attend_expanded": (i32, [vp, ctypes.POINTER(kvpub_expanded_io), vp]),
+        "kvpub_rotation_turns": (i32, [ctypes.POINTER(kvpub_rotation_config), ctypes.POINTER(u64)]),
+        "kvpub_rotate": (i32, [vp, ctypes.POINTER(kvpub_rotate_io), vp]),
+        "kvpub_store_rotated": (i32, [vp, u32, i64, vp, i64, vp, i64, vp, i64, vp, vp, rp, rp, vp]),
+        "kvpub_heads_append": (i32, [vp, hp, u32, ctypes.POINTER(kvpub_heads_rows), pp, rp, vp, vp]),
+        "kvpub_heads_attend_workspace": (u64, [hp, hqp, pp]),
+        "kvpub_heads_attend": (i32, [vp, hp, u32, u32, hqp, pp, vp, u64, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -430,3 +516,85 @@ def expanded_io(q_nope, q_rope, k_nope, k_rope, v, out, lse, q_start, k_start, n
     return kvpub_expanded_io(q_nope, q_rope, k_nope, k_rope, v, out, lse, H * 128, 128, H * 64, 64,
                              H * k_head_stride, k_head_stride, 64, H * v_head_stride, v_head_stride, H * 128, 128, H,
                              q_start, k_start, num_tokens, num_keys, num_seqs, H, max_q_len, causal, scale, 0)
+
+
+# -- rotary positions and the cache of key and value heads ----------------------
+
+def kvpub_rotation_turns(config):
+    """Returns (status, turns as a numpy uint64 array or None): the table to copy to the device."""
+    import numpy as np
+    turns = np.zeros(max(config.dim, 8) // 2, dtype=np.uint64)
+    st = load().kvpub_rotation_turns(ctypes.byref(config), turns.ctypes.data_as(ctypes.POINTER(ctypes.c_uint64)))
+    return st, (turns if st == KVPUB_OK else None)
+
+
+def kvpub_rotate(ctx, io, stream=0):
+    return load().kvpub_rotate(ctx, _ref(io), stream)
+
+
+def kvpub_store_rotated(ctx, layer, num_tokens, latent, latent_row_stride, rope, rope_row_stride, indexer,
+                        indexer_row_stride, slot_mapping, positions, rope_rotation, indexer_rotation, stream=0):
+    return load().kvpub_store_rotated(ctx, layer, num_tokens, latent, latent_row_stride, rope, rope_row_stride, indexer,
+                                      indexer_row_stride, slot_mapping, positions, _ref(rope_rotation),
+                                      _ref(indexer_rotation), stream)
+
+
+def kvpub_heads_append(ctx, cache, layer, rows, pages, rotation=None, positions=None, stream=0):
+    return load().kvpub_heads_append(ctx, _ref(cache), layer, _ref(rows), _ref(pages), _ref(rotation), positions, stream)
+
+
+def kvpub_heads_attend_workspace(cache, q, pages):
+    return load().kvpub_heads_attend_workspace(_ref(cache), _ref(q), _ref(pages))
+
+
+def kvpub_heads_attend(ctx, cache, replica, layer, q, pages, workspace, workspace_bytes, stream=0):
+    return load().kvpub_heads_attend(ctx, _ref(cache), replica, layer, _ref(q), _ref(pages), workspace, workspace_bytes,
+                                     stream)
+
+
+def rotation_config(dim, base=10000.0, scaling=SCALING_NONE, factor=1.0, original=1.0, low=1.0, high=32.0):
+    return kvpub_rotation_config(dim, scaling, base, factor, original, low, high)
+
+
+def rotation(turns, dim, start=0, layout=ROTATE_PAIRS, magnitude=1.0):
+    """Build a kvpub_rotation; turns: the device address of its table."""
+    return kvpub_rotation(turns, dim, start, layout, magnitude)
+
+
+def rotate_io(x, y, positions, rotation, num_tokens, num_heads, head_dim, type, x_token_stride=None, x_head_stride=None,
+              y_token_stride=None, y_head_stride=None, transpose=0):
+    """Build a kvpub_rotate_io from device addresses; strides default to dense [T, H, head_dim]."""
+    width = lambda s: head_dim if s is None else s
+    dense = lambda s, head: num_heads * width(head) if s is None else s
+    return kvpub_rotate_io(x, y, dense(x_token_stride, x_head_stride), width(x_head_stride),
+                           dense(y_token_stride, y_head_stride), width(y_head_stride), positions, rotation, num_tokens,
+                           num_heads, head_dim, type, transpose)
+
+
+def heads_page_bytes(num_kv_heads, head_dim):
+    """Bytes of a page of the cache of heads (KVPUB_HEADS_PAGE_BYTES)."""
+    return (num_kv_heads * (128 * head_dim + 2) + 15) // 16 * 16
+
+
+def heads(bases, num_pages, num_kv_heads, head_dim, num_layers=1, page_stride=None, layer_stride=None):
+    """Build a kvpub_heads over replicas at these device addresses; strides default to dense pages and layers."""
+    page = heads_page_bytes(num_kv_heads, head_dim) if page_stride is None else page_stride
+    layer = num_pages * page if layer_stride is None else layer_stride
+    return kvpub_heads((ctypes.c_void_p * MAX_REPLICAS)(*bases), num_pages, page, layer, len(bases), num_layers,
+                       num_kv_heads, head_dim)
+
+
+def heads_rows(k, v, num_tokens, type, k_token_stride, k_head_stride, v_token_stride, v_head_stride):
+    """Build a kvpub_heads_rows from device addresses."""
+    return kvpub_heads_rows(k, v, k_token_stride, k_head_stride, v_token_stride, v_head_stride, num_tokens, type, 0)
+
+
+def heads_queries(q, out, lse, num_tokens, num_heads, head_dim, scale, type, q_token_stride=None, q_head_stride=None,
+                  out_token_stride=None, out_head_stride=None, lse_token_stride=None):
+    """Build a kvpub_heads_queries from device addresses; strides default to dense [T, H, head_dim] and [T, H]."""
+    qh = head_dim if q_head_stride is None else q_head_stride
+    oh = head_dim if out_head_stride is None else out_head_stride
+    return kvpub_heads_queries(q, out, lse, num_heads * qh if q_token_stride is None else q_token_stride, qh,
+                               num_heads * oh if out_token_stride is None else out_token_stride, oh,
+                               num_heads if lse_token_stride is None else lse_token_stride, num_tokens, num_heads, type,
+                               scale, 0)
