@@ -36,10 +36,17 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
-constexpr uint32_t kThreads = 256, kWaves = 4;
+template <int D> constexpr int kManyWaves = D == 256 ? 8 : 16;    // of a block that has a unit's positions to itself
+constexpr uint32_t kLeastChunk = 512;
 constexpr uint32_t kTile = 32;                    // positions of a wave's step
 constexpr float kLazy = 8.0f;                     // rescale when a maximum grows past 2^8
 constexpr float kLn2 = 0.693147180559945309f;
+
+typedef __attribute__((address_space(1))) uint8_t gbyte;   // a byte in global memory
+template <class T> using gptr = __attribute__((address_space(1))) T*;
+
+// Waves that a SIMD should hold: what the registers of the accumulators leave room for.
+constexpr int waves_a_simd(int D, int RT) { return RT * D <= 64 ? 5 : (RT * D <= 128 ? 4 : (RT * D <= 512 ? 2 : 1)); }
 
 template <class E> struct Operand;
 template <> struct Operand<__bf16> {
@@ -88,6 +95,20 @@ __device__ __forceinline__ Unit unit_of(const HeadsAttendParams& p, const Places
     return u;
 }
 
+// A row's output from its joined parts, D/16 values a lane.
+template <class E, int D>
+__device__ __forceinline__ void put_row(const HeadsAttendParams& p, const Unit& u, uint32_t g, uint32_t row, uint32_t seg,
+                                        const float (&acc)[D / 16], float top, float sum) {
+    const uint32_t i = row / p.group, h = g * p.group + row - i * p.group;
+    E* dst = (E*)p.out + (int64_t)(u.s.q0 + i) * p.out_token + (int64_t)h * p.out_head + seg;
+    const float f = sum == 0.f ? 0.f : 1.f / sum;           // no position seen: 0
+    E y[D / 16];
+#pragma unroll
+    for (int n = 0; n < D / 16; ++n) y[n] = (E)(acc[n] * f);
+    __builtin_memcpy(__builtin_assume_aligned(dst, D / 8), y, sizeof y);
+    if (seg == 0 && p.lse) p.lse[(int64_t)(u.s.q0 + i) * p.lse_token + h] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+}
+
 // 64 bits of a tree row from node j on (j below 0: the positions before the tree, seen by all).
 __device__ __forceinline__ uint64_t tree_bits(const uint64_t* row, uint32_t words, int64_t j) {
     if (j < 0) {
@@ -102,6 +123,12 @@ __device__ __forceinline__ uint64_t tree_bits(const uint64_t* row, uint32_t word
     return (a >> s) | (b << (64 - s));
 }
 
+// Bits of the positions pos .. pos + 31 that lie below lim.
+__device__ __forceinline__ uint32_t first_bits(uint32_t lim, uint32_t pos) {
+    const uint32_t left = lim > pos ? lim - pos : 0u;
+    return left >= 32 ? 0xFFFFFFFFu : (1u << left) - 1;
+}
+
 // Some token of the sequence sees one of the 64 positions from pos on (the whole wave asks).
 __device__ __forceinline__ bool any_sees(const HeadsAttendParams& p, const Unit& u, uint32_t pos) {
     if ((int64_t)pos < u.base || !p.tree) return true;
@@ -113,6 +140,17 @@ __device__ __forceinline__ bool any_sees(const HeadsAttendParams& p, const Unit&
     return __any(sees);
 }
 
+__device__ __forceinline__ float power(uint32_t byte) {
+    const uint32_t b = byte < 1 ? 1u : (byte > 245 ? 245u : byte);
+    return __uint_as_float(b << 23);
+}
+
+__device__ __forceinline__ const gbyte* uniform(const uint8_t* p) {
+    const gbyte* g = (const gbyte*)p;
+    asm volatile("" : "+s"(g));
+    return g;
+}
+
 // The codes of a tile of 32 positions in one wave's registers.
 template <int D>
 struct Tile {
@@ -120,53 +158,86 @@ struct Tile {
     uint32_t v[8][D / 64];           // position j of this lane group, values (D/16) (l%16) ..
     uint32_t scales;                 // bytes of the keys and of the values
 
-    __device__ __forceinline__ void load(const uint8_t* page, uint32_t head, uint32_t groups, uint32_t half, uint32_t l16, uint32_t g4) {
-        const uint8_t* kp = page + (uint64_t)head * 128 * D + half * (kTile * D);
+    // `page`: uniform; with a 32-bit offset a lane the loads need no 64-bit addresses.
+    __device__ __forceinline__ void load_keys(const uint8_t* page, uint32_t head, uint32_t groups, uint32_t half, uint32_t lane_at) {
+        const gbyte* kp = uniform(page + head * (128 * D) + half * (kTile * D));
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
-            for (int c = 0; c < D / 64; ++c) k[u][c] = *(const i32x4*)(kp + (u * 16 + l16) * D + c * 64 + g4 * 16);
-        const uint8_t* vp = kp + 64 * D;
+            for (int c = 0; c < D / 64; ++c) k[u][c] = *(gptr<const i32x4>)(kp + lane_at + (u * 16 * D + c * 64));
+        const uint32_t at = 2 * head;
+        scales = *(kptr<uint32_t>)(page + groups * (128 * D) + (at & ~3u)) >> ((at & 2u) * 8);
+    }
+    __device__ __forceinline__ void load_values(const uint8_t* page, uint32_t head, uint32_t half, uint32_t lane_at) {
+        const gbyte* vp = uniform(page + head * (128 * D) + 64 * D + half * (kTile * D));
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const uint8_t* a = vp + ((j >> 2) * 16 + g4 * 4 + (j & 3)) * D + l16 * (D / 16);
-            if constexpr (D == 64) v[j][0] = *(const uint32_t*)a;
+            if (D == 256 && j == 4) vp += 16 * D;          // beyond what an instruction's offset holds
+            const gbyte* a = vp + lane_at + ((D == 256 ? 0 : (j >> 2) * 16) + (j & 3)) * D;
+            if constexpr (D == 64) v[j][0] = *(gptr<const uint32_t>)a;
             else if constexpr (D == 128) {
-                const u32x2 w = *(const u32x2*)a;
+                const u32x2 w = *(gptr<const u32x2>)a;
                 v[j][0] = w.x, v[j][1] = w.y;
             } else {
-                const u32x4 w = *(const u32x4*)a;
+                const u32x4 w = *(gptr<const u32x4>)a;
                 v[j][0] = w.x, v[j][1] = w.y, v[j][2] = w.z, v[j][3] = w.w;
             }
         }
-        const uint32_t at = 2 * head;
-        scales = *(const uint32_t*)(page + (uint64_t)groups * 128 * D + (at & ~3u)) >> ((at & 2u) * 8);
     }
-    static __device__ __forceinline__ float power(uint32_t byte) {
-        const uint32_t b = byte < 1 ? 1u : (byte > 245 ? 245u : byte);
-        return __uint_as_float(b << 23);
-    }
-    __device__ __forceinline__ float key_scale() const { return power(scales & 255u); }
-    __device__ __forceinline__ float value_scale() const { return power((scales >> 8) & 255u); }
 };
 
-template <class E, int D, int RT>
-__global__ __launch_bounds__(kThreads, D * RT <= 128 ? 3 : (D * RT <= 256 ? 2 : 1)) void heads_attend_kernel(const HeadsAttendParams p, const Places places) {
+template <class E>
+__device__ __forceinline__ typename Operand<E>::x8 load_query(const E* src, bool is, bool negate) {
+    u32x4 w = {0, 0, 0, 0};
+    if (is) w = *(const u32x4*)src;
+    if (negate) w ^= 0x80008000u;
+    return __builtin_bit_cast(typename Operand<E>::x8, w);
+}
+
+// W waves a block; Shared: the queries' operands stay in LDS (their registers would
+// cost the second wave a SIMD).
+template <class E, int D, int RT, int W>
+__global__ __launch_bounds__(W * 64, waves_a_simd(D, RT)) void heads_attend_kernel(const HeadsAttendParams p, const Places places) {
     typedef Operand<E> Op;
     constexpr uint32_t R = 16 * RT;
-    constexpr int NB = D / 16;
-    __shared__ float obuf[kWaves][16][D + 4];
-    __shared__ float ml[kWaves][16][2];
+    constexpr int NB = D / 16, NQ = D / 32;
+    constexpr bool Shared = RT * D >= 512;
+    struct Join {
+        float o[W][16][D + 4];
+        float ml[W][16][2];
+    };
+    union Lds {
+        Join join;
+        typename Op::x8 q[Shared ? RT * NQ : 1][64];
+        __device__ Lds() {}
+    };
+    __shared__ Lds lds;
     const uint32_t G = p.heads.groups, tid = threadIdx.x, lane = tid & 63u, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const uint32_t l16 = lane & 15u, g4 = lane >> 4;
     const uint32_t g = blockIdx.x % G, rest = blockIdx.x / G, cut = rest % p.chunks, place = rest / p.chunks;
     const Unit u = unit_of(p, places, p.first + place, R);
     if (u.rows == 0 || cut >= u.chunks) return;
 
+    const int32_t* table = p.seqs.pages + (int64_t)u.s.b * p.seqs.pages_stride;
+    const uint32_t end = u.reach < (cut + 1) * p.chunk ? u.reach : (cut + 1) * p.chunk;
+    const uint32_t last = (end + kTile - 1) / kTile;
+    const bool counts = g == 0 && u.row0 + R >= u.rows;
+    auto page_of = [&](uint32_t t) { return t < last ? uniform_load(table, t >> 1) : 0; };
+    auto at = [&](int32_t page) { return p.base + ((uint32_t)page < p.heads.num_pages ? (uint64_t)(uint32_t)page * p.heads.page_stride : 0ull); };
+    uint32_t t = cut * (p.chunk / kTile) + wave;
+    int32_t page = page_of(t), page1 = page_of(t + W);
+    const uint32_t key_at = l16 * D + g4 * 16, value_at = g4 * 4 * D + l16 * (D / 16);
+    Tile<D> tile;
+    if (t < last) {
+        tile.load_keys(at(page), g, G, t & 1u, key_at);
+        tile.load_values(at(page), g, t & 1u, value_at);
+    }
+
     // queries, and what each row sees: positions below lim (tree: of those before the tree, then its bits)
-    typename Op::x8 q[RT][D / 32];
+    typename Op::x8 q[Shared ? 1 : RT][NQ];
+    const bool negate = p.scale_log2 < 0.f;
     uint32_t lim[RT];
-    const uint64_t* tree[RT];
+    uint32_t tree[RT];                     // first word of the row's bits
     uint32_t least = 0xFFFFFFFFu;          // positions that all rows see
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
@@ -175,15 +246,17 @@ __global__ __launch_bounds__(kThreads, D * RT <= 128 ? 3 : (D * RT <= 256 ? 2 : 
         const uint32_t i = is ? row / p.group : 0u, h = g * p.group + (is ? row - i * p.group : 0u);
         const E* src = (const E*)p.q + (int64_t)(u.s.q0 + i) * p.q_token + (int64_t)h * p.q_head + g4 * 16;
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-            if (is) q[r][c] = *(const typename Op::x8*)(src + (c >> 1) * 64 + (c & 1) * 8);
-            else q[r][c] = typename Op::x8{};
+        for (int c = 0; c < NQ; ++c) {
+            const E* from = src + (c >> 1) * 64 + (c & 1) * 8;
+            if constexpr (!Shared) q[r][c] = load_query<E>(from, is, negate);
+            else if ((r * NQ + c) % W == (int)wave) lds.q[r * NQ + c][lane] = load_query<E>(from, is, negate);
         }
         const int64_t top = u.base + (p.tree ? 0 : (int64_t)i + 1);
         lim[r] = is ? (top > 0 ? (uint32_t)top : 0u) : 0xFFFFFFFFu;
-        tree[r] = p.tree && is ? p.tree + (uint64_t)(u.s.q0 + i) * p.tree_words : nullptr;
+        tree[r] = (u.s.q0 + i) * p.tree_words;
         least = lim[r] < least ? lim[r] : least;
     }
+    if constexpr (Shared) __syncthreads();
 #pragma unroll
     for (int d = 1; d < 16; d <<= 1) {
         const uint32_t o = __shfl_xor(least, d);
@@ -201,150 +274,136 @@ __global__ __launch_bounds__(kThreads, D * RT <= 128 ? 3 : (D * RT <= 256 ? 2 : 
         for (int n = 0; n < NB; ++n) o[r][n] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
 
-    const int32_t* table = p.seqs.pages + (int64_t)u.s.b * p.seqs.pages_stride;
-    const uint32_t end = u.reach < (cut + 1) * p.chunk ? u.reach : (cut + 1) * p.chunk;
-    const uint32_t last = (end + kTile - 1) / kTile;
-    const bool counts = g == 0 && u.row0 + R >= u.rows;
-    auto page_of = [&](uint32_t t) { return t < last ? __builtin_amdgcn_readfirstlane(table[t >> 1]) : 0; };
-    auto at = [&](int32_t page) { return p.base + ((uint32_t)page < p.heads.num_pages ? (uint64_t)(uint32_t)page * p.heads.page_stride : 0ull); };
-
-    uint32_t t = cut * (p.chunk / kTile) + wave;
-    int32_t page = page_of(t), page1 = page_of(t + kWaves);
-    Tile<D> cur;
-    if (t < last) cur.load(at(page), g, G, t & 1u, l16, g4);
     while (t < last) {
-        Tile<D> next = cur;
-        if (t + kWaves < last) next.load(at(page1), g, G, t & 1u, l16, g4);
-        const int32_t page2 = page_of(t + 2 * kWaves);
-        const uint32_t pos0 = t * kTile;
-        if ((uint32_t)page >= p.heads.num_pages) {
-            // hidden; counted by the rows that see most of the sequence, at a page's first half
-            if (counts && !(t & 1u) && any_sees(p, u, pos0) && lane == 0) atomicAdd(p.invalid_count, 1ull);
-        } else {
-            float x[RT][8];
-            {
-                f32x4 s[RT][2];
+        const uint32_t pos0 = t * kTile, next = t + W;
+        const int32_t page2 = page_of(next + W);
+        const bool bad = (uint32_t)page >= p.heads.num_pages;
+        // a bad page is hidden; counted by the rows that see most of the sequence, at a page's first half
+        if (bad && counts && !(t & 1u) && any_sees(p, u, pos0) && lane == 0) atomicAdd(p.invalid_count, 1ull);
+
+        f32x4 s[RT][2];
 #pragma unroll
-                for (int r = 0; r < RT; ++r) s[r][0] = s[r][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int r = 0; r < RT; ++r) s[r][0] = s[r][1] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int c = 0; c < D / 64; ++c)
+        for (int c = 0; c < D / 64; ++c)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
+            for (int h = 0; h < 2; ++h) {
+                typename Op::x8 a[2];
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            const typename Op::x8 a = Op::widen(cur.k[j][c][2 * h], cur.k[j][c][2 * h + 1]);
-#pragma unroll
-                            for (int r = 0; r < RT; ++r) s[r][j] = Op::mfma(a, q[r][2 * c + h], s[r][j]);
-                        }
-                const float ks = p.scale_log2 * cur.key_scale();
-#pragma unroll
-                for (int r = 0; r < RT; ++r)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) x[r][j] = s[r][j >> 2][j & 3] * ks;
-            }
-            if (pos0 + kTile > least) {
-                // some row does not see the whole tile.  Bit j: this lane's position j
-                uint32_t nan = 0, seen[RT];
+                for (int j = 0; j < 2; ++j) a[j] = Op::widen(tile.k[j][c][2 * h], tile.k[j][c][2 * h + 1]);
 #pragma unroll
                 for (int r = 0; r < RT; ++r) {
-                    uint32_t bits = 0xFFFFFFFFu;
-                    if (tree[r]) bits = (uint32_t)tree_bits(tree[r], p.tree_words, (int64_t)pos0 - u.base);
-                    seen[r] = 0;
+                    typename Op::x8 b;
+                    if constexpr (Shared) b = lds.q[r * NQ + 2 * c + h][lane];
+                    else b = q[r][2 * c + h];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const uint32_t at = (j >> 2) * 16 + g4 * 4 + (j & 3), pos = pos0 + at;
-                        const bool sees = pos < u.s.kv && (p.tree ? ((bits >> at) & 1u) != 0 : pos < lim[r]);
-                        seen[r] |= sees ? 1u << j : 0u;
-                        x[r][j] = sees ? x[r][j] : -INFINITY;
-                    }
-                }
-                // values that do not exist become zeros, and so do rows that hold a NaN code,
-                // with a NaN score for who sees them: a weight of 0 does not hide a NaN
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const bool is = pos0 + (j >> 2) * 16 + g4 * 4 + (j & 3) < u.s.kv;
-#pragma unroll
-                    for (int w = 0; w < D / 64; ++w) {
-                        cur.v[j][w] = is ? cur.v[j][w] : 0u;
-                        nan |= (((cur.v[j][w] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) ? 1u << j : 0u;
-                    }
-                }
-                if (__any(nan)) {
-#pragma unroll
-                    for (int d = 1; d < 16; d <<= 1) nan |= __shfl_xor(nan, d);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if ((nan >> j) & 1u) {
-#pragma unroll
-                            for (int w = 0; w < D / 64; ++w) cur.v[j][w] = 0;
-#pragma unroll
-                            for (int r = 0; r < RT; ++r) x[r][j] = (seen[r] >> j) & 1u ? NAN : x[r][j];
-                        }
+                    for (int j = 0; j < 2; ++j) s[r][j] = Op::mfma(a[j], b, s[r][j]);
                 }
             }
-            bool grows = false;
-            float high[RT];
+        // the scale of a score in powers of 2 is kept above 0 and below infinity, so that a hidden score stays -infinity
+        const float ks = fminf(fmaxf(fabsf(p.scale_log2) * power(tile.scales & 255u), FLT_MIN), FLT_MAX), vs = power((tile.scales >> 8) & 255u);
+        if (next < last) tile.load_keys(at(page1), g, G, next & 1u, key_at);
+
+        if (pos0 + kTile > least || bad) {
+            // some row does not see the whole tile.  Bits of its 32 positions; those of this lane are
+            // j and 16 + j, j < 4, of the bits from 4 (l/16) on
+            const uint32_t real = bad ? 0u : first_bits(u.s.kv, pos0), mine = real >> (g4 * 4);
+            uint32_t sees[RT];
 #pragma unroll
             for (int r = 0; r < RT; ++r) {
-                high[r] = fmaxf(fmaxf(fmaxf(x[r][0], x[r][1]), fmaxf(x[r][2], x[r][3])), fmaxf(fmaxf(x[r][4], x[r][5]), fmaxf(x[r][6], x[r][7])));
-                grows |= high[r] > m[r] + kLazy;
+                const uint32_t bits = p.tree ? (uint32_t)tree_bits(p.tree + tree[r], p.tree_words, (int64_t)pos0 - u.base) : first_bits(lim[r], pos0);
+                sees[r] = (bits & real) >> (g4 * 4);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    s[r][j >> 2][j & 3] = (sees[r] >> ((j >> 2) * 16 + (j & 3))) & 1u ? s[r][j >> 2][j & 3] : -INFINITY;
             }
-            if (__any(grows)) {
+            // values that do not exist become zeros, and so do rows that hold a NaN code,
+            // with a NaN score for who sees them: a weight of 0 does not hide a NaN
+            uint32_t nan = 0;
 #pragma unroll
-                for (int r = 0; r < RT; ++r) {
-                    high[r] = fmaxf(high[r], __shfl_xor(high[r], 16));
-                    high[r] = fmaxf(high[r], __shfl_xor(high[r], 32));
-                    const float to = high[r] > m[r] + kLazy ? high[r] : m[r], f = exp2f(m[r] - to);
-                    m[r] = to;
-                    l[r] *= f;
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t bit = 1u << ((j >> 2) * 16 + (j & 3));
 #pragma unroll
-                    for (int n = 0; n < NB; ++n) o[r][n] *= f;
+                for (int w = 0; w < D / 64; ++w) {
+                    tile.v[j][w] = mine & bit ? tile.v[j][w] : 0u;
+                    nan |= (((tile.v[j][w] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) ? bit : 0u;
                 }
             }
-            bf16x8 w[RT], low[RT];
+            if (__any(nan)) {
 #pragma unroll
-            for (int r = 0; r < RT; ++r) {
-                float sum = 0.f;
+                for (int d = 1; d < 16; d <<= 1) nan |= __shfl_xor(nan, d);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const float e = __builtin_amdgcn_exp2f(x[r][j] - m[r]);
-                    sum += e;
-                    w[r][j] = (__bf16)e;
-                    if constexpr (sizeof(E) == 2 && !__is_same(E, __bf16)) low[r][j] = (__bf16)(e - (float)w[r][j]);
+                    const uint32_t bit = 1u << ((j >> 2) * 16 + (j & 3));
+#pragma unroll
+                    for (int w = 0; w < D / 64; ++w) tile.v[j][w] = nan & bit ? 0u : tile.v[j][w];
+#pragma unroll
+                    for (int r = 0; r < RT; ++r) s[r][j >> 2][j & 3] = nan & sees[r] & bit ? NAN : s[r][j >> 2][j & 3];
                 }
-                l[r] += sum;
-            }
-            const float vs = cur.value_scale();
-#pragma unroll
-            for (int c = 0; c < D / 64; ++c) {
-                bf16x8 a[4];
-#pragma unroll
-                for (int j = 0; j < 8; j += 2) {
-                    const int lo = (int)__builtin_amdgcn_perm(cur.v[j + 1][c], cur.v[j][c], 0x05010400u);
-                    const int hi = (int)__builtin_amdgcn_perm(cur.v[j + 1][c], cur.v[j][c], 0x07030602u);
-                    const bf16x2 b0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, vs, false), b1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, vs, true);
-                    const bf16x2 b2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, vs, false), b3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, vs, true);
-                    a[0][j] = b0.x, a[0][j + 1] = b0.y, a[1][j] = b1.x, a[1][j + 1] = b1.y;
-                    a[2][j] = b2.x, a[2][j + 1] = b2.y, a[3][j] = b3.x, a[3][j + 1] = b3.y;
-                }
-#pragma unroll
-                for (int d = 0; d < 4; ++d)
-#pragma unroll
-                    for (int r = 0; r < RT; ++r) {
-                        o[r][4 * c + d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[d], w[r], o[r][4 * c + d], 0, 0, 0);
-                        if constexpr (!__is_same(E, __bf16))
-                            o[r][4 * c + d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[d], low[r], o[r][4 * c + d], 0, 0, 0);
-                    }
             }
         }
-        cur = next;
+        bool grows = false;
+        float high[RT];
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+            const float a = fmaxf(fmaxf(s[r][0][0], s[r][0][1]), s[r][0][2]), b = fmaxf(fmaxf(s[r][0][3], s[r][1][0]), s[r][1][1]);
+            high[r] = fmaxf(fmaxf(fmaxf(s[r][1][2], s[r][1][3]), a), b) * ks;
+            grows |= high[r] > m[r] + kLazy;
+        }
+        if (__any(grows)) {
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+                high[r] = fmaxf(high[r], __shfl_xor(high[r], 16));
+                high[r] = fmaxf(high[r], __shfl_xor(high[r], 32));
+                const float to = high[r] > m[r] + kLazy ? high[r] : m[r], f = __builtin_amdgcn_exp2f(m[r] - to);
+                m[r] = to;
+                l[r] *= f;
+#pragma unroll
+                for (int n = 0; n < NB; ++n) o[r][n] *= f;
+            }
+        }
+        bf16x8 w[RT], low[RT];
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+            float e[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                e[j] = __builtin_amdgcn_exp2f(fmaf(s[r][j >> 2][j & 3], ks, -m[r]));
+                w[r][j] = (__bf16)e[j];
+                if constexpr (!__is_same(E, __bf16)) low[r][j] = (__bf16)(e[j] - (float)w[r][j]);
+            }
+            l[r] += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+        }
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+            bf16x8 a[4];
+#pragma unroll
+            for (int j = 0; j < 8; j += 2) {
+                const int lo = (int)__builtin_amdgcn_perm(tile.v[j + 1][c], tile.v[j][c], 0x05010400u);
+                const int hi = (int)__builtin_amdgcn_perm(tile.v[j + 1][c], tile.v[j][c], 0x07030602u);
+                const bf16x2 b0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, vs, false), b1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, vs, true);
+                const bf16x2 b2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, vs, false), b3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, vs, true);
+                a[0][j] = b0.x, a[0][j + 1] = b0.y, a[1][j] = b1.x, a[1][j + 1] = b1.y;
+                a[2][j] = b2.x, a[2][j + 1] = b2.y, a[3][j] = b3.x, a[3][j + 1] = b3.y;
+            }
+#pragma unroll
+            for (int d = 0; d < 4; ++d)
+#pragma unroll
+                for (int r = 0; r < RT; ++r) {
+                    o[r][4 * c + d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[d], w[r], o[r][4 * c + d], 0, 0, 0);
+                    if constexpr (!__is_same(E, __bf16))
+                        o[r][4 * c + d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[d], low[r], o[r][4 * c + d], 0, 0, 0);
+                }
+        }
+        if (next < last) tile.load_values(at(page1), g, next & 1u, value_at);
         page = page1;
         page1 = page2;
-        t += kWaves;
+        t = next;
     }
 
     // the waves' parts, 16 rows at a time
     const uint32_t row = tid >> 4, seg = (tid & 15u) * NB;
+    if constexpr (Shared) __syncthreads();          // their queries' last reads
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
         if (u.row0 + r * 16 >= u.rows) break;
@@ -353,22 +412,22 @@ __global__ __launch_bounds__(kThreads, D * RT <= 128 ? 3 : (D * RT <= 256 ? 2 : 
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int n = 0; n < NB; ++n) obuf[wave][l16][(g4 * 4 + i) * NB + n] = o[r][n][i];
-        if (g4 == 0) ml[wave][l16][0] = m[r], ml[wave][l16][1] = l[r];
+            for (int n = 0; n < NB; ++n) lds.join.o[wave][l16][(g4 * 4 + i) * NB + n] = o[r][n][i];
+        if (g4 == 0) lds.join.ml[wave][l16][0] = m[r], lds.join.ml[wave][l16][1] = l[r];
         __syncthreads();
         const uint32_t mine = u.row0 + r * 16 + row;
-        if (mine < u.rows) {
-            float top = ml[0][row][0], sum = 0.f, acc[NB];
+        if (row < 16 && mine < u.rows) {
+            float top = lds.join.ml[0][row][0], sum = 0.f, acc[NB];
 #pragma unroll
-            for (uint32_t w = 1; w < kWaves; ++w) top = fmaxf(top, ml[w][row][0]);
+            for (uint32_t w = 1; w < W; ++w) top = fmaxf(top, lds.join.ml[w][row][0]);
 #pragma unroll
             for (int n = 0; n < NB; ++n) acc[n] = 0.f;
 #pragma unroll
-            for (uint32_t w = 0; w < kWaves; ++w) {
-                const float f = exp2f(ml[w][row][0] - top);
-                sum = fmaf(ml[w][row][1], f, sum);
+            for (uint32_t w = 0; w < W; ++w) {
+                const float f = exp2f(lds.join.ml[w][row][0] - top);
+                sum = fmaf(lds.join.ml[w][row][1], f, sum);
 #pragma unroll
-                for (int n = 0; n < NB; ++n) acc[n] = fmaf(obuf[w][row][seg + n], f, acc[n]);
+                for (int n = 0; n < NB; ++n) acc[n] = fmaf(lds.join.o[w][row][seg + n], f, acc[n]);
             }
             if (u.chunks > 1) {
                 const uint64_t slot = (((uint64_t)place * G + g) * p.chunks + cut) * R + r * 16 + row;
@@ -376,50 +435,63 @@ __global__ __launch_bounds__(kThreads, D * RT <= 128 ? 3 : (D * RT <= 256 ? 2 : 
                 for (int n = 0; n < NB; ++n) p.part[slot * D + seg + n] = acc[n];
                 if (seg == 0) p.part_ml[slot * 2] = top, p.part_ml[slot * 2 + 1] = sum;
             } else {
-                const uint32_t i = mine / p.group, h = g * p.group + mine - i * p.group;
-                E* dst = (E*)p.out + (int64_t)(u.s.q0 + i) * p.out_token + (int64_t)h * p.out_head + seg;
-                const float f = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
-                for (int n = 0; n < NB; ++n) dst[n] = (E)(acc[n] * f);
-                if (seg == 0 && p.lse) p.lse[(int64_t)(u.s.q0 + i) * p.lse_token + h] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+                put_row<E, D>(p, u, g, mine, seg, acc, top, sum);
             }
         }
         __syncthreads();
     }
 }
 
-// The parts of units that several blocks cut, joined in their order.
+// The parts of units that several blocks cut, joined in their order: 16 lanes a row,
+// which hold 16 cuts' maxima and sums at a time.
 template <class E, int D>
-__global__ __launch_bounds__(kThreads) void join_kernel(const HeadsAttendParams p, const Places places, uint32_t R) {
+__global__ __launch_bounds__(256) void join_kernel(const HeadsAttendParams p, const Places places, uint32_t R) {
     constexpr int NB = D / 16;
     const uint32_t G = p.heads.groups, g = blockIdx.x % G, place = blockIdx.x / G;
     const Unit u = unit_of(p, places, p.first + place, R);
     if (u.rows == 0 || u.chunks <= 1) return;
-    const uint32_t seg = (threadIdx.x & 15u) * NB;
+    const uint32_t l16 = threadIdx.x & 15u, seg = l16 * NB;
     for (uint32_t r = threadIdx.x >> 4; r < R && u.row0 + r < u.rows; r += 16) {
         const uint64_t slot = ((uint64_t)place * G + g) * p.chunks * R + r;
         float top = -FLT_MAX, sum = 0.f, acc[NB];
-        for (uint32_t c = 0; c < u.chunks; ++c) top = fmaxf(top, p.part_ml[(slot + (uint64_t)c * R) * 2]);
+        for (uint32_t c = l16; c < u.chunks; c += 16) top = fmaxf(top, p.part_ml[(slot + (uint64_t)c * R) * 2]);
+#pragma unroll
+        for (int d = 1; d < 16; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
 #pragma unroll
         for (int n = 0; n < NB; ++n) acc[n] = 0.f;
-        for (uint32_t c = 0; c < u.chunks; ++c) {
-            const uint64_t s = slot + (uint64_t)c * R;
-            const float f = exp2f(p.part_ml[s * 2] - top);
-            sum = fmaf(p.part_ml[s * 2 + 1], f, sum);
+        for (uint32_t c0 = 0; c0 < u.chunks; c0 += 16) {
+            float f = 0.f, part = 0.f;
+            if (c0 + l16 < u.chunks) {
+                const float2 ml = *(const float2*)(p.part_ml + (slot + (uint64_t)(c0 + l16) * R) * 2);
+                f = exp2f(ml.x - top);
+                part = ml.y * f;
+            }
+            const uint32_t many = u.chunks - c0 < 16 ? u.chunks - c0 : 16u;
+            for (uint32_t k = 0; k < many; k += 4) {
+                float x[4][NB], w[4];
 #pragma unroll
-            for (int n = 0; n < NB; ++n) acc[n] = fmaf(p.part[s * D + seg + n], f, acc[n]);
+                for (uint32_t i = 0; i < 4; ++i) {
+                    const uint32_t c = k + i < many ? k + i : many - 1;
+                    const float* from = p.part + (slot + (uint64_t)(c0 + c) * R) * D + seg;
+#pragma unroll
+                    for (int n = 0; n < NB; ++n) x[i][n] = from[n];
+                }
+#pragma unroll
+                for (uint32_t i = 0; i < 4; ++i) {
+                    if (k + i >= many) break;
+                    w[i] = __shfl(f, k + i, 16);
+                    sum += __shfl(part, k + i, 16);
+#pragma unroll
+                    for (int n = 0; n < NB; ++n) acc[n] = fmaf(x[i][n], w[i], acc[n]);
+                }
+            }
         }
-        const uint32_t mine = u.row0 + r, i = mine / p.group, h = g * p.group + mine - i * p.group;
-        E* dst = (E*)p.out + (int64_t)(u.s.q0 + i) * p.out_token + (int64_t)h * p.out_head + seg;
-        const float f = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
-        for (int n = 0; n < NB; ++n) dst[n] = (E)(acc[n] * f);
-        if (seg == 0 && p.lse) p.lse[(int64_t)(u.s.q0 + i) * p.lse_token + h] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+        put_row<E, D>(p, u, g, u.row0 + r, seg, acc, top, sum);
     }
 }
 
-// Blocks that a launch is cut for, by the rows of a unit: what the card holds at once, twice.
-uint64_t wanted_blocks(uint32_t rows) { return 32768 / rows; }
+// Blocks that a launch is cut for, by the rows of a unit.
+uint64_t wanted_blocks(uint32_t rows) { return 131072 / rows / (rows > 16 ? 2 : 1); }
 
 Places unit_places(uint32_t rows, uint32_t group, uint64_t num_seqs, uint64_t num_tokens, uint64_t max_q, uint64_t* total) {
     uint32_t shift = 0;
@@ -427,18 +499,18 @@ Places unit_places(uint32_t rows, uint32_t group, uint64_t num_seqs, uint64_t nu
     return places(group, shift, 1, (max_q * group + rows - 1) / rows, num_seqs, num_tokens, total);
 }
 
-template <class E, int D, int RT>
+template <class E, int D, int RT, int W>
 hipError_t launch(HeadsAttendParams p, const Places& w, hipStream_t stream) {
     const uint32_t G = p.heads.groups, total = p.units;
-    const uint32_t most = std::max<uint32_t>(1, ((1u << 24) - 1) / (G * p.chunks));     // a launch holds fewer than 2^32 threads
+    const uint32_t most = std::max<uint32_t>(1, ((1u << 22) - 1) / (G * p.chunks));     // a launch holds fewer than 2^32 threads
     for (uint64_t first = 0; first < total; first += most) {
         p.first = (uint32_t)first;
         p.units = (uint32_t)std::min<uint64_t>(most, total - first);
-        heads_attend_kernel<E, D, RT><<<p.units * G * p.chunks, kThreads, 0, stream>>>(p, w);
+        heads_attend_kernel<E, D, RT, W><<<p.units * G * p.chunks, W * 64, 0, stream>>>(p, w);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
         if (p.chunks > 1) {
-            join_kernel<E, D><<<p.units * G, kThreads, 0, stream>>>(p, w, 16 * RT);
+            join_kernel<E, D><<<p.units * G, 256, 0, stream>>>(p, w, 16 * RT);
             e = hipGetLastError();
             if (e != hipSuccess) return e;
         }
@@ -447,10 +519,11 @@ hipError_t launch(HeadsAttendParams p, const Places& w, hipStream_t stream) {
 }
 
 template <class E, int D>
-hipError_t launch(const HeadsAttendParams& p, const Places& w, uint32_t rows, hipStream_t stream) {
-    if (rows == 16) return launch<E, D, 1>(p, w, stream);
-    if (rows == 32 || D == 256) return launch<E, D, 2>(p, w, stream);
-    if constexpr (D < 256) return launch<E, D, 4>(p, w, stream);
+hipError_t launch(const HeadsAttendParams& p, const Places& w, const HeadsAttendPlan& plan, hipStream_t stream) {
+    if (plan.rows == 16 && plan.waves > 4) return launch<E, D, 1, kManyWaves<D>>(p, w, stream);
+    if (plan.rows == 16) return launch<E, D, 1, 4>(p, w, stream);
+    if (plan.rows == 32) return launch<E, D, 2, 4>(p, w, stream);
+    if constexpr (D < 256) return launch<E, D, 4, 4>(p, w, stream);
     return hipErrorInvalidValue;
 }
 
@@ -462,12 +535,16 @@ HeadsAttendPlan plan_heads_attend(const HeadsParams& h, uint32_t group, uint64_t
     const uint64_t rows = max_q * group;
     a.rows = rows <= 16 ? 16 : (rows <= 32 || h.dim == 256 ? 32 : 64);
     (void)unit_places(a.rows, group, num_seqs, num_tokens, max_q, &a.units);
-    const uint64_t most = std::max<uint64_t>(1, (max_kv + 127) / 128), blocks = a.units * h.groups;
-    const uint64_t cuts = std::max<uint64_t>(1, std::min(most, wanted_blocks(a.rows) / std::max<uint64_t>(1, blocks)));
-    a.chunk = (uint32_t)std::max<uint64_t>(128, ((max_kv + cuts - 1) / cuts + 127) / 128 * 128);
+    const uint64_t most = std::max<uint64_t>(1, (max_kv + kLeastChunk - 1) / kLeastChunk), blocks = a.units * h.groups;
+    // few units over short sequences: one block of many waves each, and no join
+    const uint64_t many = h.dim == 256 ? kManyWaves<256> : kManyWaves<128>;
+    const bool one = a.rows == 16 && blocks <= 256 && max_kv <= many * kTile * 4;
+    a.waves = one ? (uint32_t)many : 4;
+    const uint64_t cuts = one ? 1 : std::max<uint64_t>(1, std::min(most, wanted_blocks(a.rows) / std::max<uint64_t>(1, blocks)));
+    a.chunk = (uint32_t)std::max<uint64_t>(kLeastChunk, ((max_kv + cuts - 1) / cuts + 127) / 128 * 128);
     a.chunks = (uint32_t)std::max<uint64_t>(1, (max_kv + a.chunk - 1) / a.chunk);
     // parts of as many rows as the wanted blocks hold, or as the bounds allow: either grows with every bound
-    const uint64_t parts = std::min(wanted_blocks(a.rows) * a.rows, (num_tokens * group + num_seqs * a.rows) * h.groups * most);
+    const uint64_t parts = std::min<uint64_t>(wanted_blocks(16) * 16, (num_tokens * group + num_seqs * a.rows) * h.groups * most);
     a.bytes = parts * (h.dim + 2) * 4;
     return a;
 }
@@ -484,9 +561,9 @@ hipError_t launch_heads_attend(const HeadsAttendParams& p, void* workspace, hipS
     a.part = static_cast<float*>(workspace);
     a.part_ml = a.part + plan.bytes / 4 / (p.heads.dim + 2) * p.heads.dim;
     const bool half = p.type == KVPUB_FP16;
-    if (p.heads.dim == 64) return half ? launch<_Float16, 64>(a, w, plan.rows, stream) : launch<__bf16, 64>(a, w, plan.rows, stream);
-    if (p.heads.dim == 128) return half ? launch<_Float16, 128>(a, w, plan.rows, stream) : launch<__bf16, 128>(a, w, plan.rows, stream);
-    return half ? launch<_Float16, 256>(a, w, plan.rows, stream) : launch<__bf16, 256>(a, w, plan.rows, stream);
+    if (p.heads.dim == 64) return half ? launch<_Float16, 64>(a, w, plan, stream) : launch<__bf16, 64>(a, w, plan, stream);
+    if (p.heads.dim == 128) return half ? launch<_Float16, 128>(a, w, plan, stream) : launch<__bf16, 128>(a, w, plan, stream);
+    return half ? launch<_Float16, 256>(a, w, plan, stream) : launch<__bf16, 256>(a, w, plan, stream);
 }
 
 }  // namespace kvpub

@@ -301,6 +301,7 @@ struct HeadsAttendParams {
 // How a call is cut: query rows of a unit, positions of a cut, workspace.
 struct HeadsAttendPlan {
     uint32_t rows;
+    uint32_t waves;              // of a block
     uint32_t chunk;
     uint32_t chunks;
     uint64_t units;

@@ -31,35 +31,50 @@ struct Places {
 // tokens.  Every lane of the wave gets the same answer: 64 candidates a step, 3 steps for 65536.
 // q_start is taken as within the call's tokens; what is not ascending gives
 // places that are found wrong, never outside the arrays.
-__device__ __forceinline__ uint32_t first_token(const SeqParams& p, uint32_t b) {
-    if (!p.q_start) return b;
-    const int32_t q = p.q_start[b];
+__device__ __forceinline__ uint32_t within_tokens(const SeqParams& p, int32_t q) {
     return q < 0 ? 0u : ((uint32_t)q > p.num_tokens ? p.num_tokens : (uint32_t)q);
 }
 
+// A uniform load through the scalar cache, of what no kernel of the call writes: its
+// wait does not drain the vector loads in flight.
+template <class T> using kptr = const __attribute__((address_space(4))) T*;
+__device__ __forceinline__ int32_t uniform_load(const int32_t* p, uint64_t i) { return ((kptr<int32_t>)p)[i]; }
+
 __device__ __forceinline__ SeqOf find_sequence(const SeqParams& p, uint32_t place, const Places& w) {
-    const uint32_t lane = threadIdx.x & 63u;
-    uint32_t lo = 0, size = p.num_seqs;
+    uint32_t lo = 0;
     bool found = true;
-    while (size > 1) {
-        const uint32_t step = (size + 63) / 64, at = lo + lane * step;
-        const bool is = lane * step < size;
-        const uint64_t key = is ? w.key(first_token(p, at), at) : ~0ull;
-        const uint64_t below = __ballot(is && key <= place);
-        if (!below) { found = false; break; }
-        const uint32_t k = 63u - (uint32_t)__builtin_clzll(below);
-        const uint32_t end = lo + size;
-        lo += k * step;
-        size = step < end - lo ? step : end - lo;
+    if (w.num == 0) {                       // as many places for each sequence
+        lo = place / w.more;
+        found = lo < p.num_seqs;
+        lo = found ? lo : 0;
+    } else {
+        const uint32_t lane = threadIdx.x & 63u;
+        uint32_t size = p.num_seqs;
+        while (size > 1) {
+            const uint32_t step = (size + 63) / 64, at = lo + lane * step;
+            const bool is = lane * step < size;
+            const uint64_t key = is ? w.key(within_tokens(p, p.q_start[at]), at) : ~0ull;
+            const uint64_t below = __ballot(is && key <= place);
+            if (!below) { found = false; break; }
+            const uint32_t k = 63u - (uint32_t)__builtin_clzll(below);
+            const uint32_t end = lo + size;
+            lo += k * step;
+            size = step < end - lo ? step : end - lo;
+        }
     }
     SeqOf s;
     s.b = __builtin_amdgcn_readfirstlane(lo);
-    s.q0 = __builtin_amdgcn_readfirstlane(first_token(p, s.b));
-    const uint32_t q1 = p.q_start ? __builtin_amdgcn_readfirstlane(first_token(p, s.b + 1)) : s.b + 1;
-    s.n = q1 > s.q0 ? q1 - s.q0 : 0u;
+    const int32_t len = uniform_load(p.kv_len, s.b);
+    uint32_t end = s.b + 1;
+    s.q0 = s.b;
+    if (p.q_start) {
+        const int32_t q0 = uniform_load(p.q_start, s.b), q1 = uniform_load(p.q_start, s.b + 1);
+        s.q0 = within_tokens(p, q0);
+        end = within_tokens(p, q1);
+    }
+    s.n = end > s.q0 ? end - s.q0 : 0u;
     s.m = s.n < p.max_q ? s.n : p.max_q;
-    const int32_t kv = __builtin_amdgcn_readfirstlane(p.kv_len[s.b]);
-    s.kv = kv < 0 ? 0u : ((uint32_t)kv < p.max_kv ? (uint32_t)kv : p.max_kv);
+    s.kv = len < 0 ? 0u : ((uint32_t)len < p.max_kv ? (uint32_t)len : p.max_kv);
     const uint64_t key = w.key(s.q0, s.b);
     s.found = found && place >= key;
     s.place = (uint32_t)(place - key);
