@@ -36,8 +36,11 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
-template <int D> constexpr int kManyWaves = D == 256 ? 8 : 16;    // of a block that has a unit's positions to itself
-constexpr uint32_t kLeastChunk = 512;
+constexpr uint32_t kWaves = 4, kThreads = kWaves * 64;
+constexpr uint32_t kLeastChunk = 512;             // of a block, for up to kLeastChunk / kChunkRows rows
+constexpr uint32_t kChunkRows = 64;
+constexpr uint32_t kWanted = 4096, kWantedWide = 1024;       // blocks, of 16 rows and of more
+constexpr uint32_t kFull = 512;
 constexpr uint32_t kTile = 32;                    // positions of a wave's step
 constexpr float kLazy = 8.0f;                     // rescale when a maximum grows past 2^8
 constexpr float kLn2 = 0.693147180559945309f;
@@ -46,7 +49,7 @@ typedef __attribute__((address_space(1))) uint8_t gbyte;   // a byte in global m
 template <class T> using gptr = __attribute__((address_space(1))) T*;
 
 // Waves that a SIMD should hold: what the registers of the accumulators leave room for.
-constexpr int waves_a_simd(int D, int RT) { return RT * D <= 64 ? 5 : (RT * D <= 128 ? 4 : (RT * D <= 512 ? 2 : 1)); }
+constexpr int waves_a_simd(int D, int RT) { return RT * D <= 64 ? 5 : (RT * D <= 128 ? 3 : (RT * D <= 512 ? 2 : 1)); }
 
 template <class E> struct Operand;
 template <> struct Operand<__bf16> {
@@ -67,6 +70,10 @@ template <> struct Operand<_Float16> {
     }
     static __device__ __forceinline__ f32x4 mfma(x8 a, x8 b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
 };
+
+__device__ __forceinline__ uint32_t token_of(const HeadsAttendParams& p, uint32_t row) {
+    return (uint32_t)(((uint64_t)row * p.group_magic) >> p.group_shift);
+}
 
 // A unit of work and what its rows see.
 struct Unit {
@@ -89,24 +96,24 @@ __device__ __forceinline__ Unit unit_of(const HeadsAttendParams& p, const Places
     }
     u.base = (int64_t)u.s.kv - u.s.n;
     const uint32_t last = (u.row0 + R < u.rows ? u.row0 + R : u.rows) - 1;
-    const int64_t lim = u.base + last / p.group + 1;
+    const int64_t lim = u.base + token_of(p, last) + 1;
     u.reach = p.tree ? u.s.kv : (lim > 0 ? (uint32_t)lim : 0u);
     u.chunks = u.reach ? (u.reach + p.chunk - 1) / p.chunk : 1u;
     return u;
 }
 
-// A row's output from its joined parts, D/16 values a lane.
-template <class E, int D>
-__device__ __forceinline__ void put_row(const HeadsAttendParams& p, const Unit& u, uint32_t g, uint32_t row, uint32_t seg,
-                                        const float (&acc)[D / 16], float top, float sum) {
-    const uint32_t i = row / p.group, h = g * p.group + row - i * p.group;
+// A row's output from its joined parts, N values a lane.
+template <class E, int D, int N, class A>
+__device__ __forceinline__ void put_row(const HeadsAttendParams& p, const Unit& u, uint32_t g, uint32_t row, uint32_t seg, const A& acc,
+                                        float top, float sum) {
+    const uint32_t i = token_of(p, row), h = g * p.group + row - i * p.group;
     E* dst = (E*)p.out + (int64_t)(u.s.q0 + i) * p.out_token + (int64_t)h * p.out_head + seg;
     const float f = sum == 0.f ? 0.f : 1.f / sum;           // no position seen: 0
-    E y[D / 16];
+    E y[N];
 #pragma unroll
-    for (int n = 0; n < D / 16; ++n) y[n] = (E)(acc[n] * f);
-    __builtin_memcpy(__builtin_assume_aligned(dst, D / 8), y, sizeof y);
-    if (seg == 0 && p.lse) p.lse[(int64_t)(u.s.q0 + i) * p.lse_token + h] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+    for (int n = 0; n < N; ++n) y[n] = (E)(acc[n] * f);
+    __builtin_memcpy(__builtin_assume_aligned(dst, N * sizeof(E) < 16 ? N * sizeof(E) : 16), y, sizeof y);
+    if (seg == 0 && p.lse) p.lse[(int64_t)(u.s.q0 + i) * p.lse_token + h] = sum == 0.f ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * kLn2;
 }
 
 // 64 bits of a tree row from node j on (j below 0: the positions before the tree, seen by all).
@@ -187,20 +194,18 @@ struct Tile {
 };
 
 template <class E>
-__device__ __forceinline__ typename Operand<E>::x8 load_query(const E* src, bool is, bool negate) {
-    u32x4 w = {0, 0, 0, 0};
-    if (is) w = *(const u32x4*)src;
-    if (negate) w ^= 0x80008000u;
+__device__ __forceinline__ typename Operand<E>::x8 load_query(const E* src, uint32_t signs) {
+    const u32x4 w = *(const u32x4*)src ^ signs;
     return __builtin_bit_cast(typename Operand<E>::x8, w);
 }
 
-// W waves a block; Shared: the queries' operands stay in LDS (their registers would
-// cost the second wave a SIMD).
-template <class E, int D, int RT, int W>
-__global__ __launch_bounds__(W * 64, waves_a_simd(D, RT)) void heads_attend_kernel(const HeadsAttendParams p, const Places places) {
+// Shared: the queries' operands stay in LDS (their registers would cost the second
+// wave a SIMD).
+template <class E, int D, int RT>
+__global__ __launch_bounds__(kThreads, waves_a_simd(D, RT)) void heads_attend_kernel(const HeadsAttendParams p, const Places places) {
     typedef Operand<E> Op;
     constexpr uint32_t R = 16 * RT;
-    constexpr int NB = D / 16, NQ = D / 32;
+    constexpr int NB = D / 16, NQ = D / 32, W = kWaves;
     constexpr bool Shared = RT * D >= 512;
     struct Join {
         float o[W][16][D + 4];
@@ -214,7 +219,8 @@ __global__ __launch_bounds__(W * 64, waves_a_simd(D, RT)) void heads_attend_kern
     __shared__ Lds lds;
     const uint32_t G = p.heads.groups, tid = threadIdx.x, lane = tid & 63u, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const uint32_t l16 = lane & 15u, g4 = lane >> 4;
-    const uint32_t g = blockIdx.x % G, rest = blockIdx.x / G, cut = rest % p.chunks, place = rest / p.chunks;
+    // the longest first: a causal sequence's last rows
+    const uint32_t turn = blockIdx.x / G, g = blockIdx.x - turn * G, place = p.units - 1 - turn, cut = blockIdx.y;
     const Unit u = unit_of(p, places, p.first + place, R);
     if (u.rows == 0 || cut >= u.chunks) return;
 
@@ -235,7 +241,7 @@ __global__ __launch_bounds__(W * 64, waves_a_simd(D, RT)) void heads_attend_kern
 
     // queries, and what each row sees: positions below lim (tree: of those before the tree, then its bits)
     typename Op::x8 q[Shared ? 1 : RT][NQ];
-    const bool negate = p.scale_log2 < 0.f;
+    const uint32_t signs = p.scale_log2 < 0.f ? 0x80008000u : 0u;
     uint32_t lim[RT];
     uint32_t tree[RT];                     // first word of the row's bits
     uint32_t least = 0xFFFFFFFFu;          // positions that all rows see
@@ -243,13 +249,13 @@ __global__ __launch_bounds__(W * 64, waves_a_simd(D, RT)) void heads_attend_kern
     for (int r = 0; r < RT; ++r) {
         const uint32_t row = u.row0 + r * 16 + l16;
         const bool is = row < u.rows;
-        const uint32_t i = is ? row / p.group : 0u, h = g * p.group + (is ? row - i * p.group : 0u);
+        const uint32_t i = is ? token_of(p, row) : 0u, h = g * p.group + (is ? row - i * p.group : 0u);     // rows of none take the first's
         const E* src = (const E*)p.q + (int64_t)(u.s.q0 + i) * p.q_token + (int64_t)h * p.q_head + g4 * 16;
 #pragma unroll
         for (int c = 0; c < NQ; ++c) {
             const E* from = src + (c >> 1) * 64 + (c & 1) * 8;
-            if constexpr (!Shared) q[r][c] = load_query<E>(from, is, negate);
-            else if ((r * NQ + c) % W == (int)wave) lds.q[r * NQ + c][lane] = load_query<E>(from, is, negate);
+            if constexpr (!Shared) q[r][c] = load_query<E>(from, signs);
+            else if ((r * NQ + c) % W == (int)wave) lds.q[r * NQ + c][lane] = load_query<E>(from, signs);
         }
         const int64_t top = u.base + (p.tree ? 0 : (int64_t)i + 1);
         lim[r] = is ? (top > 0 ? (uint32_t)top : 0u) : 0xFFFFFFFFu;
@@ -416,7 +422,7 @@ __global__ __launch_bounds__(W * 64, waves_a_simd(D, RT)) void heads_attend_kern
         if (g4 == 0) lds.join.ml[wave][l16][0] = m[r], lds.join.ml[wave][l16][1] = l[r];
         __syncthreads();
         const uint32_t mine = u.row0 + r * 16 + row;
-        if (row < 16 && mine < u.rows) {
+        if (mine < u.rows) {
             float top = lds.join.ml[0][row][0], sum = 0.f, acc[NB];
 #pragma unroll
             for (uint32_t w = 1; w < W; ++w) top = fmaxf(top, lds.join.ml[w][row][0]);
@@ -424,7 +430,7 @@ __global__ __launch_bounds__(W * 64, waves_a_simd(D, RT)) void heads_attend_kern
             for (int n = 0; n < NB; ++n) acc[n] = 0.f;
 #pragma unroll
             for (uint32_t w = 0; w < W; ++w) {
-                const float f = exp2f(lds.join.ml[w][row][0] - top);
+                const float f = __builtin_amdgcn_exp2f(lds.join.ml[w][row][0] - top);
                 sum = fmaf(lds.join.ml[w][row][1], f, sum);
 #pragma unroll
                 for (int n = 0; n < NB; ++n) acc[n] = fmaf(lds.join.o[w][row][seg + n], f, acc[n]);
@@ -435,63 +441,56 @@ __global__ __launch_bounds__(W * 64, waves_a_simd(D, RT)) void heads_attend_kern
                 for (int n = 0; n < NB; ++n) p.part[slot * D + seg + n] = acc[n];
                 if (seg == 0) p.part_ml[slot * 2] = top, p.part_ml[slot * 2 + 1] = sum;
             } else {
-                put_row<E, D>(p, u, g, mine, seg, acc, top, sum);
+                put_row<E, D, NB>(p, u, g, mine, seg, acc, top, sum);
             }
         }
         __syncthreads();
     }
 }
 
-// The parts of units that several blocks cut, joined in their order: 16 lanes a row,
-// which hold 16 cuts' maxima and sums at a time.
+// The parts of units that several blocks cut, joined in their order: D/4 lanes a row,
+// 16 cuts' parts on the way at a time, each 16 lanes with those cuts' maxima and sums.
 template <class E, int D>
 __global__ __launch_bounds__(256) void join_kernel(const HeadsAttendParams p, const Places places, uint32_t R) {
-    constexpr int NB = D / 16;
-    const uint32_t G = p.heads.groups, g = blockIdx.x % G, place = blockIdx.x / G;
+    constexpr uint32_t kLanes = D / 4, kRows = 256 / kLanes;
+    const uint32_t G = p.heads.groups, place = blockIdx.x / G, g = blockIdx.x - place * G;
     const Unit u = unit_of(p, places, p.first + place, R);
     if (u.rows == 0 || u.chunks <= 1) return;
-    const uint32_t l16 = threadIdx.x & 15u, seg = l16 * NB;
-    for (uint32_t r = threadIdx.x >> 4; r < R && u.row0 + r < u.rows; r += 16) {
+    const uint32_t l16 = threadIdx.x & 15u, lane = threadIdx.x % kLanes;
+    const uint32_t rows = u.rows - u.row0 < R ? u.rows - u.row0 : R;
+    for (uint32_t r = threadIdx.x / kLanes; r < rows; r += kRows) {
         const uint64_t slot = ((uint64_t)place * G + g) * p.chunks * R + r;
-        float top = -FLT_MAX, sum = 0.f, acc[NB];
-        for (uint32_t c = l16; c < u.chunks; c += 16) top = fmaxf(top, p.part_ml[(slot + (uint64_t)c * R) * 2]);
-#pragma unroll
-        for (int d = 1; d < 16; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
-#pragma unroll
-        for (int n = 0; n < NB; ++n) acc[n] = 0.f;
+        float top = -FLT_MAX, sum = 0.f;
+        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
         for (uint32_t c0 = 0; c0 < u.chunks; c0 += 16) {
-            float f = 0.f, part = 0.f;
-            if (c0 + l16 < u.chunks) {
-                const float2 ml = *(const float2*)(p.part_ml + (slot + (uint64_t)(c0 + l16) * R) * 2);
-                f = exp2f(ml.x - top);
-                part = ml.y * f;
-            }
             const uint32_t many = u.chunks - c0 < 16 ? u.chunks - c0 : 16u;
-            for (uint32_t k = 0; k < many; k += 4) {
-                float x[4][NB], w[4];
+            f32x4 x[16];
 #pragma unroll
-                for (uint32_t i = 0; i < 4; ++i) {
-                    const uint32_t c = k + i < many ? k + i : many - 1;
-                    const float* from = p.part + (slot + (uint64_t)(c0 + c) * R) * D + seg;
-#pragma unroll
-                    for (int n = 0; n < NB; ++n) x[i][n] = from[n];
-                }
-#pragma unroll
-                for (uint32_t i = 0; i < 4; ++i) {
-                    if (k + i >= many) break;
-                    w[i] = __shfl(f, k + i, 16);
-                    sum += __shfl(part, k + i, 16);
-#pragma unroll
-                    for (int n = 0; n < NB; ++n) acc[n] = fmaf(x[i][n], w[i], acc[n]);
-                }
+            for (uint32_t i = 0; i < 16; ++i)
+                if (i < many) x[i] = *(const f32x4*)(p.part + (slot + (uint64_t)(c0 + i) * R) * D + lane * 4);
+            float m = -FLT_MAX, l = 0.f;
+            if (l16 < many) {
+                const float2 ml = *(const float2*)(p.part_ml + (slot + (uint64_t)(c0 + l16) * R) * 2);
+                m = ml.x, l = ml.y;
             }
+            float high = fmaxf(top, m);
+#pragma unroll
+            for (int d = 1; d < 16; d <<= 1) high = fmaxf(high, __shfl_xor(high, d));
+            const float old = __builtin_amdgcn_exp2f(top - high), f = __builtin_amdgcn_exp2f(m - high);
+            top = high;
+            sum *= old;
+            acc *= old;
+            l *= f;
+#pragma unroll
+            for (int d = 1; d < 16; d <<= 1) l += __shfl_xor(l, d);
+            sum += l;
+#pragma unroll
+            for (uint32_t i = 0; i < 16; ++i)
+                if (i < many) acc += x[i] * __shfl(f, i, 16);
         }
-        put_row<E, D>(p, u, g, u.row0 + r, seg, acc, top, sum);
+        put_row<E, D, 4>(p, u, g, u.row0 + r, lane * 4, acc, top, sum);
     }
 }
-
-// Blocks that a launch is cut for, by the rows of a unit.
-uint64_t wanted_blocks(uint32_t rows) { return 131072 / rows / (rows > 16 ? 2 : 1); }
 
 Places unit_places(uint32_t rows, uint32_t group, uint64_t num_seqs, uint64_t num_tokens, uint64_t max_q, uint64_t* total) {
     uint32_t shift = 0;
@@ -499,14 +498,14 @@ Places unit_places(uint32_t rows, uint32_t group, uint64_t num_seqs, uint64_t nu
     return places(group, shift, 1, (max_q * group + rows - 1) / rows, num_seqs, num_tokens, total);
 }
 
-template <class E, int D, int RT, int W>
+template <class E, int D, int RT>
 hipError_t launch(HeadsAttendParams p, const Places& w, hipStream_t stream) {
     const uint32_t G = p.heads.groups, total = p.units;
-    const uint32_t most = std::max<uint32_t>(1, ((1u << 22) - 1) / (G * p.chunks));     // a launch holds fewer than 2^32 threads
+    const uint32_t most = std::max<uint32_t>(1, ((1u << 24) - 1) / (G * p.chunks));     // a launch holds fewer than 2^32 threads
     for (uint64_t first = 0; first < total; first += most) {
         p.first = (uint32_t)first;
         p.units = (uint32_t)std::min<uint64_t>(most, total - first);
-        heads_attend_kernel<E, D, RT, W><<<p.units * G * p.chunks, W * 64, 0, stream>>>(p, w);
+        heads_attend_kernel<E, D, RT><<<dim3(p.units * G, p.chunks), kThreads, 0, stream>>>(p, w);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
         if (p.chunks > 1) {
@@ -520,10 +519,9 @@ hipError_t launch(HeadsAttendParams p, const Places& w, hipStream_t stream) {
 
 template <class E, int D>
 hipError_t launch(const HeadsAttendParams& p, const Places& w, const HeadsAttendPlan& plan, hipStream_t stream) {
-    if (plan.rows == 16 && plan.waves > 4) return launch<E, D, 1, kManyWaves<D>>(p, w, stream);
-    if (plan.rows == 16) return launch<E, D, 1, 4>(p, w, stream);
-    if (plan.rows == 32) return launch<E, D, 2, 4>(p, w, stream);
-    if constexpr (D < 256) return launch<E, D, 4, 4>(p, w, stream);
+    if (plan.rows == 16) return launch<E, D, 1>(p, w, stream);
+    if (plan.rows == 32) return launch<E, D, 2>(p, w, stream);
+    if constexpr (D < 256) return launch<E, D, 4>(p, w, stream);
     return hipErrorInvalidValue;
 }
 
@@ -534,17 +532,18 @@ HeadsAttendPlan plan_heads_attend(const HeadsParams& h, uint32_t group, uint64_t
     HeadsAttendPlan a;
     const uint64_t rows = max_q * group;
     a.rows = rows <= 16 ? 16 : (rows <= 32 || h.dim == 256 ? 32 : 64);
+    if (a.rows == 64) {
+        (void)unit_places(64, group, num_seqs, num_tokens, max_q, &a.units);
+        if (a.units * h.groups < kFull) a.rows = 32;
+    }
     (void)unit_places(a.rows, group, num_seqs, num_tokens, max_q, &a.units);
-    const uint64_t most = std::max<uint64_t>(1, (max_kv + kLeastChunk - 1) / kLeastChunk), blocks = a.units * h.groups;
-    // few units over short sequences: one block of many waves each, and no join
-    const uint64_t many = h.dim == 256 ? kManyWaves<256> : kManyWaves<128>;
-    const bool one = a.rows == 16 && blocks <= 256 && max_kv <= many * kTile * 4;
-    a.waves = one ? (uint32_t)many : 4;
-    const uint64_t cuts = one ? 1 : std::max<uint64_t>(1, std::min(most, wanted_blocks(a.rows) / std::max<uint64_t>(1, blocks)));
-    a.chunk = (uint32_t)std::max<uint64_t>(kLeastChunk, ((max_kv + cuts - 1) / cuts + 127) / 128 * 128);
+    const uint64_t least = std::max<uint64_t>(kLeastChunk, std::min<uint64_t>(rows, a.rows) * kChunkRows), blocks = a.units * h.groups;
+    const uint64_t most = std::max<uint64_t>(1, (max_kv + least - 1) / least);
+    const uint64_t cuts = std::max<uint64_t>(1, std::min(most, (a.rows == 16 ? kWanted : kWantedWide) / std::max<uint64_t>(1, blocks)));
+    a.chunk = (uint32_t)std::max<uint64_t>(least, ((max_kv + cuts - 1) / cuts + 127) / 128 * 128);
     a.chunks = (uint32_t)std::max<uint64_t>(1, (max_kv + a.chunk - 1) / a.chunk);
-    // parts of as many rows as the wanted blocks hold, or as the bounds allow: either grows with every bound
-    const uint64_t parts = std::min<uint64_t>(wanted_blocks(16) * 16, (num_tokens * group + num_seqs * a.rows) * h.groups * most);
+    // parts of as many rows as the bounds allow, which grows with each of them; the rows of a unit that none has count too
+    const uint64_t parts = std::min<uint64_t>(kWanted * 64, (num_tokens * group + num_seqs * 64) * h.groups * std::max<uint64_t>(1, (max_kv + kLeastChunk - 1) / kLeastChunk));
     a.bytes = parts * (h.dim + 2) * 4;
     return a;
 }
@@ -558,6 +557,11 @@ hipError_t launch_heads_attend(const HeadsAttendParams& p, void* workspace, hipS
     uint64_t total;
     const Places w = unit_places(plan.rows, p.group, p.seqs.num_seqs, p.seqs.num_tokens, p.seqs.max_q, &total);
     a.units = (uint32_t)total;
+    // ceil(2^(31 + s) / group), 2^s >= group: exact for rows below 2^31
+    uint32_t shift = 0;
+    while ((1u << shift) < p.group) ++shift;
+    a.group_shift = 31 + shift;
+    a.group_magic = (uint32_t)(((1ull << a.group_shift) + p.group - 1) / p.group);
     a.part = static_cast<float*>(workspace);
     a.part_ml = a.part + plan.bytes / 4 / (p.heads.dim + 2) * p.heads.dim;
     const bool half = p.type == KVPUB_FP16;

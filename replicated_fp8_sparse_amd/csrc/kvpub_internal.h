@@ -282,6 +282,8 @@ struct HeadsAttendParams {
     const uint8_t* base;         // the replica, already offset to the layer
     uint32_t type;
     uint32_t group;              // query heads of a key-value head
+    uint32_t group_magic;        // row / group = row * group_magic / 2^group_shift below 2^31 rows
+    uint32_t group_shift;
     const uint16_t* q;
     uint16_t* out;
     int64_t q_token, q_head, out_token, out_head, lse_token;
@@ -301,7 +303,6 @@ struct HeadsAttendParams {
 // How a call is cut: query rows of a unit, positions of a cut, workspace.
 struct HeadsAttendPlan {
     uint32_t rows;
-    uint32_t waves;              // of a block
     uint32_t chunk;
     uint32_t chunks;
     uint64_t units;
