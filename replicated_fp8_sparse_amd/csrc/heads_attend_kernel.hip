@@ -39,8 +39,9 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 constexpr uint32_t kWaves = 4, kThreads = kWaves * 64;
 constexpr uint32_t kLeastChunk = 512;             // of a block, for up to kLeastChunk / kChunkRows rows
 constexpr uint32_t kChunkRows = 64;
+constexpr uint32_t kWhole = 768, kMostChunks = 64;
 constexpr uint32_t kWanted = 4096, kWantedWide = 1024;       // blocks, of 16 rows and of more
-constexpr uint32_t kFull = 512;
+constexpr uint32_t kFull = 1024;
 constexpr uint32_t kTile = 32;                    // positions of a wave's step
 constexpr float kLazy = 8.0f;                     // rescale when a maximum grows past 2^8
 constexpr float kLn2 = 0.693147180559945309f;
@@ -290,22 +291,34 @@ __global__ __launch_bounds__(kThreads, waves_a_simd(D, RT)) void heads_attend_ke
         f32x4 s[RT][2];
 #pragma unroll
         for (int r = 0; r < RT; ++r) s[r][0] = s[r][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+        typename Op::x8 b[RT];
+        if constexpr (Shared) {
 #pragma unroll
-        for (int c = 0; c < D / 64; ++c)
+            for (int r = 0; r < RT; ++r) b[r] = lds.q[r * NQ][lane];
+        }
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                typename Op::x8 a[2];
+        for (int c = 0; c < NQ; ++c) {
+            // queries from LDS are read a step ahead
+            typename Op::x8 a[2], ahead[RT];
+            if constexpr (Shared) {
 #pragma unroll
-                for (int j = 0; j < 2; ++j) a[j] = Op::widen(tile.k[j][c][2 * h], tile.k[j][c][2 * h + 1]);
-#pragma unroll
-                for (int r = 0; r < RT; ++r) {
-                    typename Op::x8 b;
-                    if constexpr (Shared) b = lds.q[r * NQ + 2 * c + h][lane];
-                    else b = q[r][2 * c + h];
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) s[r][j] = Op::mfma(a[j], b, s[r][j]);
-                }
+                for (int r = 0; r < RT; ++r) ahead[r] = lds.q[r * NQ + (c + 1 < NQ ? c + 1 : c)][lane];
             }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) a[j] = Op::widen(tile.k[j][c >> 1][2 * (c & 1)], tile.k[j][c >> 1][2 * (c & 1) + 1]);
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    if constexpr (Shared) s[r][j] = Op::mfma(a[j], b[r], s[r][j]);
+                    else s[r][j] = Op::mfma(a[j], q[r][c], s[r][j]);
+                }
+            if constexpr (Shared) {
+#pragma unroll
+                for (int r = 0; r < RT; ++r) b[r] = ahead[r];
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
         // the scale of a score in powers of 2 is kept above 0 and below infinity, so that a hidden score stays -infinity
         const float ks = fminf(fmaxf(fabsf(p.scale_log2) * power(tile.scales & 255u), FLT_MIN), FLT_MAX), vs = power((tile.scales >> 8) & 255u);
         if (next < last) tile.load_keys(at(page1), g, G, next & 1u, key_at);
@@ -538,12 +551,12 @@ HeadsAttendPlan plan_heads_attend(const HeadsParams& h, uint32_t group, uint64_t
     }
     (void)unit_places(a.rows, group, num_seqs, num_tokens, max_q, &a.units);
     const uint64_t least = std::max<uint64_t>(kLeastChunk, std::min<uint64_t>(rows, a.rows) * kChunkRows), blocks = a.units * h.groups;
-    const uint64_t most = std::max<uint64_t>(1, (max_kv + least - 1) / least);
+    const uint64_t most = max_kv <= kWhole ? 1 : std::min<uint64_t>(kMostChunks, (max_kv + least - 1) / least);
     const uint64_t cuts = std::max<uint64_t>(1, std::min(most, (a.rows == 16 ? kWanted : kWantedWide) / std::max<uint64_t>(1, blocks)));
     a.chunk = (uint32_t)std::max<uint64_t>(least, ((max_kv + cuts - 1) / cuts + 127) / 128 * 128);
     a.chunks = (uint32_t)std::max<uint64_t>(1, (max_kv + a.chunk - 1) / a.chunk);
     // parts of as many rows as the bounds allow, which grows with each of them; the rows of a unit that none has count too
-    const uint64_t parts = std::min<uint64_t>(kWanted * 64, (num_tokens * group + num_seqs * 64) * h.groups * std::max<uint64_t>(1, (max_kv + kLeastChunk - 1) / kLeastChunk));
+    const uint64_t parts = std::min<uint64_t>(kWanted * 16, (num_tokens * group + num_seqs * 64) * h.groups * std::min<uint64_t>(kMostChunks, (max_kv + kLeastChunk - 1) / kLeastChunk + 1));
     a.bytes = parts * (h.dim + 2) * 4;
     return a;
 }
