@@ -4,8 +4,7 @@
 // An angle is position * turns modulo 2^64 in units of 2^-64 turns, where turns is
 // the pair's frequency: one 64-bit product, exact, so a position of a million is
 // as good as the first (in binary32 the angle itself would be off by 0.03).  Its
-// high 32 bits, rounded, are the nearest quarter turn and a signed rest of at most
-// an eighth; sine and cosine of the rest are Taylor's polynomials in Horner's form,
+// high 32 bits are the nearest quarter turn and a signed rest of at most an eighth; sine and cosine of the rest are Taylor's polynomials in Horner's form,
 // up to x^9 and x^10: what is cut off stays below 2^-29.
 #pragma once
 
@@ -19,8 +18,9 @@ struct Turn {
 };
 
 __device__ __forceinline__ Turn turn_of(int32_t position, uint64_t turns) {
-    const uint64_t a = (uint64_t)(int64_t)position * turns;
-    const uint32_t u = (uint32_t)((a + (1ull << 31)) >> 32);
+    // the product's high word: two 32-bit products, and the sign's part of the low one
+    const uint32_t lo = (uint32_t)turns, hi = (uint32_t)(turns >> 32);
+    const uint32_t u = __umulhi((uint32_t)position, lo) + (uint32_t)position * hi - (position < 0 ? lo : 0u);
     const uint32_t quarter = (u + (1u << 29)) >> 30;
     const int32_t rest = (int32_t)(u - (quarter << 30));              // -2^29 .. 2^29 - 1
     const float x = (float)rest * 1.46291807926715968e-09f;           // 2 pi / 2^32
@@ -39,38 +39,70 @@ __device__ __forceinline__ Turn turn_of(int32_t position, uint64_t turns) {
 __device__ __forceinline__ float turned_first(float u, float v, float c, float s) { return fmaf(u, c, -(v * s)); }
 __device__ __forceinline__ float turned_second(float u, float v, float c, float s) { return fmaf(u, s, v * c); }
 
-// x, the values e0 .. e0+7 of `row` (e0 a multiple of 8), rotated where the
-// rotation covers them.  Halves: a value's partner lies half the rotated part away
-// and is read from the row again.
-template <class T>
-__device__ __forceinline__ void rotate8(float (&x)[8], const T* row, uint32_t e0, int32_t position, const RotationParams& r) {
+// Eight values of a row that one lane takes: two groups of 4, which are 4 pairs
+// where the rotation covers them.  Units below dim/8 are its pairs in order (neighbours:
+// 8 values in a row; halves: 4 of each half), the others what lies around them.
+struct RowUnit {
+    uint32_t at0, at1;       // first values of the groups
+    bool turned;
+};
+__device__ __forceinline__ RowUnit row_unit(uint32_t unit, uint32_t dim, uint32_t start, bool halves) {
+    RowUnit u;
+    u.turned = unit < dim / 8;
+    if (!u.turned) {
+        u.at0 = (unit - dim / 8) * 8;
+        if (u.at0 >= start) u.at0 += dim;
+        u.at1 = u.at0 + 4;
+    } else {
+        u.at0 = start + unit * (halves ? 4 : 8);
+        u.at1 = u.at0 + (halves ? dim / 2 : 4);
+    }
+    return u;
+}
+
+// The frequencies of a unit's pairs, the sines and cosines at a position, and the pairs turned.
+struct Turns4 {
+    uint64_t f[4];
+    __device__ __forceinline__ void load(const uint64_t* turns, uint32_t unit, bool turned) {
 #pragma unroll
-    for (uint32_t g = 0; g < 2; ++g) {
-        const uint32_t rel = e0 + 4 * g - r.start;
-        if (rel >= r.dim) continue;                       // also where e0 + 4 g < start
-        if (r.halves) {
-            const uint32_t half = r.dim / 2;
-            const bool second = rel >= half;
-            const uint32_t pair = second ? rel - half : rel;
-            const T* other = row + r.start + (second ? pair : pair + half);
-            T w[4];
-            __builtin_memcpy(w, __builtin_assume_aligned(other, 4 * sizeof(T)), sizeof w);
+        for (int i = 0; i < 4; ++i) f[i] = turned ? turns[unit * 4 + i] : 0;
+    }
+};
+struct Angles4 {
+    float c[4], s[4];
+    __device__ __forceinline__ void set(int32_t position, const Turns4& t, float magnitude, float sign) {
 #pragma unroll
-            for (uint32_t i = 0; i < 4; ++i) {
-                const Turn t = turn_of(position, r.turns[pair + i]);
-                const float c = t.c * r.magnitude, s = t.s * r.magnitude, o = (float)w[i], m = x[4 * g + i];
-                x[4 * g + i] = second ? turned_second(o, m, c, s) : turned_first(m, o, c, s);
+        for (int i = 0; i < 4; ++i) {
+            const Turn w = turn_of(position, t.f[i]);
+            c[i] = w.c * magnitude;
+            s[i] = w.s * sign;
+        }
+    }
+    // x: the unit's first group, then the second
+    __device__ __forceinline__ void turn(float (&x)[8], bool halves) const {
+        float y[8];
+        if (halves) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                y[i] = turned_first(x[i], x[4 + i], c[i], s[i]);
+                y[4 + i] = turned_second(x[i], x[4 + i], c[i], s[i]);
             }
         } else {
 #pragma unroll
-            for (uint32_t i = 0; i < 2; ++i) {
-                const Turn t = turn_of(position, r.turns[rel / 2 + i]);
-                const float c = t.c * r.magnitude, s = t.s * r.magnitude, u = x[4 * g + 2 * i], v = x[4 * g + 2 * i + 1];
-                x[4 * g + 2 * i] = turned_first(u, v, c, s);
-                x[4 * g + 2 * i + 1] = turned_second(u, v, c, s);
+            for (int i = 0; i < 4; ++i) {
+                y[2 * i] = turned_first(x[2 * i], x[2 * i + 1], c[i], s[i]);
+                y[2 * i + 1] = turned_second(x[2 * i], x[2 * i + 1], c[i], s[i]);
             }
         }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = y[i];
     }
-}
+};
+
+// Four values of a row.
+template <class T>
+struct alignas(4 * sizeof(T)) Row4 {
+    T v[4];
+};
 
 }  // namespace kvpub

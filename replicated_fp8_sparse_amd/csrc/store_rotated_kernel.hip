@@ -73,7 +73,14 @@ __global__ __launch_bounds__(kWaves * 64) void store_rotated_kernel(const StoreR
     }
     const uint16_t* irow = p.s.indexer + (uint64_t)ti * p.s.indexer_stride;
     const uint16_t* rrow = p.s.rope + (uint64_t)tr * p.s.rope_stride;
-    const u32x4 ix = *(const u32x4*)(irow + in * 8), rp = *(const u32x4*)(rrow + (lane & 7u) * 8);
+    // what the lane takes of the rows that turn: 4 pairs (rotation.h)
+    const RowUnit ui = row_unit(in, p.indexer.dim, p.indexer.start, p.indexer.halves), ur = row_unit(lane & 7u, p.rope.dim, p.rope.start, p.rope.halves);
+    const Row4<__bf16> i0 = *(const Row4<__bf16>*)(irow + ui.at0), i1 = *(const Row4<__bf16>*)(irow + ui.at1);
+    const Row4<__bf16> p0 = *(const Row4<__bf16>*)(rrow + ur.at0), p1 = *(const Row4<__bf16>*)(rrow + ur.at1);
+    Turns4 ti4, tr4;
+    ti4.load(p.indexer.turns, in, ui.turned);
+    tr4.load(p.rope.turns, lane & 7u, ur.turned);
+    const int32_t pos_i = p.positions[ti], pos_r = p.positions[tr];
     uint32_t bad = 0;
     bool ok[4];
 #pragma unroll
@@ -91,19 +98,22 @@ __global__ __launch_bounds__(kWaves * 64) void store_rotated_kernel(const StoreR
         unpack8(lat[k], x);
         code[k] = quantize(x, scale[k]);
     }
-    float x[8];
-    unpack8(ix, x);
-    if (p.indexer.dim) rotate8(x, (const __bf16*)irow, in * 8, p.positions[ti], p.indexer);
-    code[4] = quantize(x, scale[4]);
-    u32x4 rope = rp;
-    if (p.rope.dim) {
-        unpack8(rp, x);
-        rotate8(x, (const __bf16*)rrow, (lane & 7u) * 8, p.positions[tr], p.rope);
-        __bf16 y[8];
+    float x[8], y[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = (__bf16)x[i];
-        __builtin_memcpy(&rope, y, sizeof rope);
+    for (int i = 0; i < 4; ++i) x[i] = (float)i0.v[i], x[4 + i] = (float)i1.v[i], y[i] = (float)p0.v[i], y[4 + i] = (float)p1.v[i];
+    Angles4 angles;
+    if (ui.turned) {
+        angles.set(pos_i, ti4, p.indexer.magnitude, p.indexer.magnitude);
+        angles.turn(x, p.indexer.halves);
     }
+    code[4] = quantize(x, scale[4]);
+    if (ur.turned) {
+        angles.set(pos_r, tr4, p.rope.magnitude, p.rope.magnitude);
+        angles.turn(y, p.rope.halves);
+    }
+    Row4<__bf16> r0, r1;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r0.v[i] = (__bf16)y[i], r1.v[i] = (__bf16)y[4 + i];
 
     uint64_t main_at[4], idx_at[4];
 #pragma unroll
@@ -127,9 +137,13 @@ __global__ __launch_bounds__(kWaves * 64) void store_rotated_kernel(const StoreR
                 *(u32x2*)(main + main_at[k] + lane * 8) = code[k];
                 if (in == 0) *(float*)(main + main_at[k] + 512 + row * 4) = scale[k];
             }
-        if (ok_r) *(u32x4*)(main + ri + 528 + (lane & 7u) * 16) = rope;
+        if (ok_r) {
+            *(Row4<__bf16>*)(main + ri + 528 + ur.at0 * 2) = r0;
+            *(Row4<__bf16>*)(main + ri + 528 + ur.at1 * 2) = r1;
+        }
         if (ok_i) {
-            *(u32x2*)(idx + ii + in * 8) = code[4];
+            *(uint32_t*)(idx + ii + ui.at0) = code[4].x;
+            *(uint32_t*)(idx + ii + ui.at1) = code[4].y;
             if (in == 0) *(float*)(idx + ii + 8192 + si * 4 - si * 128) = scale[4];
         }
     }
