@@ -19,7 +19,8 @@
 namespace kvpub {
 namespace {
 
-constexpr uint32_t kThreads = 512;                // half of them for the keys, half for the values
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
 
 // Largest finite magnitude of x and m.
 __device__ __forceinline__ float amax8(const float (&x)[8], float m) {
@@ -51,13 +52,15 @@ __device__ __forceinline__ uint32_t recode4(uint32_t old, float factor) {
     return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(b[0] * factor, b[1] * factor, w, true);
 }
 
-template <class T, uint32_t D>
-__global__ __launch_bounds__(kThreads) void heads_append_kernel(const HeadsAppendParams p, const Places places) {
-    constexpr uint32_t kLanes = D / 8, kRows = kThreads / 2 / kLanes, kRounds = 64 / kRows;
-    __shared__ float top[kThreads / 64];
+// N threads, half of them for the keys, half for the values; Rounds: of rows that they pass,
+// enough for the new ones.
+template <class T, uint32_t D, uint32_t N, uint32_t Rounds>
+__global__ __launch_bounds__(N) void heads_append_kernel(const HeadsAppendParams p, const Places places) {
+    constexpr uint32_t kLanes = D / 8, kRows = N / 2 / kLanes, kHalfWaves = N / 128;
+    __shared__ float top[2][kHalfWaves];
     __shared__ int had[2];
-    const uint32_t G = p.heads.groups, tid = threadIdx.x & (kThreads / 2 - 1);
-    const uint32_t value = __builtin_amdgcn_readfirstlane(threadIdx.x / (kThreads / 2));       // 0: keys, 1: values
+    const uint32_t G = p.heads.groups, tid = threadIdx.x & (N / 2 - 1);
+    const uint32_t value = __builtin_amdgcn_readfirstlane(threadIdx.x / (N / 2));       // 0: keys, 1: values
     const uint32_t turn = blockIdx.x / G, g = blockIdx.x - turn * G;
     const SeqOf s = find_sequence(p.seqs, p.first + turn, places);
     // positions [begin, end) are stored; base may be negative
@@ -75,11 +78,11 @@ __global__ __launch_bounds__(kThreads) void heads_append_kernel(const HeadsAppen
     const int64_t token = value ? p.v_token : p.k_token;
     Turns4 turns;
     turns.load(p.rotation.turns, lane, u.turned);
-    float x[kRounds][8], m = 0.f;
+    float x[Rounds][8], m = 0.f;
 #pragma unroll
-    for (uint32_t i = 0; i < kRounds; ++i) {
-        const uint32_t r = i * kRows + row;
-        if (r >= r0 && r < r1) {
+    for (uint32_t i = 0; i < Rounds; ++i) {
+        const uint32_t r = r0 + i * kRows + row;
+        if (r < r1) {
             const T* from = src + (s.q0 + (low + r - base)) * token;
             const Row4<T> a = *(const Row4<T>*)(from + u.at0), b = *(const Row4<T>*)(from + u.at1);
 #pragma unroll
@@ -87,9 +90,9 @@ __global__ __launch_bounds__(kThreads) void heads_append_kernel(const HeadsAppen
         }
     }
 #pragma unroll
-    for (uint32_t i = 0; i < kRounds; ++i) {
-        const uint32_t r = i * kRows + row;
-        if (r >= r0 && r < r1) {
+    for (uint32_t i = 0; i < Rounds; ++i) {
+        const uint32_t r = r0 + i * kRows + row;
+        if (r < r1) {
             if (u.turned) {
                 Angles4 angles;
                 angles.set(p.positions ? p.positions[s.q0 + (low + r - base)] : (int32_t)(low + r), turns, p.rotation.magnitude, p.rotation.magnitude);
@@ -111,39 +114,49 @@ __global__ __launch_bounds__(kThreads) void heads_append_kernel(const HeadsAppen
     }
 #pragma unroll
     for (int d = 32; d; d >>= 1) m = fmaxf(m, __shfl_xor(m, d));
-    if ((tid & 63u) == 0) top[threadIdx.x >> 6] = m;
+    if ((tid & 63u) == 0) top[value][tid >> 6] = m;
     __syncthreads();
     int byte[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-        const int b = byte_of(fmaxf(fmaxf(top[4 * j], top[4 * j + 1]), fmaxf(top[4 * j + 2], top[4 * j + 3])));
+        float a = top[j][0];
+#pragma unroll
+        for (uint32_t w = 1; w < kHalfWaves; ++w) a = fmaxf(a, top[j][w]);
+        const int b = byte_of(a);
         byte[j] = b > had[j] ? b : had[j];
     }
     const int mine = value ? byte[1] : byte[0], grown = mine - (value ? had[1] : had[0]);
     const float inverse = __uint_as_float((uint32_t)(254 - mine) << 23);               // 2^(127 - byte)
-    // what older codes are multiplied by; below 2^-100 all of them vanish alike
-    const float factor = __uint_as_float((uint32_t)(127 - (grown < 100 ? grown : 100)) << 23);
-    const bool again = r0 && grown > 0;
 #pragma unroll
-    for (uint32_t i = 0; i < kRounds; ++i) {
-        const uint32_t r = i * kRows + row;
-        if (r >= r1 || (r < r0 && !again)) continue;
+    for (uint32_t i = 0; i < Rounds; ++i) {
+        const uint32_t r = r0 + i * kRows + row;
+        if (r >= r1) break;
         const uint64_t c0 = codes + (uint64_t)r * D + u.at0, c1 = codes + (uint64_t)r * D + u.at1;
-        uint32_t w0, w1;
-        if (r < r0) {
-            w0 = recode4(*(const uint32_t*)(p.base[0] + c0), factor);
-            w1 = recode4(*(const uint32_t*)(p.base[0] + c1), factor);
-        } else {
-            w0 = codes4(x[i], inverse);
-            w1 = codes4(x[i] + 4, inverse);
-        }
+        const uint32_t w0 = codes4(x[i], inverse), w1 = codes4(x[i] + 4, inverse);
         for (uint32_t b = 0; b < p.replicas; ++b) {
             *(uint32_t*)(p.base[b] + c0) = w0;
             *(uint32_t*)(p.base[b] + c1) = w1;
         }
     }
+    if (r0 && grown > 0) {
+        // older rows take the new scale; below 2^-100 all of them vanish alike
+        const float factor = __uint_as_float((uint32_t)(127 - (grown < 100 ? grown : 100)) << 23);
+        for (uint32_t r = row; r < r0; r += kRows) {
+            const uint64_t c = codes + (uint64_t)r * D + lane * 8;
+            const u32x2 old = *(const u32x2*)(p.base[0] + c), w = {recode4(old.x, factor), recode4(old.y, factor)};
+            for (uint32_t b = 0; b < p.replicas; ++b) *(u32x2*)(p.base[b] + c) = w;
+        }
+    }
     if (threadIdx.x == 0)
         for (uint32_t b = 0; b < p.replicas; ++b) *(uint16_t*)(p.base[b] + scales) = (uint16_t)(byte[0] | (byte[1] << 8));
+}
+
+// Few new tokens a sequence: two waves a block, for as many rows as they pass in two rounds.
+template <class T, uint32_t D>
+void launch(const HeadsAppendParams& p, const Places& w, uint32_t blocks, hipStream_t stream) {
+    constexpr uint32_t kFew = 2 * 64 / (D / 8);
+    if (p.seqs.max_q <= kFew) heads_append_kernel<T, D, 128, 2><<<blocks, 128, 0, stream>>>(p, w);
+    else heads_append_kernel<T, D, 512, D / 32><<<blocks, 512, 0, stream>>>(p, w);
 }
 
 }  // namespace
@@ -160,16 +173,9 @@ hipError_t launch_heads_append(const HeadsAppendParams& p, hipStream_t stream) {
         q.first = (uint32_t)first;
         const uint32_t blocks = (uint32_t)std::min(most, total - first) * G;
         const bool half = p.type == KVPUB_FP16;
-        if (p.heads.dim == 64) {
-            if (half) heads_append_kernel<_Float16, 64><<<blocks, kThreads, 0, stream>>>(q, w);
-            else heads_append_kernel<__bf16, 64><<<blocks, kThreads, 0, stream>>>(q, w);
-        } else if (p.heads.dim == 128) {
-            if (half) heads_append_kernel<_Float16, 128><<<blocks, kThreads, 0, stream>>>(q, w);
-            else heads_append_kernel<__bf16, 128><<<blocks, kThreads, 0, stream>>>(q, w);
-        } else {
-            if (half) heads_append_kernel<_Float16, 256><<<blocks, kThreads, 0, stream>>>(q, w);
-            else heads_append_kernel<__bf16, 256><<<blocks, kThreads, 0, stream>>>(q, w);
-        }
+        if (p.heads.dim == 64) half ? launch<_Float16, 64>(q, w, blocks, stream) : launch<__bf16, 64>(q, w, blocks, stream);
+        else if (p.heads.dim == 128) half ? launch<_Float16, 128>(q, w, blocks, stream) : launch<__bf16, 128>(q, w, blocks, stream);
+        else half ? launch<_Float16, 256>(q, w, blocks, stream) : launch<__bf16, 256>(q, w, blocks, stream);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }

@@ -223,6 +223,8 @@ struct RotateParams {
     uint32_t heads;
     uint32_t units;              // groups of 8 values of a row that the call touches: the rotated ones, then the copied ones
     uint32_t type;               // KVPUB_BF16, KVPUB_FP16, KVPUB_FP32
+    uint32_t across;             // set by launch_rotate: heads that a block takes beside each other
+    uint32_t tokens;             // and tokens
     float sign;                  // the magnitude, negative for the transpose
 };
 hipError_t launch_rotate(const RotateParams& p, hipStream_t stream);

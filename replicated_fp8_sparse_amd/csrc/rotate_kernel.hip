@@ -19,14 +19,14 @@ constexpr uint32_t kThreads = 256;
 // H: heads a thread takes at once.
 template <class T, bool Halves, int H>
 __global__ __launch_bounds__(kThreads) void rotate_kernel(const RotateParams p) {
-    const uint32_t rows = kThreads / p.units;                 // heads that a block takes at once
-    const uint32_t row = threadIdx.x / p.units, unit = threadIdx.x - row * p.units;
-    const uint32_t head0 = blockIdx.x * rows * H + row;
-    if (row >= rows || head0 >= p.heads) return;
+    const uint32_t rows = p.across;
+    const uint32_t row = threadIdx.x / p.units, unit = threadIdx.x - row * p.units, token = row / rows;
+    const uint32_t head0 = blockIdx.x * rows * H + row - token * rows;
+    if (token >= p.tokens || head0 >= p.heads) return;
     const RowUnit u = row_unit(unit, p.rotation.dim, p.rotation.start, Halves);
     Turns4 turns;
     turns.load(p.rotation.turns, unit, u.turned);
-    for (uint32_t t = blockIdx.y; t < p.num_tokens; t += gridDim.y) {
+    for (uint32_t t = blockIdx.y * p.tokens + token; t < p.num_tokens; t += gridDim.y * p.tokens) {
         const T* x = (const T*)p.x + (int64_t)t * p.x_token;
         T* y = (T*)p.y + (int64_t)t * p.y_token;
         Row4<T> a[H], b[H];
@@ -59,19 +59,20 @@ __global__ __launch_bounds__(kThreads) void rotate_kernel(const RotateParams p) 
 
 template <class T, int H>
 void launch(const RotateParams& p, hipStream_t stream) {
-    const uint32_t rows = kThreads / p.units;
-    const uint32_t across = (p.heads + rows * H - 1) / (rows * H);
+    const uint32_t across = (p.heads + p.across * H - 1) / (p.across * H);
     const uint32_t most = std::min(65535u, (1u << 23) / across);       // a launch holds fewer than 2^32 threads
-    const dim3 grid(across, std::min(p.num_tokens, most));
+    const dim3 grid(across, std::min((p.num_tokens + p.tokens - 1) / p.tokens, most));
     if (p.rotation.halves) rotate_kernel<T, true, H><<<grid, kThreads, 0, stream>>>(p);
     else rotate_kernel<T, false, H><<<grid, kThreads, 0, stream>>>(p);
 }
 
 template <class T>
-void launch(const RotateParams& p, hipStream_t stream) {
+void launch(RotateParams p, hipStream_t stream) {
+    const uint32_t rows = kThreads / p.units;
+    p.across = std::min(p.heads, rows);
+    p.tokens = rows / p.across;
     // several heads a thread once that still leaves every compute unit two blocks
-    const uint64_t rows = kThreads / p.units;
-    if (p.heads >= 4 * rows && (uint64_t)p.num_tokens * (p.heads / (4 * rows)) >= 512) launch<T, 4>(p, stream);
+    if (p.heads >= 4 * p.across && (uint64_t)p.num_tokens * (p.heads / (4 * p.across)) >= 512) launch<T, 4>(p, stream);
     else launch<T, 1>(p, stream);
 }
 
