@@ -20,6 +20,7 @@ namespace kvpub {
 namespace {
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 
 // Largest finite magnitude of x and m.
@@ -52,11 +53,15 @@ __device__ __forceinline__ uint32_t recode4(uint32_t old, float factor) {
     return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(b[0] * factor, b[1] * factor, w, true);
 }
 
+template <uint32_t D> constexpr uint32_t kMany = D == 256 ? 1024 : 512;
+
 // N threads, half of them for the keys, half for the values; Rounds: of rows that they pass,
 // enough for the new ones.
 template <class T, uint32_t D, uint32_t N, uint32_t Rounds>
 __global__ __launch_bounds__(N) void heads_append_kernel(const HeadsAppendParams p, const Places places) {
     constexpr uint32_t kLanes = D / 8, kRows = N / 2 / kLanes, kHalfWaves = N / 128;
+    constexpr bool Many = N > 128;
+    __shared__ __attribute__((aligned(16))) uint8_t image[2][Many ? 64 * D : 16];
     __shared__ float top[2][kHalfWaves];
     __shared__ int had[2];
     const uint32_t G = p.heads.groups, tid = threadIdx.x & (N / 2 - 1);
@@ -131,11 +136,27 @@ __global__ __launch_bounds__(N) void heads_append_kernel(const HeadsAppendParams
     for (uint32_t i = 0; i < Rounds; ++i) {
         const uint32_t r = r0 + i * kRows + row;
         if (r >= r1) break;
-        const uint64_t c0 = codes + (uint64_t)r * D + u.at0, c1 = codes + (uint64_t)r * D + u.at1;
         const uint32_t w0 = codes4(x[i], inverse), w1 = codes4(x[i] + 4, inverse);
-        for (uint32_t b = 0; b < p.replicas; ++b) {
-            *(uint32_t*)(p.base[b] + c0) = w0;
-            *(uint32_t*)(p.base[b] + c1) = w1;
+        if constexpr (Many) {
+            *(uint32_t*)(image[value] + r * D + u.at0) = w0;
+            *(uint32_t*)(image[value] + r * D + u.at1) = w1;
+        } else {
+            for (uint32_t b = 0; b < p.replicas; ++b) {
+                *(uint32_t*)(p.base[b] + codes + r * D + u.at0) = w0;
+                *(uint32_t*)(p.base[b] + codes + r * D + u.at1) = w1;
+            }
+        }
+    }
+    if constexpr (Many) {
+        // the rows put together, and stored in pieces of 16 bytes
+        __syncthreads();
+        for (uint32_t at = r0 * D + tid * 16; at < r1 * D; at += N / 2 * 16) {
+            const u32x4 w = *(const u32x4*)(image[value] + at);
+            for (uint32_t b = 0; b < p.replicas; ++b) {
+                u32x4* to = (u32x4*)(p.base[b] + codes + at);
+                if (p.stream) __builtin_nontemporal_store(w, to);
+                else *to = w;
+            }
         }
     }
     if (r0 && grown > 0) {
@@ -156,7 +177,7 @@ template <class T, uint32_t D>
 void launch(const HeadsAppendParams& p, const Places& w, uint32_t blocks, hipStream_t stream) {
     constexpr uint32_t kFew = 2 * 64 / (D / 8);
     if (p.seqs.max_q <= kFew) heads_append_kernel<T, D, 128, 2><<<blocks, 128, 0, stream>>>(p, w);
-    else heads_append_kernel<T, D, 512, D / 32><<<blocks, 512, 0, stream>>>(p, w);
+    else heads_append_kernel<T, D, kMany<D>, 16 * D / kMany<D>><<<blocks, kMany<D>, 0, stream>>>(p, w);
 }
 
 }  // namespace
@@ -167,10 +188,14 @@ hipError_t launch_heads_append(const HeadsAppendParams& p, hipStream_t stream) {
     // n tokens lie in at most floor((n + 62) / 64) + 1 blocks
     const Places w = places(1, 6, 2, ((uint64_t)p.seqs.max_q + 62) / 64 + 1, p.seqs.num_seqs, p.seqs.num_tokens, &total);
     const uint32_t G = p.heads.groups;
+    // what fills half of the L2s or more is stored past them (8 prompts of up to 4096 tokens, 38 MB: 28.2 us
+    // for 32.8; 4 of 2048, 64 values a head, 10 MB: 7.4 for 7.1)
+    const bool past = (uint64_t)p.seqs.num_tokens * G * p.heads.dim * 2 * p.replicas > (16u << 20);
     const uint64_t most = ((1u << 23) - 1) / G;                       // a launch holds fewer than 2^32 threads
     for (uint64_t first = 0; first < total; first += most) {
         HeadsAppendParams q = p;
         q.first = (uint32_t)first;
+        q.stream = past ? 1u : 0u;
         const uint32_t blocks = (uint32_t)std::min(most, total - first) * G;
         const bool half = p.type == KVPUB_FP16;
         if (p.heads.dim == 64) half ? launch<_Float16, 64>(q, w, blocks, stream) : launch<__bf16, 64>(q, w, blocks, stream);

@@ -274,6 +274,7 @@ struct HeadsAppendParams {
     const CtxHead* head;         // status
     unsigned long long* invalid_count;
     uint32_t first;              // set by launch_heads_append: the launch's first place
+    uint32_t stream;             // and whether codes are stored past the L2s
 };
 hipError_t launch_heads_append(const HeadsAppendParams& p, hipStream_t stream);
 
