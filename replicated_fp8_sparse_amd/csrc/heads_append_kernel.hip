@@ -64,6 +64,7 @@ __global__ __launch_bounds__(N) void heads_append_kernel(const HeadsAppendParams
     __shared__ __attribute__((aligned(16))) uint8_t image[2][Many ? 64 * D : 16];
     __shared__ float top[2][kHalfWaves];
     __shared__ int had[2];
+    __shared__ uint32_t stop;
     const uint32_t G = p.heads.groups, tid = threadIdx.x & (N / 2 - 1);
     const uint32_t value = __builtin_amdgcn_readfirstlane(threadIdx.x / (N / 2));       // 0: keys, 1: values
     const uint32_t turn = blockIdx.x / G, g = blockIdx.x - turn * G;
@@ -74,7 +75,6 @@ __global__ __launch_bounds__(N) void heads_append_kernel(const HeadsAppendParams
     const int64_t block = begin / 64 + s.place, low = block * 64;
     if (!s.found || end <= begin || low >= end) return;
     const int32_t page = uniform_load(p.seqs.pages, (int64_t)s.b * p.seqs.pages_stride + block);
-    const uint32_t status = (uint32_t)uniform_load((const int32_t*)&p.head->status, 0);
     const uint32_t r0 = begin > low ? (uint32_t)(begin - low) : 0u, r1 = end < low + 64 ? (uint32_t)(end - low) : 64u;
 
     const uint32_t lane = tid % kLanes, row = tid / kLanes, dim = value ? 0u : p.rotation.dim;
@@ -106,13 +106,16 @@ __global__ __launch_bounds__(N) void heads_append_kernel(const HeadsAppendParams
             m = amax8(x[i], m);
         }
     }
-    if ((status & kStatusPoisoned) || (uint32_t)page >= p.heads.num_pages) {
-        if (!(status & kStatusPoisoned) && g == 0 && threadIdx.x == 0) atomicAdd(p.invalid_count, 1ull);
+    if ((uint32_t)page >= p.heads.num_pages) {
+        if (g == 0 && threadIdx.x == 0 && !(p.head->status & kStatusPoisoned)) atomicAdd(p.invalid_count, 1ull);
         return;
     }
     const uint64_t at = (uint64_t)page * p.heads.page_stride, codes = at + (uint64_t)(2 * g + value) * 64 * D, scales = at + (uint64_t)G * 128 * D + 2 * g;
-    // the scales that older rows of the block have, read by the thread that later writes them
+    // the scales that older rows of the block have, read by the thread that later writes them; it also decides
+    // for the whole block whether the context is poisoned (a fence that times out on another stream may set the flag
+    // at any moment)
     if (threadIdx.x == 0) {
+        stop = p.head->status & kStatusPoisoned;
         const uint8_t* o = p.base[0] + scales;
 #pragma unroll
         for (int j = 0; j < 2; ++j) had[j] = r0 ? (o[j] < 1 ? 1 : (o[j] > 245 ? 245 : o[j])) : 0;
@@ -121,6 +124,7 @@ __global__ __launch_bounds__(N) void heads_append_kernel(const HeadsAppendParams
     for (int d = 32; d; d >>= 1) m = fmaxf(m, __shfl_xor(m, d));
     if ((tid & 63u) == 0) top[value][tid >> 6] = m;
     __syncthreads();
+    if (stop) return;
     int byte[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {

@@ -10,14 +10,27 @@
 // score exceeds it by more than 2^8, so most tiles neither rescale nor shuffle.
 //
 // Mapping.  Rows are (token, query head) pairs that share a key-value head: a unit
-// is 16 RT of them and one key-value head.  Scores come out transposed: positions
+// is 16, 32 or 64 of them and one key-value head.  Scores come out transposed: positions
 // down, rows across, so that a lane holds 8 positions of one row, and its weights
 // are an operand of the second product as they are if the values' positions come in the
 // same order.  Values are read by position, 16 lanes a row, and brought to columns by
-// byte permutes within a lane: no LDS before the end.  The 4 waves of a block take
-// every 4th tile of 32 positions, each from memory straight to registers one
-// tile ahead, and join their parts through LDS; long sequences are cut into chunks
-// for several blocks, which join_kernel joins in order.
+// byte permutes within a lane: no LDS before the end (but for the queries of 64
+// rows).  The 4 waves of a block take every 4th tile of 32 positions, each from
+// memory straight to registers: keys as soon as the last tile's scores are computed, values as
+// soon as its products are, so both are on their way behind the other half of the work.
+// Page numbers, lengths and scales come through the scalar cache, whose waits leave those
+// loads alone.  The waves join their parts through LDS; long sequences are cut into
+// chunks for several blocks, which join_kernel joins in order.
+//
+// Bound.  16 rows: memory.  64 sequences of up to 8192 positions over 8 heads of 128: 107 us for
+// 545 MB, a large copy's 5.1 TB/s, and 5 for the join.  64 rows: a tile takes 270 vector
+// instructions (80 of them the widening, 128 the weights) and 64 matrix instructions, which exclude each
+// other more than they overlap: beside a wave that issues 16 x 16 x 32 products
+// back to back the other waves of its SIMD issue nothing for 14 of 16 cycles (32 x 32 x 16:
+// 21 of 32), so 2100 cycles of work a tile and two waves a SIMD that need 2400.  Prompts of 2 x 4096
+// tokens behind as much context, 16 heads over 4: 240-260 us, 69-77 % of a large bf16 product's rate.
+// (Built and measured beside it: 32 x 32 x 16 products throughout, 247; the same with the next
+// tile's scores between this one's weights, one wave a SIMD, 300; 32 rows a unit, 300-315.)
 #include <algorithm>
 #include <cfloat>
 
@@ -37,10 +50,18 @@ typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
 constexpr uint32_t kWaves = 4, kThreads = kWaves * 64;
-constexpr uint32_t kLeastChunk = 512;             // of a block, for up to kLeastChunk / kChunkRows rows
+// How a call is cut (plan_heads_attend), by its bounds.  Measured, us; 128 values, 8 query heads a key-value head:
+//   one token over 8192, 2 heads: cuts of 256 / 512 / 1024 positions 11.1 / 11.1 / 13.3;
+//   over 700: in two 9.7, whole 8.5; over 65536: 128 cuts 27.5, 64 cuts 24.1
+constexpr uint32_t kLeastChunk = 512, kWhole = 768, kMostChunks = 64;
+//   cuts of at least 16 / 32 / 64 positions a row, as each row of a cut writes a part: 8 tokens of 16 sequences
+//   over 8192 (32 rows) 84 / 73 / 67
 constexpr uint32_t kChunkRows = 64;
-constexpr uint32_t kWhole = 768, kMostChunks = 64;
-constexpr uint32_t kWanted = 4096, kWantedWide = 1024;       // blocks, of 16 rows and of more
+//   cut for up to 2048 / 4096 / 8192 blocks of 16 rows: one token of 64 sequences of up to 8192 122.5 / 120.3 / 124.9;
+//   for 1024 / 2048 / 4096 of more rows: 16 trees of 24 56 / 60 / 61, prompts of 2 x 4096 260 / 317 (in two) / -
+constexpr uint32_t kWanted = 4096, kWantedWide = 1024;
+//   units of 64 rows from so many blocks on, else of 32: prompts of 2 x 2048, 64 values 57 (32 rows) / 60, in fp16
+//   105 / 114; trees 56 / 94; 2 x 4096 with 1116 blocks of 64 rows 315 / 260
 constexpr uint32_t kFull = 1024;
 constexpr uint32_t kTile = 32;                    // positions of a wave's step
 constexpr float kLazy = 8.0f;                     // rescale when a maximum grows past 2^8
@@ -49,7 +70,8 @@ constexpr float kLn2 = 0.693147180559945309f;
 typedef __attribute__((address_space(1))) uint8_t gbyte;   // a byte in global memory
 template <class T> using gptr = __attribute__((address_space(1))) T*;
 
-// Waves that a SIMD should hold: what the registers of the accumulators leave room for.
+// Waves that a SIMD should hold: what the registers of the accumulators leave room for
+// (16 rows of 128 values: 3; at 4 they spill, 133 us for 121 in the large decode).
 constexpr int waves_a_simd(int D, int RT) { return RT * D <= 64 ? 5 : (RT * D <= 128 ? 3 : (RT * D <= 512 ? 2 : 1)); }
 
 template <class E> struct Operand;

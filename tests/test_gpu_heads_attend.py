@@ -242,3 +242,48 @@ def test_graph_replays_and_two_streams(ctx):
         torch.cuda.synchronize()
         U.check_all(cache, q, seqs, what=f"replay {k}")
         U.check_all(cache, other, seqs)
+
+
+def test_no_positions_at_all(ctx):
+    """max_kv_len 0: every token sees nothing, and the tables are not looked at."""
+    cache = U.HeadsCache(1, 2, 64, replicas=1)
+    for lens in ([0, 0], [5, 300]):
+        seqs = U.Seqs(lens, [3, 1], 10, max_kv=0, table=np.full((2, 1), 2 ** 31 - 1))
+        q = U.Query(4, 4, 64)
+        U.attend(ctx, cache, q, seqs)
+        assert bool((q.out == 0).all()) and bool((q.lse == -math.inf).all())
+        q.untouched(range(4))
+    assert ctx.invalid() == 0
+
+
+@pytest.mark.parametrize("kv", [511, 512, 513, 767, 768, 769, 1024, 1025, 65536 + 7])
+def test_lengths_around_the_cuts(ctx, kv):
+    cache = cache_for([kv, 600], 1, 64, replicas=1)
+    seqs = U.Seqs([kv, 600], [2, 1], cache.pages)
+    q = U.Query(3, 4, 64)
+    U.attend(ctx, cache, q, seqs)
+    U.check_all(cache, q, seqs)
+
+
+@pytest.mark.parametrize("B,n,kv", [(40, 24, 300), (3, 500, 900), (200, 9, 40)])
+def test_units_of_32_and_64_rows_in_one_call(ctx, B, n, kv):
+    """Ragged chunks: sequences of one token beside those of many, places by tokens and by the bound."""
+    rng = np.random.default_rng(B)
+    counts = rng.integers(1, n + 1, B)
+    counts[0], counts[-1] = n, 1
+    lens = counts + rng.integers(0, kv, B)
+    cache = cache_for(lens, 2, 128, replicas=1)
+    seqs = U.Seqs(lens, counts, cache.pages)
+    q = U.Query(seqs.T, 14, 128)
+    U.attend(ctx, cache, q, seqs)
+    U.check_all(cache, q, seqs)
+
+
+def test_prompts_that_fill_the_card(ctx):
+    """More than 1024 blocks of 64 rows, and queries of both types."""
+    for kind in ("bf16", "fp16"):
+        cache = cache_for([1100, 900], 16, 64, replicas=1)
+        seqs = U.Seqs([1100, 900], [1100, 900], cache.pages)
+        q = U.Query(2000, 64, 64, kind)
+        U.attend(ctx, cache, q, seqs)
+        U.check_all(cache, q, seqs)

@@ -48,7 +48,7 @@ def run(ctx, x, y, pos, rot, kind, transpose=0):
 @pytest.mark.parametrize("halves", [False, True])
 @pytest.mark.parametrize("T,H,width,dim,start,pad,head_pad", [
     (1, 1, 8, 8, 0, 0, 0), (1, 16, 64, 64, 0, 0, 128), (5, 3, 80, 24, 16, 8, 0), (7, 128, 128, 48, 72, 0, 8), (3, 1, 1024, 1024, 0, 0, 0),
-    (300, 100, 96, 40, 56, 16, 0), (9, 1000, 64, 64, 0, 0, 0), (2, 7, 1000, 8, 992, 0, 0), (700, 33, 256, 256, 0, 0, 0)])
+    (300, 100, 96, 40, 56, 16, 0), (6000, 5, 64, 32, 8, 0, 0), (9000, 3, 64, 64, 0, 8, 0), (9, 1000, 64, 64, 0, 0, 0), (2, 7, 1000, 8, 992, 0, 0), (700, 33, 256, 256, 0, 0, 0)])
 def test_rotation(ctx, T, H, width, dim, start, pad, head_pad, halves, kind):
     rng = np.random.default_rng(T + H)
     pos = rng.integers(0, 2 ** 20, T)
