@@ -454,7 +454,7 @@ KVPUB_API kvpub_status kvpub_attend_expanded(kvpub_ctx *ctx, const kvpub_expande
  *   y1 = magnitude * (x1 cos a - x2 sin a),  y2 = magnitude * (x1 sin a + x2 cos a).
  * The frequencies are a table of turns a position in units of 2^-64, so that an
  * angle is one 64-bit product whatever the position: far ones lose nothing.
- * Angles are held to 2^-33 of a turn, sines, cosines and products in binary32.
+ * Angles are held to 2^-32 of a turn, sines, cosines and products in binary32.
  * Positions are int32 and may be negative (they turn back). */
 #define KVPUB_ROTATE_PAIRS 0u   /* pair i: values start + 2i and start + 2i + 1 */
 #define KVPUB_ROTATE_HALVES 1u  /* pair i: values start + i and start + dim/2 + i */
@@ -639,8 +639,9 @@ KVPUB_API uint64_t kvpub_heads_attend_workspace(const kvpub_heads *cache, const 
  * and -inf, what it does not see has no effect whatever its bytes hold, bad pages
  * hide their positions and are counted, tokens of no sequence keep their output,
  * the same call gives the same bits.  Scores, maxima and sums are binary32;
- * weights are rounded to bf16 for the second product (FP16: to the sum of two
- * bf16), out once to its type.  A query or a seen row that is not finite leaves
+ * weights are rounded to bf16 for the second product (FP16, and calls of at most 16
+ * (token, query head) rows a sequence and key-value head: to the sum of two bf16), out once
+ * to its type.  A query or a seen row that is not finite leaves
  * the rows it reaches unspecified, NaN as a rule.
  * T == 0 or num_seqs == 0 launches nothing. */
 KVPUB_API kvpub_status kvpub_heads_attend(kvpub_ctx *ctx, const kvpub_heads *cache, uint32_t replica, uint32_t layer,

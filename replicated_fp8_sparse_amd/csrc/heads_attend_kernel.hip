@@ -5,8 +5,10 @@
 //   score = (scale * a) (q . c),   out = sum_p w_p (b d_p) / sum_p w_p.
 // A code is exact in bf16 and fp16, and so is a value's code times its scale in
 // bf16: nothing of the cache is rounded again.  Weights are rounded to bf16 for the
-// second product (their low parts follow as a second operand for fp16 outputs,
-// whose own step is finer).  One pass: a row's running maximum moves only when a
+// second product: that leaves bf16 outputs off by 0.0021 of their norm where their own
+// rounding alone leaves 0.0017, and a second operand for the low parts costs 38 % in long
+// prompts.  Units of 16 rows, which memory bounds, take that operand (2 % of a large
+// decode), and so do fp16 outputs, whose own step is finer.  One pass: a row's running maximum moves only when a
 // score exceeds it by more than 2^8, so most tiles neither rescale nor shuffle.
 //
 // Mapping.  Rows are (token, query head) pairs that share a key-value head: a unit
@@ -230,6 +232,7 @@ __global__ __launch_bounds__(kThreads, waves_a_simd(D, RT)) void heads_attend_ke
     constexpr uint32_t R = 16 * RT;
     constexpr int NB = D / 16, NQ = D / 32, W = kWaves;
     constexpr bool Shared = RT * D >= 512;
+    constexpr bool Low = RT == 1 || !__is_same(E, __bf16);         // the weights' low parts as a second operand: see above
     struct Join {
         float o[W][16][D + 4];
         float ml[W][16][2];
@@ -411,7 +414,7 @@ __global__ __launch_bounds__(kThreads, waves_a_simd(D, RT)) void heads_attend_ke
             for (int j = 0; j < 8; ++j) {
                 e[j] = __builtin_amdgcn_exp2f(fmaf(s[r][j >> 2][j & 3], ks, -m[r]));
                 w[r][j] = (__bf16)e[j];
-                if constexpr (!__is_same(E, __bf16)) low[r][j] = (__bf16)(e[j] - (float)w[r][j]);
+                if constexpr (Low) low[r][j] = (__bf16)(e[j] - (float)w[r][j]);
             }
             l[r] += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
         }
@@ -432,7 +435,7 @@ __global__ __launch_bounds__(kThreads, waves_a_simd(D, RT)) void heads_attend_ke
 #pragma unroll
                 for (int r = 0; r < RT; ++r) {
                     o[r][4 * c + d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[d], w[r], o[r][4 * c + d], 0, 0, 0);
-                    if constexpr (!__is_same(E, __bf16))
+                    if constexpr (Low)
                         o[r][4 * c + d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[d], low[r], o[r][4 * c + d], 0, 0, 0);
                 }
         }

@@ -64,7 +64,7 @@ class Rotation:
     def apply(self, x, positions, transpose=False):
         """(rotated x [token, head, width] in 64 bits on the host, bound of the error before the last rounding).
 
-        Sine and cosine: 2^-33 turns of angle (2^-30.3 in the value), 2^-29 of polynomial, a rest below 0.8 rounded
+        Sine and cosine: 2^-32 turns of angle (2^-29.3 in the value), 2^-29 of polynomial, a rest below 0.8 rounded
         once (2^-25) and an evaluation within 2 roundings of 2^-24, the magnitude's product one more: 4 * 2^-24.
         A value is two products and a sum: at most 3 roundings of the terms' magnitudes.  7 in all, taken as 8."""
         x = x.double().cpu()
