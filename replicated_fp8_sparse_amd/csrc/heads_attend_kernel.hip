@@ -486,8 +486,8 @@ __global__ __launch_bounds__(kThreads, waves_a_simd(D, RT)) void heads_attend_ke
     }
 }
 
-// The parts of units that several blocks cut, joined in their order: D/4 lanes a row,
-// 16 cuts' parts on the way at a time, each 16 lanes with those cuts' maxima and sums.
+// The parts of units that several blocks cut, joined in their order: D/4 lanes a row, 1024/D rows
+// a block, 16 cuts' parts on the way at a time, each 16 lanes with those cuts' maxima and sums.
 template <class E, int D>
 __global__ __launch_bounds__(256) void join_kernel(const HeadsAttendParams p, const Places places, uint32_t R) {
     constexpr uint32_t kLanes = D / 4, kRows = 256 / kLanes;
@@ -496,7 +496,8 @@ __global__ __launch_bounds__(256) void join_kernel(const HeadsAttendParams p, co
     if (u.rows == 0 || u.chunks <= 1) return;
     const uint32_t l16 = threadIdx.x & 15u, lane = threadIdx.x % kLanes;
     const uint32_t rows = u.rows - u.row0 < R ? u.rows - u.row0 : R;
-    for (uint32_t r = threadIdx.x / kLanes; r < rows; r += kRows) {
+    const uint32_t r = blockIdx.y * kRows + threadIdx.x / kLanes;
+    if (r < rows) {
         const uint64_t slot = ((uint64_t)place * G + g) * p.chunks * R + r;
         float top = -FLT_MAX, sum = 0.f;
         f32x4 acc = {0.f, 0.f, 0.f, 0.f};
@@ -547,7 +548,7 @@ hipError_t launch(HeadsAttendParams p, const Places& w, hipStream_t stream) {
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
         if (p.chunks > 1) {
-            join_kernel<E, D><<<p.units * G, 256, 0, stream>>>(p, w, 16 * RT);
+            join_kernel<E, D><<<dim3(p.units * G, 16 * RT / (1024 / D)), 256, 0, stream>>>(p, w, 16 * RT);
             e = hipGetLastError();
             if (e != hipSuccess) return e;
         }
