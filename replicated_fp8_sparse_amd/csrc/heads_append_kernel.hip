@@ -12,6 +12,11 @@
 // blocks.  Half of its waves take the keys, half the values.  A row takes D/8 lanes of
 // 8 values (4 pairs of the rotation: an angle is computed once), the rows of the block
 // pass by in D/32 rounds that stay in registers between the maximum and the codes.
+//
+// Bound.  Few tokens: a launch and a chain of four reads (lengths, page, context, older scales): 64 sequences x
+// one token, 8 heads of 128, 2 replicas 5.2 us, 256 x 1 6.7.  One round of blocks (4 x up to 2048
+// tokens, 25 MB): that chain, then its bytes, 11.9 us.  Long: the angles, once for each head: 8 x up to
+// 4096 tokens into 1 replica 35 us, where the bytes alone would leave 22.
 #include "kvpub.h"
 #include "rotation.h"
 #include "sequences.h"

@@ -57,13 +57,13 @@ constexpr uint32_t kWaves = 4, kThreads = kWaves * 64;
 //   over 700: in two 9.7, whole 8.5; over 65536: 128 cuts 27.5, 64 cuts 24.1
 constexpr uint32_t kLeastChunk = 512, kWhole = 768, kMostChunks = 64;
 //   cuts of at least 16 / 32 / 64 positions a row, as each row of a cut writes a part: 8 tokens of 16 sequences
-//   over 8192 (32 rows) 84 / 73 / 67
+//   over 8192 (32 rows) 82 / 72 / 66
 constexpr uint32_t kChunkRows = 64;
 //   cut for up to 2048 / 4096 / 8192 blocks of 16 rows: one token of 64 sequences of up to 8192 122.5 / 120.3 / 124.9;
-//   for 1024 / 2048 / 4096 of more rows: 16 trees of 24 56 / 60 / 61, prompts of 2 x 4096 260 / 317 (in two) / -
+//   for 768 / 1024 / 1536 of more rows: 16 trees of 24 65 / 54 / 57, and at 2048 prompts of 2 x 4096 go in two, 317 for 260
 constexpr uint32_t kWanted = 4096, kWantedWide = 1024;
 //   units of 64 rows from so many blocks on, else of 32: prompts of 2 x 2048, 64 values 57 (32 rows) / 60, in fp16
-//   105 / 114; trees 56 / 94; 2 x 4096 with 1116 blocks of 64 rows 315 / 260
+//   105 / 112; trees 54 / 89 (48 rows: 61); 2 x 4096 with 1116 blocks of 64 rows 315 / 260
 constexpr uint32_t kFull = 1024;
 constexpr uint32_t kTile = 32;                    // positions of a wave's step
 constexpr float kLazy = 8.0f;                     // rescale when a maximum grows past 2^8
@@ -224,14 +224,15 @@ __device__ __forceinline__ typename Operand<E>::x8 load_query(const E* src, uint
     return __builtin_bit_cast(typename Operand<E>::x8, w);
 }
 
-// Shared: the queries' operands stay in LDS (their registers would cost the second
-// wave a SIMD).
+// Shared: the queries' operands stay in LDS.  64 rows of 128 values would lose the second wave a
+// SIMD to their registers; 32 rows of 128 take 52.7 us for 54.3 (16 trees of 24), 64 of 64 57.1
+// for 58.0 (prompts of 2 x 2048); 16 rows of 256 47.1 for 45.2, and keep them.
 template <class E, int D, int RT>
 __global__ __launch_bounds__(kThreads, waves_a_simd(D, RT)) void heads_attend_kernel(const HeadsAttendParams p, const Places places) {
     typedef Operand<E> Op;
     constexpr uint32_t R = 16 * RT;
     constexpr int NB = D / 16, NQ = D / 32, W = kWaves;
-    constexpr bool Shared = RT * D >= 512;
+    constexpr bool Shared = RT > 1 && RT * D >= 256;
     constexpr bool Low = RT == 1 || !__is_same(E, __bf16);         // the weights' low parts as a second operand: see above
     struct Join {
         float o[W][16][D + 4];
