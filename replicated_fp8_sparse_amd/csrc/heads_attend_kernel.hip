@@ -62,6 +62,10 @@ constexpr uint32_t kChunkRows = 64;
 //   cut for up to 2048 / 4096 / 8192 blocks of 16 rows: one token of 64 sequences of up to 8192 122.5 / 120.3 / 124.9;
 //   for 768 / 1024 / 1536 of more rows: 16 trees of 24 65 / 54 / 57, and at 2048 prompts of 2 x 4096 go in two, 317 for 260
 constexpr uint32_t kWanted = 4096, kWantedWide = 1024;
+//   and for 256 blocks, one a compute unit, into cuts of kLeastChunk whatever the rows: trees of 2 x 26 tokens, 16 heads over 1
+//   of 256, 6215 positions 24.6 / 46.9 without, 1 x 5, 32 over 2 of 128, 5772 14.4 / 23.6; for 512 blocks no more of
+//   those, but prompts of 6 x 534 behind 409 positions 20.7 / 16.5
+constexpr uint32_t kFill = 256;
 //   units of 64 rows from so many blocks on, else of 32: prompts of 2 x 2048, 64 values 57 (32 rows) / 60, in fp16
 //   105 / 112; trees 54 / 89 (48 rows: 61); 2 x 4096 with 1116 blocks of 64 rows 315 / 260
 constexpr uint32_t kFull = 1024;
@@ -577,10 +581,14 @@ HeadsAttendPlan plan_heads_attend(const HeadsParams& h, uint32_t group, uint64_t
         if (a.units * h.groups < kFull) a.rows = 32;
     }
     (void)unit_places(a.rows, group, num_seqs, num_tokens, max_q, &a.units);
-    const uint64_t least = std::max<uint64_t>(kLeastChunk, std::min<uint64_t>(rows, a.rows) * kChunkRows), blocks = a.units * h.groups;
-    const uint64_t most = max_kv <= kWhole ? 1 : std::min<uint64_t>(kMostChunks, (max_kv + least - 1) / least);
-    const uint64_t cuts = std::max<uint64_t>(1, std::min(most, (a.rows == 16 ? kWanted : kWantedWide) / std::max<uint64_t>(1, blocks)));
-    a.chunk = (uint32_t)std::max<uint64_t>(least, ((max_kv + cuts - 1) / cuts + 127) / 128 * 128);
+    const uint64_t blocks = std::max<uint64_t>(1, a.units * h.groups);
+    const auto cuts = [&](uint64_t least, uint64_t wanted) {
+        const uint64_t most = max_kv <= kWhole ? 1 : std::min<uint64_t>(kMostChunks, (max_kv + least - 1) / least);
+        return std::max<uint64_t>(1, std::min<uint64_t>(most, wanted / blocks));
+    };
+    const uint64_t by_rows = std::max<uint64_t>(kLeastChunk, std::min<uint64_t>(rows, a.rows) * kChunkRows);
+    const uint64_t n = std::max(cuts(kLeastChunk, kFill), cuts(by_rows, a.rows == 16 ? kWanted : kWantedWide));
+    a.chunk = (uint32_t)std::max<uint64_t>(kLeastChunk, ((max_kv + n - 1) / n + 127) / 128 * 128);
     a.chunks = (uint32_t)std::max<uint64_t>(1, (max_kv + a.chunk - 1) / a.chunk);
     // parts of as many rows as the bounds allow, which grows with each of them; the rows of a unit that none has count too
     const uint64_t parts = std::min<uint64_t>(kWanted * 16, (num_tokens * group + num_seqs * 64) * h.groups * std::min<uint64_t>(kMostChunks, (max_kv + kLeastChunk - 1) / kLeastChunk + 1));

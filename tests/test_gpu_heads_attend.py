@@ -279,6 +279,20 @@ def test_units_of_32_and_64_rows_in_one_call(ctx, B, n, kv):
     U.check_all(cache, q, seqs)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+@pytest.mark.parametrize("kv,n,G,H,D", [(513, 40, 1, 8, 256), (769, 33, 2, 8, 128), (1024, 26, 1, 16, 256), (3000, 90, 1, 16, 64), (6215, 26, 1, 16, 256)])
+def test_few_units_of_many_rows_are_cut_finely(ctx, kv, n, G, H, D, kind):
+    """A prompt and a tree of the same lengths: rows whose positions end in a cut before the last."""
+    lens, counts = [kv, n + 3], [n, n]
+    cache = cache_for(lens, G, D, replicas=1)
+    tree = U.random_tree(counts, 2, kv)
+    for mask in (None, tree):
+        seqs = U.Seqs(lens, counts, cache.pages, tree=mask)
+        q = U.Query(seqs.T, H, D, kind)
+        U.attend(ctx, cache, q, seqs)
+        U.check_all(cache, q, seqs)
+
+
 def test_prompts_that_fill_the_card(ctx):
     """More than 1024 blocks of 64 rows, and queries of both types."""
     for kind in ("bf16", "fp16"):
