@@ -54,21 +54,24 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 constexpr uint32_t kWaves = 4, kThreads = kWaves * 64;
 // How a call is cut (plan_heads_attend), by its bounds.  Measured, us; 128 values, 8 query heads a key-value head:
 //   one token over 8192, 2 heads: cuts of 256 / 512 / 1024 positions 11.1 / 11.1 / 13.3;
-//   over 700: in two 9.7, whole 8.5; over 65536: 128 cuts 27.5, 64 cuts 24.1
-constexpr uint32_t kLeastChunk = 512, kWhole = 768, kMostChunks = 64;
+//   over 700: in two 9.7, whole 8.5; over 65536: 64 cuts 19.5, 128 cuts 15.8
+constexpr uint32_t kLeastChunk = 512, kWhole = 768, kMostChunks = 128;
 //   cuts of at least 16 / 32 / 64 positions a row, as each row of a cut writes a part: 8 tokens of 16 sequences
 //   over 8192 (32 rows) 82 / 72 / 66
 constexpr uint32_t kChunkRows = 64;
 //   cut for up to 2048 / 4096 / 8192 blocks of 16 rows: one token of 64 sequences of up to 8192 122.5 / 120.3 / 124.9;
 //   for 768 / 1024 / 1536 of more rows: 16 trees of 24 65 / 54 / 57, and at 2048 prompts of 2 x 4096 go in two, 317 for 260
 constexpr uint32_t kWanted = 4096, kWantedWide = 1024;
-//   and for 256 blocks, one a compute unit, into cuts of kLeastChunk whatever the rows: trees of 2 x 26 tokens, 16 heads over 1
+//   and for kFill blocks, one a compute unit, into cuts of kLeastChunk whatever the rows: trees of 2 x 26 tokens, 16 heads over 1
 //   of 256, 6215 positions 24.6 / 46.9 without, 1 x 5, 32 over 2 of 128, 5772 14.4 / 23.6; for 512 blocks no more of
-//   those, but prompts of 6 x 534 behind 409 positions 20.7 / 16.5
+//   those, but prompts of 6 x 534 behind 409 positions 20.7 / 16.5, so for those only cuts of twice as many: trees of
+//   23 x 28 tokens, 2 heads of 64, over 8926 18.1 / 23.0
 constexpr uint32_t kFill = 256;
-//   units of 64 rows from so many blocks on, else of 32: prompts of 2 x 2048, 64 values 57 (32 rows) / 60, in fp16
-//   105 / 112; trees 54 / 89 (48 rows: 61); 2 x 4096 with 1116 blocks of 64 rows 315 / 260
-constexpr uint32_t kFull = 1024;
+//   units of 64 rows from kFull blocks on, as many as the card holds at once, twice as many for 64 values, of which it
+//   holds three blocks of 32 rows a compute unit; else of 32.  32 / 64 rows: chunks of 4 x 256 over 4096, 32 heads over 8
+//   of 128 (512 blocks of 64) 107 / 86, 2 x 1547 over 4701, 15 over 3 (726) 151 / 131, in fp16 167 / 163, of 64 values 82 / 94;
+//   prompts of 1 x 2048, 24 over 4 of 64 (768) 32 / 36; below: 4 x 676 over 1243, 20 over 4 (about 420) 33 / 37
+constexpr uint32_t kFull = 512;
 constexpr uint32_t kTile = 32;                    // positions of a wave's step
 constexpr float kLazy = 8.0f;                     // rescale when a maximum grows past 2^8
 constexpr float kLn2 = 0.693147180559945309f;
@@ -491,49 +494,70 @@ __global__ __launch_bounds__(kThreads, waves_a_simd(D, RT)) void heads_attend_ke
     }
 }
 
-// The parts of units that several blocks cut, joined in their order: D/4 lanes a row, 1024/D rows
-// a block, 16 cuts' parts on the way at a time, each 16 lanes with those cuts' maxima and sums.
-template <class E, int D>
-__global__ __launch_bounds__(256) void join_kernel(const HeadsAttendParams p, const Places places, uint32_t R) {
-    constexpr uint32_t kLanes = D / 4, kRows = 256 / kLanes;
+// The parts of units that several blocks cut, joined in their order: D/4 lanes a row, which share out the cuts'
+// maxima and sums; 2^shift such groups of lanes a row, each with its run of the cuts, 16 on the way at a time.
+// One token over 65536, 128 cuts: 15.8 us with the cuts shared out, 26.3 with one group a row.  Up to 16 cuts
+// one group takes them (Split false), and its loops are the whole block's, 0.2 us less.
+template <class E, int D, bool Split>
+__global__ __launch_bounds__(256) void join_kernel(const HeadsAttendParams p, const Places places, uint32_t R, uint32_t shift_) {
+    constexpr uint32_t kLanes = D / 4, kGroups = 256 / kLanes, kEach = kMostChunks / kLanes, kBatch = 16;
+    __shared__ float factors[kGroups][kMostChunks];
+    __shared__ f32x4 sums[Split ? 256 : 1];
+    const uint32_t shift = Split ? shift_ : 0u;
     const uint32_t G = p.heads.groups, place = blockIdx.x / G, g = blockIdx.x - place * G;
     const Unit u = unit_of(p, places, p.first + place, R);
     if (u.rows == 0 || u.chunks <= 1) return;
-    const uint32_t l16 = threadIdx.x & 15u, lane = threadIdx.x % kLanes;
+    const uint32_t lane = threadIdx.x % kLanes, group = threadIdx.x / kLanes, part = group & ((1u << shift) - 1);
     const uint32_t rows = u.rows - u.row0 < R ? u.rows - u.row0 : R;
-    const uint32_t r = blockIdx.y * kRows + threadIdx.x / kLanes;
+    const uint32_t r = blockIdx.y * (kGroups >> shift) + (group >> shift);
+    float top = -FLT_MAX, sum = 0.f;
+    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
     if (r < rows) {
         const uint64_t slot = ((uint64_t)place * G + g) * p.chunks * R + r;
-        float top = -FLT_MAX, sum = 0.f;
-        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-        for (uint32_t c0 = 0; c0 < u.chunks; c0 += 16) {
-            const uint32_t many = u.chunks - c0 < 16 ? u.chunks - c0 : 16u;
-            f32x4 x[16];
+        float m[kEach], l[kEach];
 #pragma unroll
-            for (uint32_t i = 0; i < 16; ++i)
-                if (i < many) x[i] = *(const f32x4*)(p.part + (slot + (uint64_t)(c0 + i) * R) * D + lane * 4);
-            float m = -FLT_MAX, l = 0.f;
-            if (l16 < many) {
-                const float2 ml = *(const float2*)(p.part_ml + (slot + (uint64_t)(c0 + l16) * R) * 2);
-                m = ml.x, l = ml.y;
+        for (uint32_t i = 0; i < kEach; ++i) {
+            const uint32_t c = i * kLanes + lane;
+            m[i] = -FLT_MAX, l[i] = 0.f;
+            if (c < u.chunks) {
+                const float2 ml = *(const float2*)(p.part_ml + (slot + (uint64_t)c * R) * 2);
+                m[i] = ml.x, l[i] = ml.y;
             }
-            float high = fmaxf(top, m);
-#pragma unroll
-            for (int d = 1; d < 16; d <<= 1) high = fmaxf(high, __shfl_xor(high, d));
-            const float old = __builtin_amdgcn_exp2f(top - high), f = __builtin_amdgcn_exp2f(m - high);
-            top = high;
-            sum *= old;
-            acc *= old;
-            l *= f;
-#pragma unroll
-            for (int d = 1; d < 16; d <<= 1) l += __shfl_xor(l, d);
-            sum += l;
-#pragma unroll
-            for (uint32_t i = 0; i < 16; ++i)
-                if (i < many) acc += x[i] * __shfl(f, i, 16);
         }
-        put_row<E, D, 4>(p, u, g, u.row0 + r, lane * 4, acc, top, sum);
+        const uint32_t each = (u.chunks + (1u << shift) - 1) >> shift, first = Split ? part * each : 0u;
+        const uint32_t end = Split && first + each < u.chunks ? first + each : u.chunks;
+        for (uint32_t c0 = first; c0 < end; c0 += kBatch) {
+            f32x4 x[kBatch];
+#pragma unroll
+            for (uint32_t i = 0; i < kBatch; ++i)
+                if (c0 + i < end) x[i] = *(const f32x4*)(p.part + (slot + (uint64_t)(c0 + i) * R) * D + lane * 4);
+            if (c0 == first) {
+#pragma unroll
+                for (uint32_t i = 0; i < kEach; ++i) top = fmaxf(top, m[i]);
+#pragma unroll
+                for (uint32_t d = 1; d < kLanes; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
+#pragma unroll
+                for (uint32_t i = 0; i < kEach; ++i) {
+                    const float f = __builtin_amdgcn_exp2f(m[i] - top);
+                    sum = fmaf(l[i], f, sum);
+                    factors[group][i * kLanes + lane] = f;
+                }
+#pragma unroll
+                for (uint32_t d = 1; d < kLanes; d <<= 1) sum += __shfl_xor(sum, d);
+                __builtin_amdgcn_wave_barrier();             // a group lies in one wave
+            }
+#pragma unroll
+            for (uint32_t i = 0; i < kBatch; ++i)
+                if (c0 + i < end) acc += x[i] * factors[group][c0 + i];
+        }
     }
+    if constexpr (Split) {
+        sums[threadIdx.x] = acc;
+        __syncthreads();
+        if (part != 0) return;
+        for (uint32_t i = 1; i < 1u << shift; ++i) acc += sums[threadIdx.x + i * kLanes];
+    }
+    if (r < rows) put_row<E, D, 4>(p, u, g, u.row0 + r, lane * 4, acc, top, sum);
 }
 
 Places unit_places(uint32_t rows, uint32_t group, uint64_t num_seqs, uint64_t num_tokens, uint64_t max_q, uint64_t* total) {
@@ -553,7 +577,12 @@ hipError_t launch(HeadsAttendParams p, const Places& w, hipStream_t stream) {
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
         if (p.chunks > 1) {
-            join_kernel<E, D><<<dim3(p.units * G, 16 * RT / (1024 / D)), 256, 0, stream>>>(p, w, 16 * RT);
+            constexpr uint32_t groups = 1024 / D;
+            uint32_t shift = 0;
+            while (p.chunks > 16u << shift && 2u << shift <= groups) ++shift;
+            const dim3 grid(p.units * G, std::max<uint32_t>(1, 16 * RT / (groups >> shift)));
+            if (shift) join_kernel<E, D, true><<<grid, 256, 0, stream>>>(p, w, 16 * RT, shift);
+            else join_kernel<E, D, false><<<grid, 256, 0, stream>>>(p, w, 16 * RT, shift);
             e = hipGetLastError();
             if (e != hipSuccess) return e;
         }
@@ -578,16 +607,18 @@ HeadsAttendPlan plan_heads_attend(const HeadsParams& h, uint32_t group, uint64_t
     a.rows = rows <= 16 ? 16 : (rows <= 32 || h.dim == 256 ? 32 : 64);
     if (a.rows == 64) {
         (void)unit_places(64, group, num_seqs, num_tokens, max_q, &a.units);
-        if (a.units * h.groups < kFull) a.rows = 32;
+        if (a.units * h.groups < (h.dim == 64 ? 2 * kFull : kFull)) a.rows = 32;
     }
     (void)unit_places(a.rows, group, num_seqs, num_tokens, max_q, &a.units);
     const uint64_t blocks = std::max<uint64_t>(1, a.units * h.groups);
-    const auto cuts = [&](uint64_t least, uint64_t wanted) {
-        const uint64_t most = max_kv <= kWhole ? 1 : std::min<uint64_t>(kMostChunks, (max_kv + least - 1) / least);
-        return std::max<uint64_t>(1, std::min<uint64_t>(most, wanted / blocks));
-    };
+    const auto cuts = [&](uint64_t most, uint64_t wanted) { return std::min(std::min<uint64_t>(most, kMostChunks), wanted / blocks); };
     const uint64_t by_rows = std::max<uint64_t>(kLeastChunk, std::min<uint64_t>(rows, a.rows) * kChunkRows);
-    const uint64_t n = std::max(cuts(kLeastChunk, kFill), cuts(by_rows, a.rows == 16 ? kWanted : kWantedWide));
+    uint64_t n = 1;
+    if (max_kv > kWhole) {
+        n = std::max(n, cuts((max_kv + by_rows - 1) / by_rows, a.rows == 16 ? kWanted : kWantedWide));
+        n = std::max(n, cuts((max_kv + kLeastChunk - 1) / kLeastChunk, kFill));
+        n = std::max(n, cuts(max_kv / (2 * kLeastChunk), 2 * kFill));
+    }
     a.chunk = (uint32_t)std::max<uint64_t>(kLeastChunk, ((max_kv + n - 1) / n + 127) / 128 * 128);
     a.chunks = (uint32_t)std::max<uint64_t>(1, (max_kv + a.chunk - 1) / a.chunk);
     // parts of as many rows as the bounds allow, which grows with each of them; the rows of a unit that none has count too

@@ -279,6 +279,15 @@ def test_units_of_32_and_64_rows_in_one_call(ctx, B, n, kv):
     U.check_all(cache, q, seqs)
 
 
+@pytest.mark.parametrize("kv,n,G,H,D", [(66000, 1, 1, 3, 256), (20000, 3, 1, 8, 128), (9000, 2, 2, 6, 64), (40000, 20, 1, 4, 256)])
+def test_more_cuts_than_one_group_of_lanes_joins(ctx, kv, n, G, H, D):
+    cache = cache_for([kv, kv // 2], G, D, replicas=1)
+    seqs = U.Seqs([kv, kv // 2], [n, n], cache.pages)
+    q = U.Query(seqs.T, H, D)
+    U.attend(ctx, cache, q, seqs)
+    U.check_all(cache, q, seqs)
+
+
 @pytest.mark.parametrize("kind", ["bf16", "fp16"])
 @pytest.mark.parametrize("kv,n,G,H,D", [(513, 40, 1, 8, 256), (769, 33, 2, 8, 128), (1024, 26, 1, 16, 256), (3000, 90, 1, 16, 64), (6215, 26, 1, 16, 256)])
 def test_few_units_of_many_rows_are_cut_finely(ctx, kv, n, G, H, D, kind):
