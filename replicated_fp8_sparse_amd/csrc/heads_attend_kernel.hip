@@ -184,11 +184,20 @@ __device__ __forceinline__ float power(uint32_t byte) {
     return __uint_as_float(b << 23);
 }
 
-__device__ __forceinline__ const gbyte* uniform(const uint8_t* p) {
-    const gbyte* g = (const gbyte*)p;
-    asm volatile("" : "+s"(g));
-    return g;
+__device__ __forceinline__ const gbyte* uniform(const gbyte* p) {
+    asm volatile("" : "+s"(p));
+    return p;
 }
+
+// The lane's number, got anew where it is asked for.
+__device__ __forceinline__ uint32_t lane_anew() {
+    uint32_t l;
+    asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=&v"(l));
+    return l;
+}
+
+template <int D> __device__ __forceinline__ uint32_t key_at(uint32_t l16, uint32_t g4) { return l16 * D + g4 * 16; }
+template <int D> __device__ __forceinline__ uint32_t value_at(uint32_t l16, uint32_t g4) { return g4 * 4 * D + l16 * (D / 16); }
 
 // The codes of a tile of 32 positions in one wave's registers.
 template <int D>
@@ -198,20 +207,32 @@ struct Tile {
     uint32_t scales;                 // bytes of the keys and of the values
 
     // `page`: uniform; with a 32-bit offset a lane the loads need no 64-bit addresses.
+    // Of 256 values the offsets are computed again each time: beside 32 rows they would be spilled, and a spilled one's
+    // wait is for all loads on the way (prompts of 2 x 1024 over 2048, 16 heads over 4: 64.3 us for 68.2).
     __device__ __forceinline__ void load_keys(const uint8_t* page, uint32_t head, uint32_t groups, uint32_t half, uint32_t lane_at) {
-        const gbyte* kp = uniform(page + head * (128 * D) + half * (kTile * D));
+        if (D == 256) {
+            const uint32_t lane = lane_anew();
+            lane_at = key_at<D>(lane & 15u, lane >> 4);
+        }
+        const gbyte* kp = uniform((const gbyte*)page + head * (128 * D) + half * (kTile * D));
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < 2; ++u) {
+            if (D == 256 && u) kp = uniform(kp + 16 * D);      // beyond what an instruction's offset holds
 #pragma unroll
-            for (int c = 0; c < D / 64; ++c) k[u][c] = *(gptr<const i32x4>)(kp + lane_at + (u * 16 * D + c * 64));
+            for (int c = 0; c < D / 64; ++c) k[u][c] = *(gptr<const i32x4>)(kp + lane_at + ((D == 256 ? 0 : u * 16 * D) + c * 64));
+        }
         const uint32_t at = 2 * head;
         scales = *(kptr<uint32_t>)(page + groups * (128 * D) + (at & ~3u)) >> ((at & 2u) * 8);
     }
     __device__ __forceinline__ void load_values(const uint8_t* page, uint32_t head, uint32_t half, uint32_t lane_at) {
-        const gbyte* vp = uniform(page + head * (128 * D) + 64 * D + half * (kTile * D));
+        if (D == 256) {
+            const uint32_t lane = lane_anew();
+            lane_at = value_at<D>(lane & 15u, lane >> 4);
+        }
+        const gbyte* vp = uniform((const gbyte*)page + head * (128 * D) + 64 * D + half * (kTile * D));
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            if (D == 256 && j == 4) vp += 16 * D;          // beyond what an instruction's offset holds
+            if (D == 256 && j == 4) vp = uniform(vp + 16 * D);
             const gbyte* a = vp + lane_at + ((D == 256 ? 0 : (j >> 2) * 16) + (j & 3)) * D;
             if constexpr (D == 64) v[j][0] = *(gptr<const uint32_t>)a;
             else if constexpr (D == 128) {
@@ -266,11 +287,11 @@ __global__ __launch_bounds__(kThreads, waves_a_simd(D, RT)) void heads_attend_ke
     auto at = [&](int32_t page) { return p.base + ((uint32_t)page < p.heads.num_pages ? (uint64_t)(uint32_t)page * p.heads.page_stride : 0ull); };
     uint32_t t = cut * (p.chunk / kTile) + wave;
     int32_t page = page_of(t), page1 = page_of(t + W);
-    const uint32_t key_at = l16 * D + g4 * 16, value_at = g4 * 4 * D + l16 * (D / 16);
+    const uint32_t keys = key_at<D>(l16, g4), values = value_at<D>(l16, g4);
     Tile<D> tile;
     if (t < last) {
-        tile.load_keys(at(page), g, G, t & 1u, key_at);
-        tile.load_values(at(page), g, t & 1u, value_at);
+        tile.load_keys(at(page), g, G, t & 1u, keys);
+        tile.load_values(at(page), g, t & 1u, values);
     }
 
     // queries, and what each row sees: positions below lim (tree: of those before the tree, then its bits)
@@ -354,7 +375,7 @@ __global__ __launch_bounds__(kThreads, waves_a_simd(D, RT)) void heads_attend_ke
         }
         // the scale of a score in powers of 2 is kept above 0 and below infinity, so that a hidden score stays -infinity
         const float ks = fminf(fmaxf(fabsf(p.scale_log2) * power(tile.scales & 255u), FLT_MIN), FLT_MAX), vs = power((tile.scales >> 8) & 255u);
-        if (next < last) tile.load_keys(at(page1), g, G, next & 1u, key_at);
+        if (next < last) tile.load_keys(at(page1), g, G, next & 1u, keys);
 
         if (pos0 + kTile > least || bad) {
             // some row does not see the whole tile.  Bits of its 32 positions; those of this lane are
@@ -447,7 +468,7 @@ __global__ __launch_bounds__(kThreads, waves_a_simd(D, RT)) void heads_attend_ke
                         o[r][4 * c + d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[d], low[r], o[r][4 * c + d], 0, 0, 0);
                 }
         }
-        if (next < last) tile.load_values(at(page1), g, next & 1u, value_at);
+        if (next < last) tile.load_values(at(page1), g, next & 1u, values);
         page = page1;
         page1 = page2;
         t = next;
