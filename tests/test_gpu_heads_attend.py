@@ -167,6 +167,26 @@ def test_scores_of_all_sizes(ctx):
         U.check_all(cache, q, seqs, what=f"scale {scale}")
 
 
+@pytest.mark.parametrize("H", [8, 40])
+def test_scores_of_many_powers_of_two_a_step(ctx, H):
+    """Scores of some 2^27, below the documented 2^30: the largest is some 2^25 above the others, so its value comes out alone."""
+    cache = U.HeadsCache(4, 1, 64, replicas=1)
+    seqs = U.Seqs([200], [1], 4)
+    q = U.Query(1, H, 64, scale=1.0, mag=2.0 ** 24)
+    U.attend(ctx, cache, q, seqs)
+    kv, _ = cache.values(0, seqs.table[0], 200)
+    x = q.q[0, :, :64].double() @ kv[0, 0].T
+    two = x.topk(2, 1)
+    assert bool((two.values[:, 0] < 2.0 ** 30).all()) and bool((two.values[:, 0] - two.values[:, 1] > 2.0 ** 16).all())
+    want = kv[1, 0][two.indices[:, 0]]
+    # the one weight, 2^x, is rounded to bf16 beside a sum that is not: half a step, 2^-8, and the output's own half
+    tol = (U.half_step(q.dtype) + 2.0 ** -8) * (1 + 2.0 ** -8) * want.abs()
+    assert bool(((q.out[0].double() - want).abs() <= tol).all())
+    # a score: D + 24 roundings of the sum of its terms' magnitudes
+    tol = (64 + 24) * 2.0 ** -24 * (q.q[0, :, :64].double().abs() @ kv[0, 0].abs().T).amax(1)
+    assert bool(((q.lse[0].double() - two.values[:, 0]).abs() <= tol).all())
+
+
 def test_scales_far_apart(ctx):
     """Blocks of 2^-40 and of 2^30 beside each other: the weights decide, not the order."""
     cache = U.HeadsCache(6, 1, 128, replicas=1)
