@@ -76,12 +76,10 @@ constexpr uint32_t kTile = 32;                    // positions of a wave's step
 constexpr float kLazy = 8.0f;                     // rescale when a maximum grows past 2^8
 constexpr float kLn2 = 0.693147180559945309f;
 
-typedef __attribute__((address_space(1))) uint8_t gbyte;   // a byte in global memory
-template <class T> using gptr = __attribute__((address_space(1))) T*;
 
 // Waves that a SIMD should hold: what the registers of the accumulators leave room for
 // (16 rows of 128 values: 3; at 4 they spill, 133 us for 121 in the large decode).
-constexpr int waves_a_simd(int D, int RT) { return RT * D <= 64 ? 5 : (RT * D <= 128 ? 3 : (RT * D <= 512 ? 2 : 1)); }
+constexpr int waves_a_simd(int D, int RT) { return RT * D <= 64 ? 4 : (RT * D <= 128 ? 3 : (RT * D <= 512 ? 2 : 1)); }
 
 template <class E> struct Operand;
 template <> struct Operand<__bf16> {
@@ -134,17 +132,21 @@ __device__ __forceinline__ Unit unit_of(const HeadsAttendParams& p, const Places
     return u;
 }
 
-// A row's output from its joined parts, N values a lane.
-template <class E, int D, int N, class A>
-__device__ __forceinline__ void put_row(const HeadsAttendParams& p, const Unit& u, uint32_t g, uint32_t row, uint32_t seg, const A& acc,
+// A row's output from its joined parts: N pieces of 4 values a lane, 64 values apart, the first at `seg`.
+template <class E, int N>
+__device__ __forceinline__ void put_row(const HeadsAttendParams& p, const Unit& u, uint32_t g, uint32_t row, uint32_t seg, const f32x4 (&acc)[N],
                                         float top, float sum) {
     const uint32_t i = token_of(p, row), h = g * p.group + row - i * p.group;
     E* dst = (E*)p.out + (int64_t)(u.s.q0 + i) * p.out_token + (int64_t)h * p.out_head + seg;
     const float f = sum == 0.f ? 0.f : 1.f / sum;           // no position seen: 0
-    E y[N];
 #pragma unroll
-    for (int n = 0; n < N; ++n) y[n] = (E)(acc[n] * f);
-    __builtin_memcpy(__builtin_assume_aligned(dst, N * sizeof(E) < 16 ? N * sizeof(E) : 16), y, sizeof y);
+    for (int n = 0; n < N; ++n) {
+        const f32x4 x = acc[n] * f;
+        E y[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) y[k] = (E)x[k];
+        __builtin_memcpy(__builtin_assume_aligned(dst + n * 64, 8), y, sizeof y);
+    }
     if (seg == 0 && p.lse) p.lse[(int64_t)(u.s.q0 + i) * p.lse_token + h] = sum == 0.f ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * kLn2;
 }
 
@@ -184,9 +186,9 @@ __device__ __forceinline__ float power(uint32_t byte) {
     return __uint_as_float(b << 23);
 }
 
-__device__ __forceinline__ const gbyte* uniform(const gbyte* p) {
-    asm volatile("" : "+s"(p));
-    return p;
+// A descriptor of `bytes` bytes from p on, both uniform: loads beyond them give zeros.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t bytes_at(const uint8_t* p, uint32_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, bytes, 0x00027000);
 }
 
 // The lane's number, got anew where it is asked for.
@@ -204,42 +206,42 @@ template <int D>
 struct Tile {
     i32x4 k[2][D / 64];              // position 16 u + l%16, values 64 c + 16 (l/16) ..
     uint32_t v[8][D / 64];           // position j of this lane group, values (D/16) (l%16) ..
-    uint32_t scales;                 // bytes of the keys and of the values
+    uint32_t scales;                 // word that holds this head's bytes, for the keys and for the values: shifted only where
+                                     // they are used, as a shift here would wait for the load
 
-    // `page`: uniform; with a 32-bit offset a lane the loads need no 64-bit addresses.
+    // Through a descriptor of the tile's bytes, whose offsets are 32-bit; one of none (`any` false) gives zeros without a
+    // look at memory.  A branch about the loads would leave the compiler no number of loads on the way to count down
+    // to: it would wait for all of them (2 x 1024 tokens over 2048 of 256 values 60.5 us, so 57.0).
     // Of 256 values the offsets are computed again each time: beside 32 rows they would be spilled, and a spilled one's
-    // wait is for all loads on the way (prompts of 2 x 1024 over 2048, 16 heads over 4: 64.3 us for 68.2).
-    __device__ __forceinline__ void load_keys(const uint8_t* page, uint32_t head, uint32_t groups, uint32_t half, uint32_t lane_at) {
+    // wait is for all loads on the way, too.
+    __device__ __forceinline__ void load_keys(const uint8_t* page, uint32_t head, uint32_t groups, uint32_t half, uint32_t lane_at, bool any) {
         if (D == 256) {
             const uint32_t lane = lane_anew();
             lane_at = key_at<D>(lane & 15u, lane >> 4);
-        }
-        const gbyte* kp = uniform((const gbyte*)page + head * (128 * D) + half * (kTile * D));
+        } else asm volatile("" : "+v"(lane_at));             // sums with it stay with the instructions
+        const __amdgpu_buffer_rsrc_t from = bytes_at(page + head * (128 * D) + half * (kTile * D), any ? kTile * D : 0u);
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            if (D == 256 && u) kp = uniform(kp + 16 * D);      // beyond what an instruction's offset holds
+        for (int u = 0; u < 2; ++u)
 #pragma unroll
-            for (int c = 0; c < D / 64; ++c) k[u][c] = *(gptr<const i32x4>)(kp + lane_at + ((D == 256 ? 0 : u * 16 * D) + c * 64));
-        }
-        const uint32_t at = 2 * head;
-        scales = *(kptr<uint32_t>)(page + groups * (128 * D) + (at & ~3u)) >> ((at & 2u) * 8);
+            for (int c = 0; c < D / 64; ++c)
+                k[u][c] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(from, lane_at + c * 64, u * 16 * D, 0));
+        scales = *(kptr<uint32_t>)(page + groups * (128 * D) + (2 * head & ~3u));
     }
-    __device__ __forceinline__ void load_values(const uint8_t* page, uint32_t head, uint32_t half, uint32_t lane_at) {
+    __device__ __forceinline__ void load_values(const uint8_t* page, uint32_t head, uint32_t half, uint32_t lane_at, bool any) {
         if (D == 256) {
             const uint32_t lane = lane_anew();
             lane_at = value_at<D>(lane & 15u, lane >> 4);
-        }
-        const gbyte* vp = uniform((const gbyte*)page + head * (128 * D) + 64 * D + half * (kTile * D));
+        } else asm volatile("" : "+v"(lane_at));             // sums with it stay with the instructions
+        const __amdgpu_buffer_rsrc_t from = bytes_at(page + head * (128 * D) + 64 * D + half * (kTile * D), any ? kTile * D : 0u);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            if (D == 256 && j == 4) vp = uniform(vp + 16 * D);
-            const gbyte* a = vp + lane_at + ((D == 256 ? 0 : (j >> 2) * 16) + (j & 3)) * D;
-            if constexpr (D == 64) v[j][0] = *(gptr<const uint32_t>)a;
+            const uint32_t at = lane_at + (j & 3) * D, base = (j >> 2) * 16 * D;
+            if constexpr (D == 64) v[j][0] = __builtin_amdgcn_raw_buffer_load_b32(from, at, base, 0);
             else if constexpr (D == 128) {
-                const u32x2 w = *(gptr<const u32x2>)a;
+                const u32x2 w = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(from, at, base, 0));
                 v[j][0] = w.x, v[j][1] = w.y;
             } else {
-                const u32x4 w = *(gptr<const u32x4>)a;
+                const u32x4 w = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(from, at, base, 0));
                 v[j][0] = w.x, v[j][1] = w.y, v[j][2] = w.z, v[j][3] = w.w;
             }
         }
@@ -262,12 +264,14 @@ __global__ __launch_bounds__(kThreads, waves_a_simd(D, RT)) void heads_attend_ke
     constexpr int NB = D / 16, NQ = D / 32, W = kWaves;
     constexpr bool Shared = RT > 1 && RT * D >= 256;
     constexpr bool Low = RT == 1 || !__is_same(E, __bf16);         // the weights' low parts as a second operand: see above
+    // two of them where blocks leave the room: a wave may write the next rows before all have read these
+    constexpr int kJoins = RT > 1 && D < 256 ? 2 : 1;
     struct Join {
         float o[W][16][D + 4];
         float ml[W][16][2];
     };
     union Lds {
-        Join join;
+        Join join[kJoins];
         typename Op::x8 q[Shared ? RT * NQ : 1][64];
         __device__ Lds() {}
     };
@@ -289,14 +293,28 @@ __global__ __launch_bounds__(kThreads, waves_a_simd(D, RT)) void heads_attend_ke
     int32_t page = page_of(t), page1 = page_of(t + W);
     const uint32_t keys = key_at<D>(l16, g4), values = value_at<D>(l16, g4);
     Tile<D> tile;
-    if (t < last) {
-        tile.load_keys(at(page), g, G, t & 1u, keys);
-        tile.load_values(at(page), g, t & 1u, values);
-    }
+    tile.load_keys(at(page), g, G, t & 1u, keys, t < last);
 
-    // queries, and what each row sees: positions below lim (tree: of those before the tree, then its bits)
-    typename Op::x8 q[Shared ? 1 : RT][NQ];
+    // queries, and what each row sees: positions below lim (tree: of those before the tree, then its bits); rows of none
+    // take the sequence's first
     const uint32_t signs = p.scale_log2 < 0.f ? 0x80008000u : 0u;
+    const auto query = [&](uint32_t r, uint32_t c) {
+        const uint32_t row = u.row0 + r * 16 + l16, i = row < u.rows ? token_of(p, row) : 0u, h = g * p.group + (row < u.rows ? row - i * p.group : 0u);
+        const E* src = (const E*)p.q + (int64_t)(u.s.q0 + i) * p.q_token + (int64_t)h * p.q_head + g4 * 16;
+        return load_query<E>(src + (c >> 1) * 64 + (c & 1u) * 8, signs);
+    };
+    constexpr uint32_t kMine = RT * NQ / W;
+    typename Op::x8 q[Shared ? 1 : RT][NQ], mine[Shared ? kMine : 1];
+    if constexpr (Shared) {
+#pragma unroll
+        for (uint32_t i = 0; i < kMine; ++i) mine[i] = query((wave + i * W) / NQ, (wave + i * W) % NQ);
+    } else {
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int c = 0; c < NQ; ++c) q[r][c] = query(r, c);
+    }
+    tile.load_values(at(page), g, t & 1u, values, t < last);
     uint32_t lim[RT];
     uint32_t tree[RT];                     // first word of the row's bits
     uint32_t least = 0xFFFFFFFFu;          // positions that all rows see
@@ -304,20 +322,17 @@ __global__ __launch_bounds__(kThreads, waves_a_simd(D, RT)) void heads_attend_ke
     for (int r = 0; r < RT; ++r) {
         const uint32_t row = u.row0 + r * 16 + l16;
         const bool is = row < u.rows;
-        const uint32_t i = is ? token_of(p, row) : 0u, h = g * p.group + (is ? row - i * p.group : 0u);     // rows of none take the first's
-        const E* src = (const E*)p.q + (int64_t)(u.s.q0 + i) * p.q_token + (int64_t)h * p.q_head + g4 * 16;
-#pragma unroll
-        for (int c = 0; c < NQ; ++c) {
-            const E* from = src + (c >> 1) * 64 + (c & 1) * 8;
-            if constexpr (!Shared) q[r][c] = load_query<E>(from, signs);
-            else if ((r * NQ + c) % W == (int)wave) lds.q[r * NQ + c][lane] = load_query<E>(from, signs);
-        }
+        const uint32_t i = is ? token_of(p, row) : 0u;
         const int64_t top = u.base + (p.tree ? 0 : (int64_t)i + 1);
         lim[r] = is ? (top > 0 ? (uint32_t)top : 0u) : 0xFFFFFFFFu;
         tree[r] = (u.s.q0 + i) * p.tree_words;
         least = lim[r] < least ? lim[r] : least;
     }
-    if constexpr (Shared) __syncthreads();
+    if constexpr (Shared) {
+#pragma unroll
+        for (uint32_t i = 0; i < kMine; ++i) lds.q[wave + i * W][lane] = mine[i];
+        __syncthreads();
+    }
 #pragma unroll
     for (int d = 1; d < 16; d <<= 1) {
         const uint32_t o = __shfl_xor(least, d);
@@ -338,7 +353,6 @@ __global__ __launch_bounds__(kThreads, waves_a_simd(D, RT)) void heads_attend_ke
     // as a function of its own, inlined: the compiler then keeps its scalars in registers (1-2 % of every call)
     const auto step = [&]() __attribute__((always_inline)) {
         const uint32_t pos0 = t * kTile, next = t + W;
-        const int32_t page2 = page_of(next + W);
         const bool bad = (uint32_t)page >= p.heads.num_pages;
         // a bad page is hidden; counted by the rows that see most of the sequence, at a page's first half
         if (bad && counts && !(t & 1u) && any_sees(p, u, pos0) && lane == 0) atomicAdd(p.invalid_count, 1ull);
@@ -375,8 +389,10 @@ __global__ __launch_bounds__(kThreads, waves_a_simd(D, RT)) void heads_attend_ke
             }
         }
         // the scale of a score in powers of 2 is kept above 0 and below infinity, so that a hidden score stays -infinity
-        const float ks = fminf(fmaxf(fabsf(p.scale_log2) * power(tile.scales & 255u), FLT_MIN), FLT_MAX), vs = power((tile.scales >> 8) & 255u);
-        if (next < last) tile.load_keys(at(page1), g, G, next & 1u, keys);
+        const uint32_t scales = tile.scales >> ((2 * g & 2u) * 8);
+        const float ks = fminf(fmaxf(fabsf(p.scale_log2) * power(scales & 255u), FLT_MIN), FLT_MAX), vs = power((scales >> 8) & 255u);
+        const int32_t page2 = page_of(next + W);
+        tile.load_keys(at(page1), g, G, next & 1u, keys, next < last);
 
         if (pos0 + kTile > least || bad) {
             // some row does not see the whole tile.  Bits of its 32 positions; those of this lane are
@@ -469,51 +485,62 @@ __global__ __launch_bounds__(kThreads, waves_a_simd(D, RT)) void heads_attend_ke
                         o[r][4 * c + d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[d], low[r], o[r][4 * c + d], 0, 0, 0);
                 }
         }
-        if (next < last) tile.load_values(at(page1), g, next & 1u, values);
+        tile.load_values(at(page1), g, next & 1u, values, next < last);
         page = page1;
         page1 = page2;
         t = next;
     };
+    // the queries are waited for here: left to the loop, the wait would be in every step and for all loads on the way
+    if constexpr (!Shared) {
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int c = 0; c < NQ; ++c) asm volatile("" : "+v"(q[r][c]));
+    }
     while (t < last) step();
 
-    // the waves' parts, 16 rows at a time
-    const uint32_t row = tid >> 4, seg = (tid & 15u) * NB;
+    // the waves' parts, 16 rows at a time: 16 lanes a row, which read 64 values side by side
+    const uint32_t row = tid >> 4, seg = (tid & 15u) * 4;
     if constexpr (Shared) __syncthreads();          // their queries' last reads
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
         if (u.row0 + r * 16 >= u.rows) break;
+        Join& join = lds.join[r % kJoins];
         l[r] += __shfl_xor(l[r], 16);
         l[r] += __shfl_xor(l[r], 32);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int n = 0; n < NB; ++n) lds.join.o[wave][l16][(g4 * 4 + i) * NB + n] = o[r][n][i];
-        if (g4 == 0) lds.join.ml[wave][l16][0] = m[r], lds.join.ml[wave][l16][1] = l[r];
+            for (int n = 0; n < NB; ++n) join.o[wave][l16][(g4 * 4 + i) * NB + n] = o[r][n][i];
+        if (g4 == 0) join.ml[wave][l16][0] = m[r], join.ml[wave][l16][1] = l[r];
         __syncthreads();
         const uint32_t mine = u.row0 + r * 16 + row;
         if (mine < u.rows) {
-            float top = lds.join.ml[0][row][0], sum = 0.f, acc[NB];
+            float top = join.ml[0][row][0], sum = 0.f;
+            f32x4 acc[D / 64];
 #pragma unroll
-            for (uint32_t w = 1; w < W; ++w) top = fmaxf(top, lds.join.ml[w][row][0]);
+            for (uint32_t w = 1; w < W; ++w) top = fmaxf(top, join.ml[w][row][0]);
 #pragma unroll
-            for (int n = 0; n < NB; ++n) acc[n] = 0.f;
+            for (int n = 0; n < D / 64; ++n) acc[n] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (uint32_t w = 0; w < W; ++w) {
-                const float f = __builtin_amdgcn_exp2f(lds.join.ml[w][row][0] - top);
-                sum = fmaf(lds.join.ml[w][row][1], f, sum);
+                const float f = __builtin_amdgcn_exp2f(join.ml[w][row][0] - top);
+                sum = fmaf(join.ml[w][row][1], f, sum);
 #pragma unroll
-                for (int n = 0; n < NB; ++n) acc[n] = fmaf(lds.join.o[w][row][seg + n], f, acc[n]);
+                for (int n = 0; n < D / 64; ++n)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) acc[n][k] = fmaf(join.o[w][row][seg + n * 64 + k], f, acc[n][k]);
             }
             if (u.chunks > 1) {
                 const uint64_t slot = (((uint64_t)place * G + g) * p.chunks + cut) * R + r * 16 + row;
 #pragma unroll
-                for (int n = 0; n < NB; ++n) p.part[slot * D + seg + n] = acc[n];
+                for (int n = 0; n < D / 64; ++n) *(f32x4*)(p.part + slot * D + seg + n * 64) = acc[n];
                 if (seg == 0) p.part_ml[slot * 2] = top, p.part_ml[slot * 2 + 1] = sum;
             } else {
-                put_row<E, D, NB>(p, u, g, mine, seg, acc, top, sum);
+                put_row<E>(p, u, g, mine, seg, acc, top, sum);
             }
         }
-        __syncthreads();
+        if constexpr (kJoins == 1) __syncthreads();
     }
 }
 
@@ -534,7 +561,7 @@ __global__ __launch_bounds__(256) void join_kernel(const HeadsAttendParams p, co
     const uint32_t rows = u.rows - u.row0 < R ? u.rows - u.row0 : R;
     const uint32_t r = blockIdx.y * (kGroups >> shift) + (group >> shift);
     float top = -FLT_MAX, sum = 0.f;
-    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+    f32x4 acc[1] = {{0.f, 0.f, 0.f, 0.f}};
     if (r < rows) {
         const uint64_t slot = ((uint64_t)place * G + g) * p.chunks * R + r;
         float m[kEach], l[kEach];
@@ -571,16 +598,16 @@ __global__ __launch_bounds__(256) void join_kernel(const HeadsAttendParams p, co
             }
 #pragma unroll
             for (uint32_t i = 0; i < kBatch; ++i)
-                if (c0 + i < end) acc += x[i] * factors[group][c0 + i];
+                if (c0 + i < end) acc[0] += x[i] * factors[group][c0 + i];
         }
     }
     if constexpr (Split) {
-        sums[threadIdx.x] = acc;
+        sums[threadIdx.x] = acc[0];
         __syncthreads();
         if (part != 0) return;
-        for (uint32_t i = 1; i < 1u << shift; ++i) acc += sums[threadIdx.x + i * kLanes];
+        for (uint32_t i = 1; i < 1u << shift; ++i) acc[0] += sums[threadIdx.x + i * kLanes];
     }
-    if (r < rows) put_row<E, D, 4>(p, u, g, u.row0 + r, lane * 4, acc, top, sum);
+    if (r < rows) put_row<E>(p, u, g, u.row0 + r, lane * 4, acc, top, sum);
 }
 
 Places unit_places(uint32_t rows, uint32_t group, uint64_t num_seqs, uint64_t num_tokens, uint64_t max_q, uint64_t* total) {
