@@ -29,10 +29,11 @@
 // instructions (80 of them the widening, 128 the weights) and 64 matrix instructions, which exclude each
 // other more than they overlap: beside a wave that issues 16 x 16 x 32 products
 // back to back the other waves of its SIMD issue nothing for 14 of 16 cycles (32 x 32 x 16:
-// 21 of 32), so 2100 cycles of work a tile and two waves a SIMD that need 2400.  Prompts of 2 x 4096
-// tokens behind as much context, 16 heads over 4: 240-260 us, 69-77 % of a large bf16 product's rate.
-// (Built and measured beside it: 32 x 32 x 16 products throughout, 247; the same with the next
-// tile's scores between this one's weights, one wave a SIMD, 300; 32 rows a unit, 300-315.)
+// 21 of 32), so 2100 cycles of work a tile, of which two waves a SIMD reach some 2250.  Prompts of
+// 2 x 4096 tokens behind as much context, 16 heads over 4: 223-255 us, 72-82 % of a large bf16 product's rate.
+// (Built and measured when it took 254-260: 32 x 32 x 16 products throughout, 247; the same with the next
+// tile's scores between this one's weights, one wave a SIMD, 300; 32 rows a unit, 300-315.)  Short
+// prompts: a block's start (lengths, pages, queries, the first tile: 5 us) and the join of 64 rows (3).
 #include <algorithm>
 #include <cfloat>
 
@@ -52,26 +53,32 @@ typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
 constexpr uint32_t kWaves = 4, kThreads = kWaves * 64;
-// How a call is cut (plan_heads_attend), by its bounds.  Measured, us; 128 values, 8 query heads a key-value head:
-//   one token over 8192, 2 heads: cuts of 256 / 512 / 1024 positions 11.1 / 11.1 / 13.3;
-//   over 700: in two 9.7, whole 8.5; over 65536: 64 cuts 19.5, 128 cuts 15.8
-constexpr uint32_t kLeastChunk = 512, kWhole = 768, kMostChunks = 128;
-//   cuts of at least 16 / 32 / 64 positions a row, as each row of a cut writes a part: 8 tokens of 16 sequences
-//   over 8192 (32 rows) 82 / 72 / 66
+// How a call is cut (plan_heads_attend), by its bounds: for kFill blocks, one a compute unit, into cuts of kLeastChunk
+// positions; for twice as many into cuts of 2 kChunk; for kWanted (units of 16 rows) or kWantedWide (of more) into cuts of at
+// least kChunk and of kChunkRows for each row, as each row of a cut writes a part.  Measured, us (8 query heads a
+// key-value head and 128 values where nothing else is said):
+//   one token over 8192, 2 heads: cuts of 256 / 512 / 1024 positions 9.9 / 10.8 / 12.9, over 1000 8.7 / 10.0 / -; kept for
+//   the few blocks: 8 x 4096, 32 over 8 heads, 512 blocks 15.9 / 15.0, 16 x 8192 of 256 values 46.1 / 43.5;
+//   over 700: in two 9.5, whole 8.5; over 65536: 64 cuts 17.1, 128 cuts 14.9
+constexpr uint32_t kLeastChunk = 256, kChunk = 512, kWhole = 768, kMostChunks = 128;
+//   16 / 32 / 64 positions a row: 8 tokens of 16 sequences over 8192 (32 rows) 66 / 66 / 61, chunks of 4 x 256 over
+//   4096 98 / 100 / 81
 constexpr uint32_t kChunkRows = 64;
-//   cut for up to 2048 / 4096 / 8192 blocks of 16 rows: one token of 64 sequences of up to 8192 122.5 / 120.3 / 124.9;
-//   for 768 / 1024 / 1536 of more rows: 16 trees of 24 65 / 54 / 57, and at 2048 prompts of 2 x 4096 go in two, 317 for 260
+//   cut for up to 2048 / 4096 / 8192 blocks of 16 rows: one token of 64 sequences of up to 8192 121.6 / 121.0 / 126.3;
+//   for 768 / 1024 of more rows: 16 trees of 24 63 / 52
 constexpr uint32_t kWanted = 4096, kWantedWide = 1024;
-//   and for kFill blocks, one a compute unit, into cuts of kLeastChunk whatever the rows: trees of 2 x 26 tokens, 16 heads over 1
-//   of 256, 6215 positions 24.6 / 46.9 without, 1 x 5, 32 over 2 of 128, 5772 14.4 / 23.6; for 512 blocks no more of
-//   those, but prompts of 6 x 534 behind 409 positions 20.7 / 16.5, so for those only cuts of twice as many: trees of
-//   23 x 28 tokens, 2 heads of 64, over 8926 18.1 / 23.0
+//   with kFill 1 / 256 / 512: trees of 2 x 26 tokens, 16 heads over 1 of 256, 6215 positions 27 / 19 / 19, 1 x 5, 32 over 2,
+//   5772 20.8 / 12.9 / 12.9, prompts of 6 x 534 behind 409 positions 14.9 / 14.8 / 18.6; without the cuts for twice as
+//   many: trees of 23 x 28 tokens, 2 heads of 64, over 8926 20.6 / 17.9
 constexpr uint32_t kFill = 256;
 //   units of 64 rows from kFull blocks on, as many as the card holds at once, twice as many for 64 values, of which it
 //   holds three blocks of 32 rows a compute unit; else of 32.  32 / 64 rows: chunks of 4 x 256 over 4096, 32 heads over 8
-//   of 128 (512 blocks of 64) 107 / 86, 2 x 1547 over 4701, 15 over 3 (726) 151 / 131, in fp16 167 / 163, of 64 values 82 / 94;
-//   prompts of 1 x 2048, 24 over 4 of 64 (768) 32 / 36; below: 4 x 676 over 1243, 20 over 4 (about 420) 33 / 37
+//   (512 blocks of 64) 102 / 81, 2 x 1547 over 4701, 15 over 3 (726) 142 / 115, in fp16 166 / 150; prompts of 1 x 2048, 24
+//   over 4 of 64 (768) 30 / 34; below: 4 x 676 over 1243, 20 over 4 (about 420) 30 / 33, 16 trees of 24 52 / 76
 constexpr uint32_t kFull = 512;
+// what is cut writes at most kPartRows rows of parts, whatever its units' rows: the workspace's size goes by it
+constexpr uint32_t kPartRows = kWanted * 16;
+static_assert(kWantedWide * 64 <= kPartRows && 2 * kFill * 64 <= kPartRows, "units of 64 rows, each cut of which writes as many");
 constexpr uint32_t kTile = 32;                    // positions of a wave's step
 constexpr float kLazy = 8.0f;                     // rescale when a maximum grows past 2^8
 constexpr float kLn2 = 0.693147180559945309f;
@@ -662,17 +669,17 @@ HeadsAttendPlan plan_heads_attend(const HeadsParams& h, uint32_t group, uint64_t
     (void)unit_places(a.rows, group, num_seqs, num_tokens, max_q, &a.units);
     const uint64_t blocks = std::max<uint64_t>(1, a.units * h.groups);
     const auto cuts = [&](uint64_t most, uint64_t wanted) { return std::min(std::min<uint64_t>(most, kMostChunks), wanted / blocks); };
-    const uint64_t by_rows = std::max<uint64_t>(kLeastChunk, std::min<uint64_t>(rows, a.rows) * kChunkRows);
+    const uint64_t by_rows = std::max<uint64_t>(kChunk, std::min<uint64_t>(rows, a.rows) * kChunkRows);
     uint64_t n = 1;
     if (max_kv > kWhole) {
         n = std::max(n, cuts((max_kv + by_rows - 1) / by_rows, a.rows == 16 ? kWanted : kWantedWide));
         n = std::max(n, cuts((max_kv + kLeastChunk - 1) / kLeastChunk, kFill));
-        n = std::max(n, cuts(max_kv / (2 * kLeastChunk), 2 * kFill));
+        n = std::max(n, cuts(max_kv / (2 * kChunk), 2 * kFill));
     }
     a.chunk = (uint32_t)std::max<uint64_t>(kLeastChunk, ((max_kv + n - 1) / n + 127) / 128 * 128);
     a.chunks = (uint32_t)std::max<uint64_t>(1, (max_kv + a.chunk - 1) / a.chunk);
     // parts of as many rows as the bounds allow, which grows with each of them; the rows of a unit that none has count too
-    const uint64_t parts = std::min<uint64_t>(kWanted * 16, (num_tokens * group + num_seqs * 64) * h.groups * std::min<uint64_t>(kMostChunks, (max_kv + kLeastChunk - 1) / kLeastChunk + 1));
+    const uint64_t parts = std::min<uint64_t>(kPartRows, (num_tokens * group + num_seqs * 64) * h.groups * std::min<uint64_t>(kMostChunks, (max_kv + kLeastChunk - 1) / kLeastChunk + 1));
     a.bytes = parts * (h.dim + 2) * 4;
     return a;
 }
