@@ -58,7 +58,7 @@ __device__ __forceinline__ uint32_t recode4(uint32_t old, float factor) {
     return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(b[0] * factor, b[1] * factor, w, true);
 }
 
-template <uint32_t D> constexpr uint32_t kMany = D == 256 ? 1024 : 512;
+template <uint32_t D> constexpr uint32_t kMany = D == 256 ? 1024 : 512;         // threads of a block, at most 1024
 
 // N threads, half of them for the keys, half for the values; Rounds: of rows that they pass,
 // enough for the new ones.
@@ -200,7 +200,8 @@ hipError_t launch_heads_append(const HeadsAppendParams& p, hipStream_t stream) {
     // what fills half of the L2s or more is stored past them (8 prompts of up to 4096 tokens, 38 MB: 28.2 us
     // for 32.8; 4 of 2048, 64 values a head, 10 MB: 7.4 for 7.1)
     const bool past = (uint64_t)p.seqs.num_tokens * G * p.heads.dim * 2 * p.replicas > (16u << 20);
-    const uint64_t most = ((1u << 23) - 1) / G;                       // a launch holds fewer than 2^32 threads
+    // a launch holds fewer than 2^32 threads, 1024 a block at most: a larger grid is cut modulo 2^32, with no error
+    const uint64_t most = ((1u << 22) - 1) / G;
     for (uint64_t first = 0; first < total; first += most) {
         HeadsAppendParams q = p;
         q.first = (uint32_t)first;
