@@ -13,7 +13,8 @@
 // four RoPE rows (lanes 0..31).  Large batches: a wave takes a group's six pieces;
 // small ones: a wave a piece, as what counts there is one wave's chain.  By groups the
 // rows are put together in LDS first: stored as they lie in the lanes (8 bytes, 4, 16) 32768 tokens
-// into 4 replicas took 52 us.
+// into 4 replicas took 52 us.  A fence on another lane may poison the context at any time: the status is read
+// once for all pieces of a token, so its two rows are stored whole or left as they were.
 //
 // Bound.  Few tokens: a launch, three dependent reads and one wave's tile, 4.0-4.3 us up to
 // 256.  Many: the quantization between the reads and the writes: 8192 tokens into 4 replicas,
@@ -108,6 +109,7 @@ template <bool Split, bool Stream>
 __global__ __launch_bounds__(Split ? kPieces * 64 : 256) void store_rotated_kernel(const StoreRotatedParams p) {
     const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     __shared__ __attribute__((aligned(16))) uint8_t image[Split ? 1 : 4][Split ? 16 : 2624 + 512];
+    __shared__ CtxHead decided;
     const uint32_t T = (uint32_t)p.s.num_tokens, t0 = (Split ? blockIdx.x : blockIdx.x * 4 + wave) * 4;
     if (t0 >= T) return;
     const uint32_t last = T - 1;
@@ -118,6 +120,8 @@ __global__ __launch_bounds__(Split ? kPieces * 64 : 256) void store_rotated_kern
     int64_t slot[4];
     u32x4 lat[4];
     Turning ix, rp;
+    CtxHead head;
+    if (!Split || threadIdx.x == 0) head = *p.s.head;
 #pragma unroll
     for (uint32_t k = 0; k < 4; ++k) {
         slot[k] = p.s.slots[token(k)];
@@ -125,7 +129,11 @@ __global__ __launch_bounds__(Split ? kPieces * 64 : 256) void store_rotated_kern
     }
     if (mine(4)) ix.load(p.s.indexer + (uint64_t)token(row) * p.s.indexer_stride, in, p.indexer, p.positions[token(row)]);
     if (mine(5)) rp.load(p.s.rope + (uint64_t)token(rr) * p.s.rope_stride, lane & 7u, p.rope, p.positions[token(rr)]);
-    const CtxHead head = *p.s.head;
+    if constexpr (Split) {
+        if (threadIdx.x == 0) decided = head;
+        __syncthreads();
+        head = decided;
+    }
     if (head.status & kStatusPoisoned) return;               // a fence timed out: fail closed
     // a token's Main-KV row, its Indexer-K page and the place in it
     uint64_t main_at[4], page_at[4];
