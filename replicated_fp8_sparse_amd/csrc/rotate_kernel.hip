@@ -75,11 +75,13 @@ void launch(RotateParams p, hipStream_t stream) {
     const uint32_t rows = kThreads / p.units;
     // four heads a thread, which share its angles, once that still leaves every compute unit two blocks
     // (4096 tokens of 32 heads of 128, bf16: 13.2 us for 16.8; in 32 bits the bytes bound it: 28.5 for 27.4)
-    const bool four = sizeof(T) == 2 && p.heads >= 4 && (uint64_t)p.num_tokens * ((p.heads + 3) / 4) >= 512 * rows;
+    constexpr bool kMayFour = sizeof(T) == 2;
+    const bool four = kMayFour && p.heads >= 4 && (uint64_t)p.num_tokens * ((p.heads + 3) / 4) >= 512 * rows;
     p.across = std::min(four ? (p.heads + 3) / 4 : p.heads, rows);
     p.tokens = rows / p.across;
-    if (four) launch<T, 4>(p, stream);
-    else launch<T, 1>(p, stream);
+    if constexpr (kMayFour)
+        if (four) return launch<T, 4>(p, stream);
+    launch<T, 1>(p, stream);
 }
 
 }  // namespace
