@@ -14,6 +14,7 @@ for the keys and one for the values of each head.
 true: the library's kernels.  ``exact`` computes each result in 64 bits.
 """
 import math
+import weakref
 
 import numpy as np
 import torch
@@ -268,9 +269,7 @@ class _Context:
         cfg = kvpub.kvpub_config_init(len(self.main), 1, s["case"].get("pages", 1))
         st, self.ctx = kvpub.kvpub_create(cfg, [b.data_ptr() for b in self.main], [b.data_ptr() for b in self.idx])
         kvpub.check(st, "kvpub_create")
-
-    def __del__(self):
-        self.k.kvpub_destroy(self.ctx)
+        weakref.finalize(self, kvpub.kvpub_destroy, self.ctx)         # at the latest before the interpreter takes modules down
 
 
 def _rotation(s, name, dim, start, layout):
