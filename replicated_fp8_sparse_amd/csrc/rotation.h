@@ -27,7 +27,7 @@ __device__ __forceinline__ Turn turn_of(int32_t position, uint64_t turns) {
     const uint32_t u = __umulhi((uint32_t)position, lo) + (uint32_t)position * hi - (position < 0 ? lo : 0u);
     // the nearest quarter is the two high bits of u + an eighth; the low 30 bits of u, as a signed number, are the rest
     const uint32_t w = u + (1u << 29);
-    const float x = (float)(int32_t)(u << 2) * 3.65729506981679867e-10f;       // 2 pi / 2^34
+    const float x = (float)(int32_t)(u << 2) * 3.65729519816789921e-10f;       // 2 pi / 2^34
     const float z = x * x;
     const float s = fmaf(x * z, fmaf(z, fmaf(z, fmaf(z, 1.f / 362880.f, -1.f / 5040.f), 1.f / 120.f), -1.f / 6.f), x);
     const float c = fmaf(z, fmaf(z, fmaf(z, fmaf(z, fmaf(z, -1.f / 3628800.f, 1.f / 40320.f), -1.f / 720.f), 1.f / 24.f), -0.5f), 1.f);
