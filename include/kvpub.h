@@ -454,7 +454,7 @@ KVPUB_API kvpub_status kvpub_attend_expanded(kvpub_ctx *ctx, const kvpub_expande
  *   y1 = magnitude * (x1 cos a - x2 sin a),  y2 = magnitude * (x1 sin a + x2 cos a).
  * The frequencies are a table of turns a position in units of 2^-64, so that an
  * angle is one 64-bit product whatever the position: far ones lose nothing.
- * Angles are held to 2^-32 of a turn, sines, cosines and products in binary32.
+ * Angles are rounded to 2^-32 of a turn, sines, cosines and products are binary32.
  * Positions are int32 and may be negative (they turn back). */
 #define KVPUB_ROTATE_PAIRS 0u   /* pair i: values start + 2i and start + 2i + 1 */
 #define KVPUB_ROTATE_HALVES 1u  /* pair i: values start + i and start + dim/2 + i */
