@@ -53,32 +53,41 @@ typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
 constexpr uint32_t kWaves = 4, kThreads = kWaves * 64;
-// How a call is cut (plan_heads_attend), by its bounds: for kFill blocks, one a compute unit, into cuts of kLeastChunk
-// positions; for twice as many into cuts of 2 kChunk; for kWanted (units of 16 rows) or kWantedWide (of more) into cuts of at
-// least kChunk and of kChunkRows for each row, as each row of a cut writes a part.  Measured, us (8 query heads a
-// key-value head and 128 values where nothing else is said):
-//   one token over 8192, 2 heads: cuts of 256 / 512 / 1024 positions 9.9 / 10.8 / 12.9, over 1000 8.7 / 10.0 / -; kept for
-//   the few blocks: 8 x 4096, 32 over 8 heads, 512 blocks 15.9 / 15.0, 16 x 8192 of 256 values 46.1 / 43.5;
-//   over 700: in two 9.5, whole 8.5; over 65536: 64 cuts 17.1, 128 cuts 14.9
+// How a call is cut (plan_heads_attend), by its bounds alone.  Blocks are units times key-value heads.
+//
+// Up to kWhole positions a sequence stays whole; beyond, the blocks of units of 16 and 32 rows are cut into as many parts as
+// the most of three rules asks for, at most kMostChunks: with few blocks for a block a compute unit (kFill), in cuts of
+// kLeastChunk positions; for two a compute unit, in cuts of 2 kChunk; and for kWanted blocks of 16 rows, or kWantedWide of
+// 32, in cuts of at least kChunk and of kChunkRows for each row, as each row of a cut writes a part.  Units of 64
+// rows, 512 blocks and more, are not cut.  Measured, us (8 query heads a key-value head and 128 values where nothing
+// else is said):
+//   kWhole 768, one token, whole / cut: over 640 positions, 2 heads 7.5 / 8.4, 768 8.2 / 8.4, 769 9.1 / 8.5, 1024 9.7 / 8.5;
+//   heads of 64 values over 768 6.9 / 7.8, 1024 8.0 / 7.8, of 256 640 9.9 / 9.8, 768 11.0 / 9.9; 16 sequences, 32 over 8,
+//   768 10.3 / 12.0, 1024 12.3 / 13.3, 1300 15.2 / 15.1
+//   kLeastChunk 256 / 512 / 1024, one token over 8192, 2 heads: 9.9 / 10.8 / 12.9, over 1000 8.7 / 10.0 / -; for the few
+//   blocks alone: 8 x 4096, 32 over 8 heads, 512 blocks 15.9 / 15.0, 16 x 8192 of 256 values 46.1 / 43.5
+//   kMostChunks 64 / 128, one token over 65536: 17.1 / 14.9
 constexpr uint32_t kLeastChunk = 256, kChunk = 512, kWhole = 768, kMostChunks = 128;
-//   16 / 32 / 64 positions a row: 8 tokens of 16 sequences over 8192 (32 rows) 66 / 66 / 61, chunks of 4 x 256 over
-//   4096 98 / 100 / 81
+//   16 / 32 / 64 positions a row: 8 tokens of each of 16 sequences of 8192 (32 rows) 66 / 66 / 61
 constexpr uint32_t kChunkRows = 64;
 //   cut for up to 2048 / 4096 / 8192 blocks of 16 rows: one token of 64 sequences of up to 8192 121.6 / 121.0 / 126.3;
-//   for 768 / 1024 of more rows: 16 trees of 24 63 / 52
+//   for 768 / 1024 of 32 rows: 16 trees of 24 63 / 52
 constexpr uint32_t kWanted = 4096, kWantedWide = 1024;
 //   with kFill 1 / 256 / 512: trees of 2 x 26 tokens, 16 heads over 1 of 256, 6215 positions 27 / 19 / 19, 1 x 5, 32 over 2,
 //   5772 20.8 / 12.9 / 12.9, prompts of 6 x 534 behind 409 positions 14.9 / 14.8 / 18.6; without the cuts for twice as
 //   many: trees of 23 x 28 tokens, 2 heads of 64, over 8926 20.6 / 17.9
 constexpr uint32_t kFill = 256;
 //   units of 64 rows from kFull blocks on, as many as the card holds at once, twice as many for 64 values, of which it
-//   holds three blocks of 32 rows a compute unit; else of 32.  32 / 64 rows: chunks of 4 x 256 over 4096, 32 heads over 8
-//   (512 blocks of 64) 102 / 81, 2 x 1547 over 4701, 15 over 3 (726) 142 / 115, in fp16 166 / 150; prompts of 1 x 2048, 24
-//   over 4 of 64 (768) 30 / 34; below: 4 x 676 over 1243, 20 over 4 (about 420) 30 / 33, 16 trees of 24 52 / 76
+//   holds three blocks of 32 rows a compute unit; else of 32.  4 chunks of n tokens, 32 heads over 8, the last of
+//   kv positions, 32 / 64 rows: n = 192 (384 blocks of 64), kv = 2048 48 / 45, 8192 141 / 123; n = 240 (480) 55 / 45,
+//   179 / 153; n = 256 (512) 53 / 45, 182 / 142; n = 272 (544) 64 / 58, 221 / 192.  Below 512 the others lose:
+//   4 x 676 over 1243, 20 over 4 (about 420) 30 / 33, 16 trees of 24 52 / 76.  2 x 1547 over 4701, 15 over 3 (726) 142 / 115, in
+//   fp16 166 / 150; prompts of 1 x 2048, 24 over 4 of 64 (768) 30 / 34.  512 blocks of 64 rows in two cuts: the n = 256 above
+//   over 5000 110, whole 91, over 8192 160, whole 142; ragged, over up to 5000 93 / 82, 16384 225 / 220
 constexpr uint32_t kFull = 512;
 // what is cut writes at most kPartRows rows of parts, whatever its units' rows: the workspace's size goes by it
 constexpr uint32_t kPartRows = kWanted * 16;
-static_assert(kWantedWide * 64 <= kPartRows && 2 * kFill * 64 <= kPartRows, "units of 64 rows, each cut of which writes as many");
+static_assert(kWantedWide * 32 <= kPartRows && 2 * kFill * 32 <= kPartRows, "units of 32 rows, each cut of which writes as many");
 constexpr uint32_t kTile = 32;                    // positions of a wave's step
 constexpr float kLazy = 8.0f;                     // rescale when a maximum grows past 2^8
 constexpr float kLn2 = 0.693147180559945309f;
@@ -538,7 +547,7 @@ __global__ __launch_bounds__(kThreads, waves_a_simd(D, RT)) void heads_attend_ke
 #pragma unroll
                     for (int k = 0; k < 4; ++k) acc[n][k] = fmaf(join.o[w][row][seg + n * 64 + k], f, acc[n][k]);
             }
-            if (u.chunks > 1) {
+            if (RT < 4 && u.chunks > 1) {                     // units of 64 rows are not cut
                 const uint64_t slot = (((uint64_t)place * G + g) * p.chunks + cut) * R + r * 16 + row;
 #pragma unroll
                 for (int n = 0; n < D / 64; ++n) *(f32x4*)(p.part + slot * D + seg + n * 64) = acc[n];
@@ -671,7 +680,7 @@ HeadsAttendPlan plan_heads_attend(const HeadsParams& h, uint32_t group, uint64_t
     const auto cuts = [&](uint64_t most, uint64_t wanted) { return std::min(std::min<uint64_t>(most, kMostChunks), wanted / blocks); };
     const uint64_t by_rows = std::max<uint64_t>(kChunk, std::min<uint64_t>(rows, a.rows) * kChunkRows);
     uint64_t n = 1;
-    if (max_kv > kWhole) {
+    if (max_kv > kWhole && a.rows < 64) {
         n = std::max(n, cuts((max_kv + by_rows - 1) / by_rows, a.rows == 16 ? kWanted : kWantedWide));
         n = std::max(n, cuts((max_kv + kLeastChunk - 1) / kLeastChunk, kFill));
         n = std::max(n, cuts(max_kv / (2 * kChunk), 2 * kFill));

@@ -28,7 +28,7 @@ def plan(G, H, D, n, max_kv, seqs=None, tokens=None, max_q=None):
     blocks = max(1, unit_places(R, group, seqs, tokens, max_q) * G)
     cuts = lambda most, wanted: min(most, k["kMostChunks"], wanted // blocks)
     each, cut = max(k["kChunk"], min(rows, R) * k["kChunkRows"]), 1
-    if max_kv > k["kWhole"]:
+    if max_kv > k["kWhole"] and R < 64:
         cut = max(cut, cuts(-(-max_kv // each), k["kWanted"] if R == 16 else k["kWantedWide"]))
         cut = max(cut, cuts(-(-max_kv // k["kLeastChunk"]), k["kFill"]))
         cut = max(cut, cuts(max_kv // (2 * k["kChunk"]), 2 * k["kFill"]))

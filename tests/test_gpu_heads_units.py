@@ -25,7 +25,7 @@ def cache_for(lens, G, D, **kw):
 SIZES = [
     ((64, 1), (8, 32, 128, [1100, 1083], [1100, 1500])),
     ((64, 1), (8, 24, 128, [700, 650, 1], [700, 900, 65])),
-    ((64, 2), (8, 32, 128, [256] * 4, [5000, 256, 4100, 2500])),
+    ((64, 1), (8, 32, 128, [256] * 4, [5000, 256, 4100, 2500])),
     ((64, 1), (16, 64, 64, [1200, 1100], [1200, 1163])),
     ((32, 1), (8, 32, 128, [256, 200], [300, 260])),
     ((32, 5), (8, 32, 128, [70, 3], [6000, 3100])),
@@ -64,7 +64,7 @@ def test_causal(ctx, want, size, kind):
 
 @pytest.mark.parametrize("kind", ["bf16", "fp16"])
 @pytest.mark.parametrize("want,G,H,D,n,lens", [
-    ((64, 1), 8, 32, 128, [64] * 15 + [61], [3000, 64, 100, 700] * 4), ((64, 2), 8, 32, 128, [256] * 4, [4900, 256, 300, 2500]),
+    ((64, 1), 8, 32, 128, [64] * 15 + [61], [3000, 64, 100, 700] * 4), ((64, 1), 8, 32, 128, [256] * 4, [4900, 256, 300, 2500]),
     ((64, 1), 16, 64, 64, [64] * 15 + [61], [1000, 64, 100, 700] * 4), ((32, 2), 8, 32, 128, [24] * 7 + [21], [2500, 24, 100, 700] * 2),
     ((32, 4), 4, 16, 256, [70, 33], [2500, 90])])
 def test_trees(ctx, want, G, H, D, n, lens, kind):
@@ -81,7 +81,7 @@ def test_trees(ctx, want, G, H, D, n, lens, kind):
 
 @pytest.mark.parametrize("kind", ["bf16", "fp16"])
 @pytest.mark.parametrize("want,G,H,D,n,lens", [
-    ((64, 1), 8, 32, 128, [600, 520], [600, 1000]), ((64, 2), 8, 32, 128, [256] * 4, [4500, 256, 300, 2500]),
+    ((64, 1), 8, 32, 128, [600, 520], [600, 1000]), ((64, 1), 8, 32, 128, [256] * 4, [4500, 256, 300, 2500]),
     ((64, 1), 16, 64, 64, [1200, 1100], [1200, 1163]), ((32, 1), 8, 32, 128, [130, 120], [200, 400]), ((32, 4), 4, 16, 256, [70, 33], [2500, 90])])
 def test_bad_pages_and_hidden_nan_codes(ctx, want, G, H, D, n, lens, kind):
     """A page that is not there in the middle and at the end of a sequence, and a position whose codes are NaN among the
@@ -120,3 +120,18 @@ def runs(mask):
     """[first, end) of the runs of true values."""
     edges = np.flatnonzero(np.diff(np.r_[0, mask.astype(np.int8), 0]))
     return list(zip(edges[::2].tolist(), edges[1::2].tolist()))
+
+
+def test_units_of_64_rows_stay_whole(ctx):
+    """512 blocks of them give the bits that the same tokens have in a call of more blocks."""
+    G, H, D, n, lens = 8, 32, 128, [256] * 4, [5000, 256, 4100, 2500]
+    cache = cache_for(lens + [64], G, D)
+    few = U.Seqs(lens, n, cache.pages, seed=1)
+    table = np.concatenate([few.table, np.full((1, few.table.shape[1]), cache.pages - 1, np.int32)])
+    more = U.Seqs(lens + [64], n + [64], cache.pages, table=table)
+    assert plan(G, H, D, few.n, few.max_kv) == (64, 1, 512) and plan(G, H, D, more.n, more.max_kv)[0] == 64
+    a, b = U.Query(few.T, H, D), U.Query(more.T, H, D)
+    b.q[:few.T] = a.q
+    U.attend(ctx, cache, a, few)
+    U.attend(ctx, cache, b, more)
+    assert torch.equal(a.out, b.out[:few.T]) and torch.equal(a.lse, b.lse[:few.T])
