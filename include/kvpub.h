@@ -641,8 +641,9 @@ KVPUB_API uint64_t kvpub_heads_attend_workspace(const kvpub_heads *cache, const 
  * the same call gives the same bits.  Scores, maxima and sums are binary32;
  * weights are rounded to bf16 for the second product (FP16, and calls of at most 16
  * (token, query head) rows a sequence and key-value head: to the sum of two bf16), out once
- * to its type.  A query or a seen row that is not finite, or a score whose
- * magnitude passes 2^30, leaves the rows it reaches unspecified, NaN as a rule.
+ * to its type.  A query or a seen row that is not finite, a score whose
+ * magnitude passes 2^30, or a value whose magnitude passes 2^88 (the sums are of weights up to 2^8 before they are
+ * divided) leaves the rows it reaches unspecified, NaN as a rule.
  * T == 0 or num_seqs == 0 launches nothing. */
 KVPUB_API kvpub_status kvpub_heads_attend(kvpub_ctx *ctx, const kvpub_heads *cache, uint32_t replica, uint32_t layer,
                                           const kvpub_heads_queries *q, const kvpub_pages *pages, void *workspace,

@@ -4,7 +4,7 @@
 // Mathematics.  With codes c and d of a block's keys and values and its scales a, b,
 //   score = (scale * a) (q . c),   out = sum_p w_p (b d_p) / sum_p w_p.
 // A code is exact in bf16 and fp16, and so is a value's code times its scale in
-// bf16: nothing of the cache is rounded again.  Weights are rounded to bf16 for the
+// bf16 (but for multiples of 2^-135 below 2^-126, which the two least scales have): nothing of the cache is rounded again.  Weights are rounded to bf16 for the
 // second product: that leaves bf16 outputs off by 0.0021 of their norm where their own
 // rounding alone leaves 0.0017, and a second operand for the low parts costs 38 % in long
 // prompts.  Units of 16 rows, which memory bounds, take that operand (2 % of a large
