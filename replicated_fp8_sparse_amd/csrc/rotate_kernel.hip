@@ -51,6 +51,12 @@ __global__ __launch_bounds__(kThreads) void rotate_kernel(const RotateParams p) 
 #pragma unroll
                 for (int i = 0; i < 4; ++i) w[i] = (float)a[h].v[i], w[4 + i] = (float)b[h].v[i];
                 angles.turn(w, Halves);
+                // a sum is rounded to binary32 before its type: joined with the conversion in some places and not in others,
+                // one value would have different bits in different heads
+                if constexpr (__is_same(T, _Float16)) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) asm("" : "+v"(w[i]));
+                }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) a[h].v[i] = (T)w[i], b[h].v[i] = (T)w[4 + i];
             }
