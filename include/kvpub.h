@@ -534,8 +534,10 @@ KVPUB_API kvpub_status kvpub_rotate(kvpub_ctx *ctx, const kvpub_rotate_io *io, k
  * rotation leaves that row as it is; both NULL is kvpub_store, and `positions`
  * is not read).  The RoPE values are rounded to bf16 once; the Indexer-K values are
  * not rounded before their scale and codes: scale = RN32(amax / 448), code =
- * e4m3fn(RN32(x / scale)) of the rotated binary32 values.  Everything else,
- * arguments and slots included, is as for kvpub_store. */
+ * e4m3fn(RN32(x / scale)) of the rotated binary32 values.  If the context is
+ * poisoned while the call runs, each token's two rows are stored whole, in every
+ * replica, or left as they were.  Everything else, arguments and slots included, is
+ * as for kvpub_store. */
 KVPUB_API kvpub_status kvpub_store_rotated(kvpub_ctx *ctx, uint32_t layer, int64_t num_tokens,
                                            const void *latent, int64_t latent_row_stride,
                                            const void *rope, int64_t rope_row_stride,
@@ -559,7 +561,10 @@ KVPUB_API kvpub_status kvpub_store_rotated(kvpub_ctx *ctx, uint32_t layer, int64
  * (but for those that become subnormal).
  *
  * The context gives the device, the fail-closed state of its fences and the
- * counter of bad pages; the descriptor names the memory, which is the caller's. */
+ * counter of bad pages; the descriptor names the memory, which is the caller's.
+ * A program without a latent cache makes its context over one page of that, which
+ * the calls below do not touch: kvpub_config_init(&cfg, 1, 1, 1) and device
+ * allocations of KVPUB_MAIN_PAGE_BYTES and KVPUB_IDX_PAGE_BYTES as its two bases. */
 #define KVPUB_HEADS_PAGE_BYTES(num_kv_heads, head_dim) \
     (((uint64_t)(num_kv_heads) * (128u * (uint64_t)(head_dim) + 2u) + 15u) / 16u * 16u)
 
@@ -602,8 +607,10 @@ typedef struct {
  * is not read; tokens beyond the first max_q_len of a sequence, negative
  * positions, and tokens that belong to no sequence are not stored.  A page
  * number outside the cache's pages drops its rows, and is counted once a call.
- * A context poisoned by a fence timeout stores nothing.  Asynchronous on
- * `stream`; no allocation, no synchronization, safe under stream capture. */
+ * A context poisoned by a fence timeout stores nothing; if it is poisoned while
+ * the call runs, each block of 64 positions and head is stored whole, in every
+ * replica, or left as it was.  Asynchronous on `stream`; no allocation, no
+ * synchronization, safe under stream capture. */
 KVPUB_API kvpub_status kvpub_heads_append(kvpub_ctx *ctx, const kvpub_heads *cache, uint32_t layer,
                                           const kvpub_heads_rows *rows, const kvpub_pages *pages,
                                           const kvpub_rotation *rotation, const int32_t *positions,

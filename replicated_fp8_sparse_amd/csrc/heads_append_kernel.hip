@@ -15,8 +15,8 @@
 //
 // Bound.  Few tokens: a launch and a chain of four reads (lengths, page, context, older scales): 64 sequences x
 // one token, 8 heads of 128, 2 replicas 5.2 us, 256 x 1 6.7.  One round of blocks (4 x up to 2048
-// tokens, 25 MB): that chain, then its bytes, 11.9 us.  Long: the angles, once for each head: 8 x up to
-// 4096 tokens into 1 replica 35 us, where the bytes alone would leave 22.
+// tokens, 25 MB): that chain, then its bytes, 11.3-11.9 us.  Long: the angles, once for each head: 8 x up to
+// 4096 tokens into 1 replica 33-34 us, where the bytes alone would leave 19.
 #include "kvpub.h"
 #include "rotation.h"
 #include "sequences.h"

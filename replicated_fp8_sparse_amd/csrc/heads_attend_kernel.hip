@@ -16,8 +16,8 @@
 // down, rows across, so that a lane holds 8 positions of one row, and its weights
 // are an operand of the second product as they are if the values' positions come in the
 // same order.  Values are read by position, 16 lanes a row, and brought to columns by
-// byte permutes within a lane: no LDS before the end (but for the queries of 64
-// rows).  The 4 waves of a block take every 4th tile of 32 positions, each from
+// byte permutes within a lane: no LDS before the end (but for the queries of 32 rows of 128
+// values and more, and of 64 rows).  The 4 waves of a block take every 4th tile of 32 positions, each from
 // memory straight to registers: keys as soon as the last tile's scores are computed, values as
 // soon as its products are, so both are on their way behind the other half of the work.
 // Page numbers, lengths and scales come through the scalar cache, whose waits leave those
@@ -29,8 +29,9 @@
 // instructions (80 of them the widening, 128 the weights) and 64 matrix instructions, which exclude each
 // other more than they overlap: beside a wave that issues 16 x 16 x 32 products
 // back to back the other waves of its SIMD issue nothing for 14 of 16 cycles (32 x 32 x 16:
-// 21 of 32), so 2100 cycles of work a tile, of which two waves a SIMD reach some 2250.  Prompts of
-// 2 x 4096 tokens behind as much context, 16 heads over 4: 223-255 us, 72-82 % of a large bf16 product's rate.
+// 21 of 32), so 2100 cycles of work a tile, of which two waves a SIMD reach some 2270: by the counters matrix instructions
+// take 45 % of the SIMDs' cycles and the other vector instructions 47 %.  Prompts of 2 x 4096 tokens behind as
+// much context, 16 heads over 4: 230-256 us from card to card, 72-80 % of a large bf16 product's rate.
 // (Built and measured when it took 254-260: 32 x 32 x 16 products throughout, 247; the same with the next
 // tile's scores between this one's weights, one wave a SIMD, 300; 32 rows a unit, 300-315.)  Short
 // prompts: a block's start (lengths, pages, queries, the first tile: 5 us) and the join of 64 rows (3).

@@ -9,7 +9,7 @@
 //
 // Bound.  Memory: 8192 tokens of 128 heads, 64 of 192 values rotated, bf16 55.7 us, 3000 of 32
 // heads of 128, 48 rotated, binary32 20.0: a large copy's 5.16 TB/s would leave 52 and 19.  One token: a
-// launch and two dependent reads, 2.8 us.
+// launch and two dependent reads, 2.9 us.
 #include <algorithm>
 
 #include "kvpub.h"

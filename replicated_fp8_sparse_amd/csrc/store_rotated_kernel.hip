@@ -17,8 +17,9 @@
 // once for all pieces of a token, so its two rows are stored whole or left as they were.
 //
 // Bound.  Few tokens: a launch, three dependent reads and one wave's tile, 4.0-4.3 us up to
-// 256.  Many: the quantization between the reads and the writes: 8192 tokens into 4 replicas,
-// 37 MB, 11.1 us (a large copy's rate would leave 7.3), 32768 32 us (29).
+// 256.  Many: what lies between the reads and the writes: 8192 tokens into 4 replicas,
+// 37 MB, 10.9-11.3 us (a large copy's rate would leave 7.3; kvpub_store, same rows, 7.8), 32768 30 us (29).  The
+// divisions are 0.4 of that: 0.1 the Indexer-K tile's, 0.3 the latent tiles' scales and reciprocals.
 #include "rotation.h"
 
 namespace kvpub {
